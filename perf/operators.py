@@ -488,7 +488,7 @@ def exact(case, seed):
             flat = cache[:case["pool"]].double().reshape(-1, case["kv_heads"], case["dim"])
             flat[at] = rows.double()[keep]
             both.append(flat.view(case["pool"], case["block"], case["kv_heads"], case["dim"]))
-        return both
+        return tuple(both)
     if op == "write_keys":
         if case["layout"] == "plain":
             return None
