@@ -306,6 +306,217 @@ QSA_API qsa_status qsa_topk_check(const float *logits, int64_t logits_stride, co
 QSA_API qsa_status qsa_expand(const int32_t *idx, int32_t num_rows, int32_t k, int32_t ratio,
                               const int32_t *token_lens, int32_t *tokens_out, void *stream);
 
+/*
+ * The calls below stand around the scorer and the selection in a serving step:
+ *
+ *   qsa_plan_batch        request lengths -> block table, slot maps, visible counts
+ *   qsa_write_kv          new keys and values into the paged caches
+ *   qsa_write_keys        new index keys into the scorer's cache
+ *   qsa_paged_attention   attention over all visible tokens
+ *   qsa_sparse_attention  attention over the tokens of the selected columns
+ */
+
+typedef struct qsa_plan_shape {
+    int32_t num_reqs;     /* n requests                                            */
+    int32_t max_blocks;   /* columns of block_table                                */
+    int32_t block_size;   /* B tokens per block                                    */
+    int32_t ratio;        /* tokens per compressed index column; divides B         */
+    int32_t num_rows;     /* R: entries of the per-row outputs                     */
+    int32_t num_free;     /* entries of free_blocks                                */
+    int64_t num_blocks;   /* blocks in the pool                                    */
+} qsa_plan_shape;
+
+/*
+ * qsa_plan_batch -- the metadata of one step, from request lengths.
+ *
+ * Request i holds past_lens[i] cached tokens (clamped to [0, max_blocks * B]) and
+ * brings new_lens[i] new ones (negative: none).  Its rows are
+ * [q_starts[i], q_starts[i + 1]), the row of its j-th new token stands for token
+ * t = past + j.  Rows behind num_rows do not exist: the requests that would hold
+ * them bring fewer tokens, down to none.
+ *
+ *   past_lens, new_lens [n] int32.
+ *   free_blocks  [num_free] int32 pool blocks to take from, in order.
+ *   block_table  [n][max_blocks] int32, updated: entries
+ *                [ceil(past / B), ceil((past + new) / B)) of request i (up to
+ *                max_blocks) take the next free blocks, request by request; -1
+ *                once the list is used up.  Other entries are left alone.
+ *   q_starts     [n + 1] int32.
+ *   row_to_req   [R] int32.
+ *   ctx_lens     [R] int32 visible tokens, t + 1 (at most max_blocks * B).
+ *   slots        [R] int64 block_table[i][t / B] * B + t % B, or -1 where the
+ *                table has no place for the token (t past its end, or an entry
+ *                outside [0, num_blocks)).
+ *   col_lens     [R] int32 whole compressed columns visible, ctx_lens / ratio, or
+ *                NULL: qsa_paged_logits' ctx_lens over a cache with the same
+ *                block table and B / ratio columns per block.
+ *   col_slots    [R] int64 slot of the column that the row's token completes
+ *                ((t + 1) % ratio == 0), block * (B / ratio) + (t % B) / ratio,
+ *                else -1; or NULL.
+ *   blocks_used  [1] int32 blocks asked of the free list (more than num_free:
+ *                that many were missing), or NULL.
+ *
+ * Rows behind the last request's get request 0, no visible token and no slots,
+ * so a batch padded for a captured graph passes through the other calls.  The
+ * call does not change its own inputs but for block_table's new entries: called
+ * again it gives the same answer.
+ *
+ * Device precondition: free_blocks are distinct blocks of the pool that no entry
+ * holds.  Compiled set: n <= 4096.  Range: max_blocks * B <= 2^30, R <= 2^30.
+ */
+QSA_API qsa_status qsa_plan_batch(const int32_t *past_lens, const int32_t *new_lens, const int32_t *free_blocks,
+                                  int32_t *block_table, int32_t *q_starts, int32_t *row_to_req, int32_t *ctx_lens,
+                                  int64_t *slots, int32_t *col_lens, int64_t *col_slots, int32_t *blocks_used,
+                                  const qsa_plan_shape *shape, void *stream);
+
+/* Validation of qsa_plan_batch's host-visible arguments only: no HIP call. */
+QSA_API qsa_status qsa_plan_batch_check(const int32_t *past_lens, const int32_t *new_lens,
+                                        const int32_t *free_blocks, const int32_t *block_table,
+                                        const int32_t *q_starts, const int32_t *row_to_req, const int32_t *ctx_lens,
+                                        const int64_t *slots, const qsa_plan_shape *shape);
+
+typedef struct qsa_kv_shape {
+    int32_t num_rows;          /* R rows to write                                  */
+    int32_t num_kv_heads;
+    int32_t head_dim;          /* 64 or 128                                        */
+    int32_t block_size;        /* B tokens per block                               */
+    int32_t dtype;             /* QSA_BF16 or QSA_FP16, sources and caches         */
+    int32_t reserved;
+    int64_t num_blocks;
+    /* strides in elements (the last dimension is contiguous): of k and v, and
+     * of kcache and vcache                                                      */
+    int64_t src_row_stride, src_head_stride;
+    int64_t kv_block_stride, kv_slot_stride, kv_head_stride;
+} qsa_kv_shape;
+
+/*
+ * qsa_write_kv -- k and v [R][num_kv_heads][head_dim] into the paged caches, row r
+ * at slot slots[r] (block slots[r] / B, place slots[r] % B).  Rows whose slot is
+ * outside [0, num_blocks * B) write nothing.
+ *
+ * Device precondition: the slots written are distinct (two rows for one slot
+ * leave a mixture of both).  Alignment: pointers 16 bytes, strides multiples of 8
+ * elements.  kcache and vcache have the same strides.
+ */
+QSA_API qsa_status qsa_write_kv(const void *k, const void *v, const int64_t *slots, void *kcache, void *vcache,
+                                const qsa_kv_shape *shape, void *stream);
+QSA_API qsa_status qsa_write_kv_check(const void *k, const void *v, const int64_t *slots, const void *kcache,
+                                      const void *vcache, const qsa_kv_shape *shape);
+
+typedef struct qsa_keys_shape {
+    int32_t num_rows;          /* R keys to write                                  */
+    int32_t head_dim;          /* D: 64 or 128                                     */
+    int32_t block_size;        /* B key columns per block                          */
+    int32_t src_dtype;         /* QSA_BF16 or QSA_FP16                             */
+    int32_t k_dtype;           /* src_dtype, or QSA_FP8_E4M3FN                     */
+    int32_t kv_layout;         /* qsa_kv_layout                                    */
+    int64_t num_blocks;
+    int64_t src_stride;        /* elements between keys, >= D                      */
+} qsa_keys_shape;
+
+/*
+ * qsa_write_keys -- index keys [R][D] into qsa_paged_logits' key cache, key r at
+ * slot slots[r] (rows whose slot is outside [0, num_blocks * B) write nothing).
+ * 16-bit keys are copied.  For an fp8 cache each key x is stored as codes
+ * rne(x / s) with s = max|x| / 448, or 1 for a key of zeros, in the layout's
+ * place for its scale; a paged fp8 cache without kscale holds rne(x), saturated
+ * to +-448.  A key with an infinity or a NaN spoils its own slot only.
+ *
+ * Device precondition: the slots written are distinct.  Alignment: keys and kcache
+ * 16 bytes, src_stride a multiple of 8 elements.
+ */
+QSA_API qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, float *kscale,
+                                  const qsa_keys_shape *shape, void *stream);
+QSA_API qsa_status qsa_write_keys_check(const void *keys, const int64_t *slots, const void *kcache,
+                                        const float *kscale, const qsa_keys_shape *shape);
+
+typedef struct qsa_attn_shape {
+    int32_t num_rows;          /* R query rows of q and out                        */
+    int32_t num_heads;         /* Hq query heads                                   */
+    int32_t num_kv_heads;      /* Hk; query head h reads kv head h / (Hq / Hk)     */
+    int32_t head_dim;          /* D: 64 or 128                                     */
+    int32_t block_size;        /* B tokens per block                               */
+    int32_t num_reqs;          /* rows of block_table                              */
+    int32_t max_blocks;        /* columns of block_table                           */
+    int32_t dtype;             /* QSA_BF16 or QSA_FP16: q, caches and out          */
+    float scale;               /* of the scores, positive                          */
+    int32_t reserved;
+    int64_t num_blocks;
+    /* strides in elements (the last dimension is contiguous)                    */
+    int64_t q_row_stride, q_head_stride;
+    int64_t out_row_stride, out_head_stride;
+    int64_t kv_block_stride, kv_slot_stride, kv_head_stride;
+} qsa_attn_shape;
+
+/*
+ * qsa_paged_attention -- attention of new tokens over the paged cache:
+ *
+ *     out[r, h, :] = sum_c p_c v[c],  p = softmax_c(scale * q[r, h, :] . k[c])
+ *     lse[r, h]    = log sum_c exp(scale * q[r, h, :] . k[c])
+ *
+ * over the columns c < ctx_lens[r] of the row's request (clamped to
+ * [0, max_blocks * B]); a chunk of new tokens is causal when ctx_lens are
+ * qsa_plan_batch's.  Token c lies in pool block block_table[i][c / B] at place
+ * c % B.  A row that sees nothing has out 0 and lse -inf.
+ *
+ *   q         [R][Hq][D], rows of one request together.
+ *   ctx_lens  [R] int32; any counts, not only causal ones.
+ *   q_starts  [num_reqs + 1] int32, non-decreasing: request i's rows are
+ *             [q_starts[i], q_starts[i + 1]) (values are clamped to [0, R]).
+ *             Rows outside all requests are left as they were in out and lse.
+ *   lse       [R][Hq] f32 contiguous, or NULL.
+ *   workspace qsa_paged_attention_workspace_bytes(shape) bytes, 16-byte aligned,
+ *             or NULL: then few rows over long contexts are not spread over the
+ *             chip.  No initialisation; calls that share it must be ordered.
+ *
+ * Keys and values of columns that no row of the request sees are not used, and
+ * what only other rows see does not change a row, infinities and NaN included.
+ * A table entry outside [0, num_blocks) is not dereferenced: rows that see its
+ * columns are NaN.  Weights are rounded to dtype before the second product;
+ * sums, maxima and lse are 32-bit.
+ *
+ * Compiled set: Hq / Hk <= 128, Hq <= 8192, B <= 1024.  Range: max_blocks * B <=
+ * 2^30, R and num_reqs <= 2^22.  Alignment: pointers 16 bytes, strides multiples
+ * of 8 elements.
+ */
+QSA_API qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vcache,
+                                       const int32_t *block_table, const int32_t *ctx_lens,
+                                       const int32_t *q_starts, void *out, float *lse, const qsa_attn_shape *shape,
+                                       void *workspace, int64_t workspace_bytes, void *stream);
+QSA_API qsa_status qsa_paged_attention_check(const void *q, const void *kcache, const void *vcache,
+                                             const int32_t *block_table, const int32_t *ctx_lens,
+                                             const int32_t *q_starts, const void *out, const qsa_attn_shape *shape,
+                                             const void *workspace, int64_t workspace_bytes);
+QSA_API int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *shape);
+
+/*
+ * qsa_sparse_attention -- the same over selected tokens: row r attends to tokens
+ * idx[r][p] * ratio + j, j < ratio, for its non-negative idx (qsa_topk's output,
+ * or with ratio 1 qsa_expand's); tokens at or behind token_lens[r] are left out.
+ * The order of a row's indices does not matter; an index given twice counts
+ * twice.  A row without tokens has out 0 and lse -inf.
+ *
+ *   row_to_req [R] int32; a value outside [0, num_reqs) makes the row's outputs
+ *              NaN (if it selects anything).
+ *   idx        [R][k] int32, negative entries are padding, anywhere.
+ *   token_lens [R] int32 or NULL (the table's max_blocks * B).
+ *   workspace  as above, qsa_sparse_attention_workspace_bytes(shape, k, ratio).
+ *
+ * The other arguments, errors and limits are qsa_paged_attention's; k * ratio <=
+ * 2^24.
+ */
+QSA_API qsa_status qsa_sparse_attention(const void *q, const void *kcache, const void *vcache,
+                                        const int32_t *block_table, const int32_t *row_to_req, const int32_t *idx,
+                                        int32_t k, int32_t ratio, const int32_t *token_lens, void *out, float *lse,
+                                        const qsa_attn_shape *shape, void *workspace, int64_t workspace_bytes,
+                                        void *stream);
+QSA_API qsa_status qsa_sparse_attention_check(const void *q, const void *kcache, const void *vcache,
+                                              const int32_t *block_table, const int32_t *row_to_req,
+                                              const int32_t *idx, int32_t k, int32_t ratio, const void *out,
+                                              const qsa_attn_shape *shape, const void *workspace,
+                                              int64_t workspace_bytes);
+QSA_API int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *shape, int32_t k, int32_t ratio);
+
 /* Message for the calling thread's last non-OK status ("" if none). Owned by the
  * library; valid until the thread's next call. */
 QSA_API const char *qsa_last_error(void);

@@ -1,5 +1,6 @@
 """Python binding of libqsaidx: paged MQA-logits scoring and per-row top-k on
-MI355X (gfx950).
+MI355X (gfx950), and the calls around them in a serving step (batch plan, cache
+writes, attention; in ``serving.py``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI declared in ``include/qsaidx.h``.  Tensors are torch
@@ -27,7 +28,10 @@ KV_PAGED, KV_COPACKED, KV_COPACKED_SHUFFLED = 0, 1, 2
 EXPORTED = ("qsa_paged_logits", "qsa_paged_logits_timed", "qsa_paged_logits_check", "qsa_topk",
             "qsa_topk_timed", "qsa_topk_check", "qsa_topk_workspace_bytes", "qsa_topk_noalloc",
             "qsa_paged_logits_topk", "qsa_paged_logits_topk_timed", "qsa_paged_logits_topk_workspace_bytes",
-            "qsa_expand", "qsa_last_error", "qsa_version")
+            "qsa_expand", "qsa_plan_batch", "qsa_plan_batch_check", "qsa_write_kv", "qsa_write_kv_check",
+            "qsa_write_keys", "qsa_write_keys_check", "qsa_paged_attention", "qsa_paged_attention_check",
+            "qsa_paged_attention_workspace_bytes", "qsa_sparse_attention", "qsa_sparse_attention_check",
+            "qsa_sparse_attention_workspace_bytes", "qsa_last_error", "qsa_version")
 
 
 class QsaError(RuntimeError):
@@ -442,3 +446,9 @@ def paged_logits_topk(q, kcache, block_table, ctx_lens, row_to_req, *, k: int, w
     if call.workspace is not None:
         call.workspace.record_stream(_torch_stream(stream))
     return call()
+
+
+from .serving import (AttnShape, BatchPlan, KeysShape, KvShape, PlanShape, PreparedPagedAttention,  # noqa: E402
+                      PreparedPlanBatch, PreparedSparseAttention, PreparedWriteKeys, PreparedWriteKv,
+                      make_attn_shape, paged_attention, paged_attention_workspace_bytes, plan_batch,
+                      sparse_attention, sparse_attention_workspace_bytes, write_keys, write_kv)

@@ -5,12 +5,15 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include "api_common.h"
 #include "qsa_internal.h"
 #include "qsaidx.h"
 
 namespace {
-
 thread_local char g_err[512] = "";
+}
+
+namespace qsa {
 
 qsa_status fail(qsa_status st, const char *fmt, ...) {
     va_list ap;
@@ -25,9 +28,14 @@ qsa_status ok() {
     return QSA_OK;
 }
 
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace qsa
 
-constexpr int64_t kMaxBytes = (int64_t)1 << 62;
+namespace {
+
+using qsa::aligned16;
+using qsa::fail;
+using qsa::kMaxBytes;
+using qsa::ok;
 
 qsa_status check_logits(const void *q, const float *w, const void *kcache, const float *kscale,
                         const int32_t *block_table, const int32_t *ctx_lens,

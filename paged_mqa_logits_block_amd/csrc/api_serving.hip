@@ -1,0 +1,395 @@
+// C-ABI entry points around the scorer: the batch plan, the cache writes, and
+// attention over the paged cache (all visible tokens, or the selected ones).
+// As in api.hip, validation reads host scalars only and every call can be
+// captured.
+#include <math.h>
+
+#include "api_common.h"
+#include "attn_internal.h"
+#include "qsa_internal.h"
+#include "qsaidx.h"
+
+namespace {
+
+using qsa::aligned16;
+using qsa::fail;
+using qsa::ok;
+
+qsa_status launched(hipError_t e) {
+    return e == hipSuccess ? ok() : fail(QSA_E_HIP, "launch failed: %s", hipGetErrorString(e));
+}
+
+qsa_status check_plan(const int32_t *past_lens, const int32_t *new_lens, const int32_t *free_blocks,
+                      const int32_t *block_table, const int32_t *q_starts, const int32_t *row_to_req,
+                      const int32_t *ctx_lens, const int64_t *slots, const qsa_plan_shape *s) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0 || s->num_free < 0)
+        return fail(QSA_E_INVALID, "num_rows = %d and num_free = %d must be >= 0", s->num_rows, s->num_free);
+    if (s->num_reqs < 1 || s->max_blocks < 1 || s->block_size < 1 || s->num_blocks < 1 || s->ratio < 1)
+        return fail(QSA_E_INVALID, "num_reqs, max_blocks, block_size, num_blocks and ratio must be >= 1");
+    if (s->block_size % s->ratio != 0)
+        return fail(QSA_E_INVALID, "ratio = %d does not divide block_size = %d", s->ratio, s->block_size);
+    if (!past_lens || !new_lens || !block_table || !q_starts || (s->num_free > 0 && !free_blocks) ||
+        (s->num_rows > 0 && (!row_to_req || !ctx_lens || !slots)))
+        return fail(QSA_E_INVALID, "past_lens, new_lens, free_blocks, block_table, q_starts, row_to_req, ctx_lens "
+                                   "and slots must be non-NULL");
+    if (s->num_reqs > qsa::kPlanMaxReqs)
+        return fail(QSA_E_UNSUPPORTED, "num_reqs = %d (built: up to %d)", s->num_reqs, qsa::kPlanMaxReqs);
+    if ((int64_t)s->max_blocks * s->block_size > (1 << 30))
+        return fail(QSA_E_RANGE, "max_blocks * block_size = %lld > 2^30", (long long)s->max_blocks * s->block_size);
+    if (s->num_rows > (1 << 30)) return fail(QSA_E_RANGE, "num_rows = %d > 2^30", s->num_rows);
+    if (s->num_blocks > ((int64_t)1 << 50)) return fail(QSA_E_RANGE, "num_blocks too large");
+    return ok();
+}
+
+qsa_status check_write_kv(const void *k, const void *v, const int64_t *slots, const void *kcache, const void *vcache,
+                          const qsa_kv_shape *s) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0) return fail(QSA_E_INVALID, "num_rows = %d < 0", s->num_rows);
+    if (s->num_kv_heads < 1 || s->head_dim < 1 || s->block_size < 1 || s->num_blocks < 1)
+        return fail(QSA_E_INVALID, "num_kv_heads, head_dim, block_size and num_blocks must be >= 1");
+    if (s->src_row_stride < 0 || s->src_head_stride < 0 || s->kv_block_stride < 0 || s->kv_slot_stride < 0 ||
+        s->kv_head_stride < 0)
+        return fail(QSA_E_INVALID, "strides must be >= 0");
+    if (s->num_rows > 0 && (!k || !v || !slots || !kcache || !vcache))
+        return fail(QSA_E_INVALID, "k, v, slots, kcache and vcache must be non-NULL");
+    if (s->dtype != QSA_BF16 && s->dtype != QSA_FP16) return fail(QSA_E_DTYPE, "dtype = %d (built: bf16, fp16)", s->dtype);
+    if (s->head_dim != 64 && s->head_dim != 128)
+        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
+    if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
+    if (s->num_kv_heads > 1024) return fail(QSA_E_UNSUPPORTED, "num_kv_heads = %d (built: 1 to 1024)", s->num_kv_heads);
+    if (s->kv_head_stride < (s->num_kv_heads > 1 ? s->head_dim : 0) ||
+        s->kv_slot_stride < (s->block_size > 1 ? s->head_dim : 0) ||
+        s->kv_block_stride < (s->num_blocks > 1 ? s->head_dim : 0))
+        return fail(QSA_E_INVALID, "cache strides must be at least head_dim");
+    if (s->num_blocks > ((int64_t)1 << 50) || s->kv_block_stride > ((int64_t)1 << 50) / s->num_blocks ||
+        s->kv_slot_stride > ((int64_t)1 << 40) || s->kv_head_stride > ((int64_t)1 << 40) ||
+        s->src_row_stride > ((int64_t)1 << 30) || s->src_head_stride > ((int64_t)1 << 30))
+        return fail(QSA_E_RANGE, "cache or source too large");
+    if (s->num_rows > 0 && (!aligned16(k) || !aligned16(v) || !aligned16(kcache) || !aligned16(vcache)))
+        return fail(QSA_E_ALIGN, "k, v, kcache and vcache must be 16-byte aligned");
+    if (s->num_rows > 0 && ((s->src_row_stride | s->src_head_stride | s->kv_block_stride | s->kv_slot_stride |
+                             s->kv_head_stride) & 7) != 0)
+        return fail(QSA_E_ALIGN, "strides must be multiples of 8 elements");
+    return ok();
+}
+
+qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *kcache, const float *kscale,
+                            const qsa_keys_shape *s) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0) return fail(QSA_E_INVALID, "num_rows = %d < 0", s->num_rows);
+    if (s->head_dim < 1 || s->block_size < 1 || s->num_blocks < 1)
+        return fail(QSA_E_INVALID, "head_dim, block_size and num_blocks must be >= 1");
+    if (s->src_stride < s->head_dim && s->num_rows > 1)
+        return fail(QSA_E_INVALID, "src_stride = %lld < head_dim = %d", (long long)s->src_stride, s->head_dim);
+    if (s->num_rows > 0 && (!keys || !slots || !kcache))
+        return fail(QSA_E_INVALID, "keys, slots and kcache must be non-NULL");
+    if (s->src_dtype != QSA_BF16 && s->src_dtype != QSA_FP16)
+        return fail(QSA_E_DTYPE, "src_dtype = %d (built: bf16, fp16)", s->src_dtype);
+    if (s->k_dtype != QSA_FP8_E4M3FN && s->k_dtype != s->src_dtype)
+        return fail(QSA_E_DTYPE, "k_dtype = %d: e4m3 or the source's type", s->k_dtype);
+    if (s->kv_layout < QSA_KV_PAGED || s->kv_layout > QSA_KV_COPACKED_SHUFFLED)
+        return fail(QSA_E_INVALID, "kv_layout = %d", s->kv_layout);
+    const bool fp8 = s->k_dtype == QSA_FP8_E4M3FN, copacked = s->kv_layout != QSA_KV_PAGED;
+    if (copacked && !fp8) return fail(QSA_E_UNSUPPORTED, "co-packed layouts hold fp8 keys only");
+    if (kscale && (!fp8 || copacked))
+        return fail(QSA_E_INVALID, "kscale applies to fp8 keys in the paged layout only");
+    if (s->head_dim != 64 && s->head_dim != 128)
+        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
+    if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
+    if (s->kv_layout == QSA_KV_COPACKED_SHUFFLED && s->block_size % 16 != 0)
+        return fail(QSA_E_UNSUPPORTED, "the preshuffled layout needs block_size %% 16 == 0");
+    if (s->num_blocks > ((int64_t)1 << 40) || s->src_stride > ((int64_t)1 << 30))
+        return fail(QSA_E_RANGE, "cache or source too large");
+    if (s->num_rows > 0 && (!aligned16(keys) || !aligned16(kcache)))
+        return fail(QSA_E_ALIGN, "keys and kcache must be 16-byte aligned");
+    if (s->num_rows > 1 && s->src_stride % 8 != 0)
+        return fail(QSA_E_ALIGN, "src_stride must be a multiple of 8 elements");
+    return ok();
+}
+
+// The requests that the streaming kernel takes: up to this many stacked pairs
+// per kv head.
+constexpr int kStreamPairs = 64;
+// Workgroups that a split launch aims at, and the most splits
+constexpr int kSplitGroups = 1024, kMaxSplits = 64;
+
+struct AttnPlan {
+    int sub_heads, num_subs, stream_rows;  // heads per workgroup, workgroups per kv head, rows per streaming tile
+    int few_rows;                          // requests of up to this many rows are streamed
+    int slots, slots_per_req, splits;
+    bool stream, tile;
+    int64_t bytes;
+};
+
+AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
+    AttnPlan p = {};
+    const int group = s->num_heads / s->num_kv_heads;
+    p.num_subs = (group + qsa::kAttnTile - 1) / qsa::kAttnTile;
+    p.sub_heads = (group + p.num_subs - 1) / p.num_subs;
+    p.num_subs = (group + p.sub_heads - 1) / p.sub_heads;
+    p.stream_rows = sparse ? 1 : qsa::kAttnTile / p.sub_heads;
+    p.few_rows = group >= kStreamPairs ? 1 : kStreamPairs / group;
+    int64_t tiles;
+    if (sparse) {
+        p.stream = true;
+        p.slots = s->num_rows;
+        tiles = s->num_rows;
+    } else {
+        // with one request its rows are the call's rows, but for padding behind them
+        p.stream = s->num_reqs > 1 || s->num_rows <= p.few_rows;
+        p.tile = s->num_rows > p.few_rows;
+        const int T = p.stream_rows;
+        const int rows = p.few_rows < s->num_rows ? p.few_rows : s->num_rows;
+        const int64_t all = (int64_t)s->num_rows / T + s->num_reqs, per = (rows + T - 1) / T;
+        p.slots_per_req = per * s->num_reqs <= all ? (int)per : 0;
+        p.slots = (int)(p.slots_per_req ? per * s->num_reqs : all);
+        tiles = (s->num_rows + T - 1) / T;
+        const int64_t least = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
+        if (tiles < least) tiles = least;
+        if (tiles > p.slots) tiles = p.slots;
+    }
+    const int64_t groups = tiles * s->num_kv_heads * p.num_subs;
+    int64_t splits = groups > 0 ? (kSplitGroups + groups - 1) / groups : 1;
+    const int64_t most = keys / (qsa::kStreamKeys * qsa::kStreamWaves);
+    if (splits > most) splits = most;
+    if (splits > kMaxSplits) splits = kMaxSplits;
+    p.splits = splits < 1 || !p.stream ? 1 : (int)splits;
+    p.bytes = p.splits > 1 ? (int64_t)p.slots * s->num_kv_heads * p.num_subs * p.splits * qsa::kAttnTile *
+                                 (s->head_dim + 2) * 4
+                           : 0;
+    return p;
+}
+
+qsa_status check_attn(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
+                      const int32_t *per_row, const int32_t *starts_or_idx, const void *out,
+                      const qsa_attn_shape *s, bool sparse, int32_t k, int32_t ratio) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0) return fail(QSA_E_INVALID, "num_rows = %d < 0", s->num_rows);
+    if (s->num_heads < 1 || s->num_kv_heads < 1 || s->head_dim < 1 || s->block_size < 1 || s->num_reqs < 1 ||
+        s->max_blocks < 1 || s->num_blocks < 1)
+        return fail(QSA_E_INVALID, "num_heads, num_kv_heads, head_dim, block_size, num_reqs, max_blocks and "
+                                   "num_blocks must be >= 1");
+    if (s->num_heads % s->num_kv_heads != 0)
+        return fail(QSA_E_INVALID, "num_heads = %d is not a multiple of num_kv_heads = %d", s->num_heads, s->num_kv_heads);
+    if (!(s->scale > 0.0f) || isinf(s->scale)) return fail(QSA_E_INVALID, "scale must be positive and finite");
+    if (s->q_row_stride < 0 || s->q_head_stride < 0 || s->out_row_stride < 0 || s->out_head_stride < 0 ||
+        s->kv_block_stride < 0 || s->kv_slot_stride < 0 || s->kv_head_stride < 0)
+        return fail(QSA_E_INVALID, "strides must be >= 0");
+    if ((s->num_rows > 1 && s->out_row_stride < s->head_dim) || (s->num_heads > 1 && s->out_head_stride < s->head_dim))
+        return fail(QSA_E_INVALID, "the strides of out must be at least head_dim");
+    if (sparse) {
+        if (k < 1) return fail(QSA_E_INVALID, "k = %d < 1", k);
+        if (ratio < 1) return fail(QSA_E_INVALID, "ratio = %d < 1", ratio);
+    }
+    if (s->num_rows > 0 && (!q || !kcache || !vcache || !block_table || !per_row || !starts_or_idx || !out))
+        return fail(QSA_E_INVALID, "q, kcache, vcache, block_table, %s and out must be non-NULL",
+                    sparse ? "row_to_req, idx" : "ctx_lens, q_starts");
+    if (s->dtype != QSA_BF16 && s->dtype != QSA_FP16) return fail(QSA_E_DTYPE, "dtype = %d (built: bf16, fp16)", s->dtype);
+    if (s->head_dim != 64 && s->head_dim != 128)
+        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
+    if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
+    if (s->num_heads / s->num_kv_heads > 128)
+        return fail(QSA_E_UNSUPPORTED, "%d heads per kv head (built: 1 to 128)", s->num_heads / s->num_kv_heads);
+    if (s->num_heads > 8192) return fail(QSA_E_UNSUPPORTED, "num_heads = %d (built: up to 8192)", s->num_heads);
+    if (s->num_rows > (1 << 22) || s->num_reqs > (1 << 22))
+        return fail(QSA_E_RANGE, "num_rows = %d or num_reqs = %d > 2^22", s->num_rows, s->num_reqs);
+    if ((int64_t)s->max_blocks * s->block_size > (1 << 30))
+        return fail(QSA_E_RANGE, "max_blocks * block_size = %lld > 2^30", (long long)s->max_blocks * s->block_size);
+    if (sparse && (int64_t)k * ratio > (1 << 24))
+        return fail(QSA_E_RANGE, "k * ratio = %lld > 2^24", (long long)k * ratio);
+    const int64_t most = (int64_t)1 << 38;
+    if (s->num_blocks > ((int64_t)1 << 50) || s->kv_block_stride > ((int64_t)1 << 50) / s->num_blocks ||
+        s->kv_slot_stride > most || s->kv_head_stride > most || s->q_row_stride > most || s->q_head_stride > most ||
+        s->out_row_stride > most || s->out_head_stride > most)
+        return fail(QSA_E_RANGE, "a stride or the cache is too large");
+    if (s->num_rows > 0 && (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(out)))
+        return fail(QSA_E_ALIGN, "q, kcache, vcache and out must be 16-byte aligned");
+    if (s->num_rows > 0 && ((s->q_row_stride | s->q_head_stride | s->out_row_stride | s->out_head_stride |
+                             s->kv_block_stride | s->kv_slot_stride | s->kv_head_stride) & 7) != 0)
+        return fail(QSA_E_ALIGN, "strides must be multiples of 8 elements");
+    return ok();
+}
+
+qsa_status check_workspace(const void *workspace, int64_t bytes, int64_t need) {
+    if (!workspace) return ok();
+    if (bytes < need)
+        return fail(QSA_E_INVALID, "workspace_bytes = %lld < %lld", (long long)bytes, (long long)need);
+    if (need > 0 && !aligned16(workspace)) return fail(QSA_E_ALIGN, "workspace must be 16-byte aligned");
+    return ok();
+}
+
+qsa::AttnArgs attn_args(const void *q, const void *kcache, const void *vcache, const int32_t *block_table, void *out,
+                        float *lse, const qsa_attn_shape *s) {
+    qsa::AttnArgs a = {};
+    a.q = q;
+    a.kcache = static_cast<const uint8_t *>(kcache);
+    a.vcache = static_cast<const uint8_t *>(vcache);
+    a.block_table = block_table;
+    a.out = out;
+    a.lse = lse;
+    a.num_rows = s->num_rows;
+    a.num_kv_heads = s->num_kv_heads;
+    a.group = s->num_heads / s->num_kv_heads;
+    a.head_dim = s->head_dim;
+    a.block_size = s->block_size;
+    a.num_reqs = s->num_reqs;
+    a.max_blocks = s->max_blocks;
+    a.cap = s->max_blocks * s->block_size;
+    a.dtype = s->dtype;
+    a.scale_log2 = s->scale * 1.44269504088896340736f;
+    a.num_blocks = s->num_blocks;
+    a.q_row = s->q_row_stride;
+    a.q_head = s->q_head_stride;
+    a.o_row = s->out_row_stride;
+    a.o_head = s->out_head_stride;
+    a.kv_block = s->kv_block_stride;
+    a.kv_slot = s->kv_slot_stride;
+    a.kv_head = s->kv_head_stride;
+    return a;
+}
+
+void stream_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
+    a.sub_heads = p.sub_heads;
+    a.num_subs = p.num_subs;
+    a.tile_rows = p.stream_rows;
+    a.slots = p.slots;
+    a.slots_per_req = p.slots_per_req;
+    a.splits = workspace ? p.splits : 1;
+    a.part = static_cast<float *>(workspace);
+}
+
+}  // namespace
+
+extern "C" {
+
+qsa_status qsa_plan_batch_check(const int32_t *past_lens, const int32_t *new_lens, const int32_t *free_blocks,
+                                const int32_t *block_table, const int32_t *q_starts, const int32_t *row_to_req,
+                                const int32_t *ctx_lens, const int64_t *slots, const qsa_plan_shape *shape) {
+    return check_plan(past_lens, new_lens, free_blocks, block_table, q_starts, row_to_req, ctx_lens, slots, shape);
+}
+
+qsa_status qsa_plan_batch(const int32_t *past_lens, const int32_t *new_lens, const int32_t *free_blocks,
+                          int32_t *block_table, int32_t *q_starts, int32_t *row_to_req, int32_t *ctx_lens,
+                          int64_t *slots, int32_t *col_lens, int64_t *col_slots, int32_t *blocks_used,
+                          const qsa_plan_shape *s, void *stream) {
+    qsa_status st = check_plan(past_lens, new_lens, free_blocks, block_table, q_starts, row_to_req, ctx_lens, slots, s);
+    if (st != QSA_OK) return st;
+    qsa::PlanArgs a = {past_lens, new_lens, free_blocks, block_table, q_starts, row_to_req, ctx_lens, slots, col_lens,
+                       col_slots, blocks_used, s->num_reqs, s->max_blocks, s->block_size, s->ratio, s->num_rows,
+                       s->num_free, s->num_blocks};
+    return launched(qsa::launch_plan(a, static_cast<hipStream_t>(stream)));
+}
+
+qsa_status qsa_write_kv_check(const void *k, const void *v, const int64_t *slots, const void *kcache,
+                              const void *vcache, const qsa_kv_shape *shape) {
+    return check_write_kv(k, v, slots, kcache, vcache, shape);
+}
+
+qsa_status qsa_write_kv(const void *k, const void *v, const int64_t *slots, void *kcache, void *vcache,
+                        const qsa_kv_shape *s, void *stream) {
+    qsa_status st = check_write_kv(k, v, slots, kcache, vcache, s);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    qsa::WriteKvArgs a = {static_cast<const uint8_t *>(k), static_cast<const uint8_t *>(v), slots,
+                          static_cast<uint8_t *>(kcache), static_cast<uint8_t *>(vcache), s->num_rows,
+                          s->num_kv_heads, s->head_dim, s->block_size, s->num_blocks, s->src_row_stride,
+                          s->src_head_stride, s->kv_block_stride, s->kv_slot_stride, s->kv_head_stride};
+    return launched(qsa::launch_write_kv(a, static_cast<hipStream_t>(stream)));
+}
+
+qsa_status qsa_write_keys_check(const void *keys, const int64_t *slots, const void *kcache, const float *kscale,
+                                const qsa_keys_shape *shape) {
+    return check_write_keys(keys, slots, kcache, kscale, shape);
+}
+
+qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, float *kscale,
+                          const qsa_keys_shape *s, void *stream) {
+    qsa_status st = check_write_keys(keys, slots, kcache, kscale, s);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    const int64_t elt = s->k_dtype == QSA_FP8_E4M3FN ? 1 : 2;
+    const int64_t block = (int64_t)s->block_size * (s->head_dim * elt + (s->kv_layout != QSA_KV_PAGED ? 4 : 0));
+    qsa::WriteKeysArgs a = {static_cast<const uint8_t *>(keys), slots, static_cast<uint8_t *>(kcache), kscale,
+                            s->num_rows, s->head_dim, s->block_size, s->src_dtype, s->k_dtype, s->kv_layout,
+                            s->num_blocks, s->src_stride, block};
+    return launched(qsa::launch_write_keys(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *s) {
+    if (!s || s->num_rows <= 0 || s->num_reqs < 1 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads) return 0;
+    return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes;
+}
+
+qsa_status qsa_paged_attention_check(const void *q, const void *kcache, const void *vcache,
+                                     const int32_t *block_table, const int32_t *ctx_lens, const int32_t *q_starts,
+                                     const void *out, const qsa_attn_shape *s, const void *workspace,
+                                     int64_t workspace_bytes) {
+    qsa_status st = check_attn(q, kcache, vcache, block_table, ctx_lens, q_starts, out, s, false, 0, 0);
+    if (st != QSA_OK) return st;
+    return check_workspace(workspace, workspace_bytes, qsa_paged_attention_workspace_bytes(s));
+}
+
+qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
+                               const int32_t *ctx_lens, const int32_t *q_starts, void *out, float *lse,
+                               const qsa_attn_shape *s, void *workspace, int64_t workspace_bytes, void *stream) {
+    qsa_status st = qsa_paged_attention_check(q, kcache, vcache, block_table, ctx_lens, q_starts, out, s, workspace,
+                                              workspace_bytes);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    const AttnPlan p = plan_attn(s, false, (int64_t)s->max_blocks * s->block_size);
+    qsa::AttnArgs a = attn_args(q, kcache, vcache, block_table, out, lse, s);
+    a.ctx_lens = ctx_lens;
+    a.q_starts = q_starts;
+    hipError_t e = hipSuccess;
+    if (p.tile) {
+        qsa::AttnArgs b = a;
+        b.tile_rows = 256 / b.group;
+        b.slots = s->num_rows / b.tile_rows + s->num_reqs;
+        b.min_rows = p.stream ? p.few_rows + 1 : 1;
+        b.max_rows = s->num_rows;
+        e = qsa::launch_attn_tile(b, static_cast<hipStream_t>(stream));
+    }
+    if (e == hipSuccess && p.stream) {
+        stream_shape(a, p, workspace);
+        a.min_rows = 1;
+        a.max_rows = p.tile ? p.few_rows : s->num_rows;
+        e = qsa::launch_attn_stream(a, false, static_cast<hipStream_t>(stream));
+    }
+    return launched(e);
+}
+
+int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *s, int32_t k, int32_t ratio) {
+    if (!s || s->num_rows <= 0 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads || k < 1 || ratio < 1) return 0;
+    return plan_attn(s, true, (int64_t)k * ratio).bytes;
+}
+
+qsa_status qsa_sparse_attention_check(const void *q, const void *kcache, const void *vcache,
+                                      const int32_t *block_table, const int32_t *row_to_req, const int32_t *idx,
+                                      int32_t k, int32_t ratio, const void *out, const qsa_attn_shape *s,
+                                      const void *workspace, int64_t workspace_bytes) {
+    qsa_status st = check_attn(q, kcache, vcache, block_table, row_to_req, idx, out, s, true, k, ratio);
+    if (st != QSA_OK) return st;
+    return check_workspace(workspace, workspace_bytes, qsa_sparse_attention_workspace_bytes(s, k, ratio));
+}
+
+qsa_status qsa_sparse_attention(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
+                                const int32_t *row_to_req, const int32_t *idx, int32_t k, int32_t ratio,
+                                const int32_t *token_lens, void *out, float *lse, const qsa_attn_shape *s,
+                                void *workspace, int64_t workspace_bytes, void *stream) {
+    qsa_status st = qsa_sparse_attention_check(q, kcache, vcache, block_table, row_to_req, idx, k, ratio, out, s,
+                                               workspace, workspace_bytes);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    const AttnPlan p = plan_attn(s, true, (int64_t)k * ratio);
+    qsa::AttnArgs a = attn_args(q, kcache, vcache, block_table, out, lse, s);
+    a.ctx_lens = token_lens;
+    a.row_to_req = row_to_req;
+    a.idx = idx;
+    a.k = k;
+    a.ratio = ratio;
+    stream_shape(a, p, workspace);
+    return launched(qsa::launch_attn_stream(a, true, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

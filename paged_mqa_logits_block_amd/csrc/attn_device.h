@@ -1,0 +1,252 @@
+// Device-side parts shared by the attention kernels: operand types, the copies
+// to LDS, the transposed reads and the score / output products of one wave.
+//
+// One wave works on 32 stacked (row, head) pairs and 32 keys at a time, with the
+// 32x32x16 MFMA in transposed form:
+//
+//   S^T = K Q^T:  A = K (lane: key l & 31, elements 8 (l >> 5) .. + 7 of each 16),
+//                 B = Q (lane: pair l & 31, the same elements)
+//   O^T = V^T P^T: A = V^T (lane: output element l & 31), B = P^T
+//
+// A lane of the result holds one column, pair l & 31, and 16 of the 32 rows:
+// register i is row 8 (i >> 2) + 4 (l >> 5) + (i & 3).  So each lane keeps the
+// running maximum and sum of its own pair, a step's maximum needs one exchange
+// (with lane l ^ 32), rescaling the output is a product by a value that the
+// lane already has, and the scores feed the second product without moving
+// between lanes: MFMA sums over its 16 inner elements in any order, so inner
+// element 8 (l >> 5) + j of step t stands for key 16 t + 4 (l >> 5) + j (j < 4) or
+// 16 t + 8 + 4 (l >> 5) + j - 4, which are registers 8 t .. 8 t + 7 of the scores.
+#pragma once
+
+#include "attn_internal.h"
+#include "qsa_device.h"
+#include "qsa_internal.h"
+
+namespace qsa {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+constexpr float kLn2 = 0.693147180559945f;
+
+template <int DT>
+struct Half;
+template <>
+struct Half<kBF16> {
+    typedef __bf16 T;
+    typedef bf16x8 V8;
+};
+template <>
+struct Half<kFP16> {
+    typedef _Float16 T;
+    typedef f16x8 V8;
+};
+
+template <int DT>
+__device__ __forceinline__ f32x16 mfma32(i32x4 a, i32x4 b, f32x16 c) {
+    typedef typename Half<DT>::V8 V8;
+    if constexpr (DT == kBF16)
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+}
+
+// 8 values rounded to nearest into 16 bits.  The weights are rounded here to
+// the caches' type: each is off by at most half a step of that type relative to
+// itself, as the output is, and the MFMA then runs at its 16-bit rate.  The sum
+// of the weights is taken before the rounding.
+template <int DT>
+__device__ __forceinline__ i32x4 pack8(const f32x16 &p, int at) {
+    typename Half<DT>::V8 v;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = (typename Half<DT>::T)p[at + j];
+    return __builtin_bit_cast(i32x4, v);
+}
+
+template <int DT>
+__device__ __forceinline__ float to_f32(uint16_t u) {
+    return (float)__builtin_bit_cast(typename Half<DT>::T, u);
+}
+
+// max(v, v of lane l ^ 32)
+__device__ __forceinline__ float xor32_max(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// 16 bytes per lane from global memory to LDS at lds_wave + 16 * lane (lds_wave
+// wave-uniform); outstanding on the vector memory counter until wait_copies().
+__device__ __forceinline__ void copy16(const void *src, uint32_t lds_wave) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(src), "s"(lds_wave)
+        : "memory");
+}
+
+__device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_offset(const void *p) {
+    return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+
+// Keys and values lie in LDS as rows of D elements, the 16-byte chunks of a row
+// permuted by an XOR with the row's number: the copies write LDS linearly, so
+// each lane takes its chunk from the permuted place in global memory.  K rows
+// are read by 32 lanes at the same chunk (16 bytes each): the permutation puts
+// the rows of every 16 neighbouring lanes into different 16-byte columns of the
+// banks.  V is read transposed, 4 rows x 16 elements by 16 lanes: the chunk
+// pairs of 4 neighbouring rows are kept apart.
+template <int D>
+__device__ __forceinline__ int swz_k(int row) {
+    return D == 128 ? (row & 15) : ((row >> 1) & 7);
+}
+template <int D>
+__device__ __forceinline__ int swz_v(int row) {
+    return D == 128 ? 2 * (row & 7) : 2 * ((row >> 1) & 3);
+}
+
+// scores S^T of 32 keys (LDS rows from kbase) against the wave's pairs
+template <int DT, int D>
+__device__ __forceinline__ f32x16 score_tile(const uint8_t *kbase, const i32x4 (&q)[D / 16], int lane) {
+    const int row = lane & 31, h = lane >> 5;
+    f32x16 s = {};
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c) {
+        const i32x4 k = *reinterpret_cast<const i32x4 *>(kbase + row * 2 * D + (((2 * c + h) ^ swz_k<D>(row)) << 4));
+        s = mfma32<DT>(k, q[c], s);
+    }
+    return s;
+}
+
+// four rows' elements as the transposing read gives them: lane i of 16 gets
+// element i of the group's 16, rows 0..3
+__device__ __forceinline__ s16x4 read_tr(const uint8_t *p) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
+}
+
+// O^T += V^T P^T over 32 keys (LDS rows from vbase), p the weights of score_tile's
+// layout
+template <int DT, int D>
+__device__ __forceinline__ void output_tile(const uint8_t *vbase, const f32x16 &p, f32x16 (&o)[D / 32], int lane) {
+    const int h = lane >> 5, half = (lane >> 4) & 1, i = lane & 15;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const i32x4 b = pack8<DT>(p, 8 * t);
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) {
+            const int chunk = 4 * m + 2 * half + ((i & 3) >> 1);
+            s16x4 v[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int row = 16 * t + 8 * u + 4 * h + (i >> 2);
+                v[u] = read_tr(vbase + row * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1));
+            }
+            i32x4 a;
+            const auto v0 = __builtin_bit_cast(i32x2, v[0]), v1 = __builtin_bit_cast(i32x2, v[1]);
+            a[0] = v0[0];
+            a[1] = v0[1];
+            a[2] = v1[0];
+            a[3] = v1[1];
+            o[m] = mfma32<DT>(a, b, o[m]);
+        }
+    }
+}
+
+// the key (0..31) that register i of a score tile holds in this lane
+__device__ __forceinline__ int score_key(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
+
+// The request that takes row tile `slot`, and the tile's first row: request i,
+// rows [s_i, s_{i+1}), owns the slots from s_i / T + i on.  These are strictly
+// increasing in i and leave room for ceil(len / T) tiles each, so no prefix sum
+// over the requests is needed.  Returns false for a slot without rows.
+//
+// Where the launch takes only requests of few rows, slots_per_req > 0 gives
+// every request that many slots instead.
+struct RowTile {
+    int req, row0, rows;
+};
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int slot, RowTile &t) {
+    const int n = a.num_reqs, T = a.tile_rows, lane = lane_id();
+    const auto start = [&](int i) { return min(max(a.q_starts[i], 0), a.num_rows); };
+    int lo = 0, j;
+    if (a.slots_per_req > 0) {
+        lo = slot / a.slots_per_req;
+        j = slot - lo * a.slots_per_req;
+    } else {
+        // 64-way search for the last i in [0, n) with start(i) / T + i <= slot
+        int len = n;
+        while (len > 1) {
+            const int step = (len + kWave - 1) / kWave;
+            const int off = lane * step, i = lo + off;
+            const bool le = off < len && start(i) / T + i <= slot;
+            const uint64_t b = ballot(le);
+            const int last = b ? 63 - __builtin_clzll(b) : 0;
+            lo += last * step;
+            len = min(step, len - last * step);
+        }
+        j = slot - (start(lo) / T + lo);
+    }
+    const int s0 = start(lo), s1 = start(lo + 1);
+    const int64_t row0 = (int64_t)s0 + (int64_t)j * T;
+    const int rows = s1 - s0;
+    if (j < 0 || row0 >= s1 || rows < a.min_rows || rows > a.max_rows) return false;
+    t.req = lo;
+    t.row0 = (int)row0;
+    t.rows = min(T, s1 - (int)row0);
+    return true;
+}
+
+__device__ __forceinline__ float wave_sum_f(float v) {
+#pragma unroll
+    for (int m = 1; m < kWave; m <<= 1) v += xor_lane_f(v, m);
+    return v;
+}
+
+// One pair's softmax state over keys [k0, k1), by one wave with plain loads: the
+// key range of every pair is its own, where the tile kernels multiply a zero
+// weight with the value of a key that another row of the tile sees.  Taken only
+// when such a value is not finite (see the caller).
+template <int DT, int D>
+__device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, int k0,
+                                                    int k1, float &m, float &l, float (&o)[D / 64]) {
+    const int lane = lane_id();
+    m = kNegInf;
+    l = 0.0f;
+    for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
+    for (int base = k0; base < k1; base += kWave) {
+        const int key = base + lane;
+        float s = kNegInf;
+        int64_t off = 0;
+        if (key < k1) {
+            const int e = a.block_table[(int64_t)req * a.max_blocks + key / a.block_size];
+            const bool bad = e < 0 || e >= a.num_blocks;
+            off = (bad ? 0 : (int64_t)e * a.kv_block) + (int64_t)(key % a.block_size) * a.kv_slot + hk * a.kv_head;
+            const uint16_t *k = reinterpret_cast<const uint16_t *>(a.kcache) + off;
+            float dot = 0.0f;
+            for (int d = 0; d < D; ++d) dot += to_f32<DT>(q[d]) * to_f32<DT>(k[d]);
+            s = bad ? __builtin_nanf("") : dot * a.scale_log2;
+        }
+        const float top = fmaxf(m, wave_max_f(s));
+        const float ref = top == kNegInf ? 0.0f : top;
+        const float p = __builtin_amdgcn_exp2f(s - ref), keep = __builtin_amdgcn_exp2f(m - ref);
+        l = l * keep + wave_sum_f(p);
+        for (int i = 0; i < D / 64; ++i) o[i] *= keep;
+        m = top;
+        for (int j = 0; j < min(kWave, k1 - base); ++j) {
+            const float pj = readlane_f(p, j);
+            const int64_t oj = ((int64_t)readlane((int)(off >> 32), j) << 32) | (uint32_t)readlane((int)off, j);
+            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache) + oj;
+            for (int i = 0; i < D / 64; ++i) o[i] += pj * to_f32<DT>(v[lane * (D / 64) + i]);
+        }
+    }
+}
+
+}  // namespace qsa

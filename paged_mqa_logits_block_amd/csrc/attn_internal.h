@@ -1,0 +1,93 @@
+// Host/device interface of the attention kernels (paged chunk attention and
+// attention over selected tokens) and of the kernels that fill their inputs.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qsa {
+
+// Stacked (row, head) pairs of one wave's MFMA tile.
+constexpr int kAttnTile = 32;
+// Keys per step of a streaming wave, and waves per streaming workgroup.
+constexpr int kStreamKeys = 32;
+constexpr int kStreamWaves = 4;
+
+struct AttnArgs {
+    const void *q;
+    const uint8_t *kcache;
+    const uint8_t *vcache;
+    const int32_t *block_table;
+    const int32_t *ctx_lens;    // dense: visible keys per row; sparse: token limit per row, or null
+    const int32_t *q_starts;    // dense: [num_reqs + 1]
+    const int32_t *row_to_req;  // sparse
+    const int32_t *idx;         // sparse: [num_rows][k]
+    void *out;
+    float *lse;                 // or null
+    float *part;                // split partials, or null when splits == 1
+    int32_t num_rows;
+    int32_t num_kv_heads;
+    int32_t group;              // query heads per kv head
+    int32_t head_dim;
+    int32_t block_size;
+    int32_t num_reqs;
+    int32_t max_blocks;
+    int32_t cap;                // tokens a table row can hold
+    int32_t k, ratio;           // sparse: selected columns per row, tokens per column
+    int32_t dtype;
+    float scale_log2;           // softmax scale * log2(e)
+    int64_t num_blocks;
+    int64_t q_row, q_head;      // strides in elements
+    int64_t o_row, o_head;
+    int64_t kv_block, kv_slot, kv_head;
+    // launch shape
+    int32_t slots;              // row tiles of the grid
+    int32_t slots_per_req;      // dense: > 0 where every request has that many
+    int32_t sub_heads;          // query heads per workgroup of one kv head
+    int32_t num_subs;           // workgroups per kv head
+    int32_t tile_rows;          // query rows per tile
+    int32_t splits;
+    int32_t min_rows, max_rows; // dense: the requests this launch takes, by their row count
+};
+
+hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
+hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s);
+
+struct PlanArgs {
+    const int32_t *past_lens, *new_lens, *free_blocks;
+    int32_t *block_table, *q_starts, *row_to_req, *ctx_lens;
+    int64_t *slots;
+    int32_t *col_lens;
+    int64_t *col_slots;
+    int32_t *blocks_used;
+    int32_t num_reqs, max_blocks, block_size, ratio, num_rows, num_free;
+    int64_t num_blocks;
+};
+
+constexpr int kPlanMaxReqs = 4096;
+hipError_t launch_plan(const PlanArgs &a, hipStream_t s);
+
+struct WriteKvArgs {
+    const uint8_t *k, *v;
+    const int64_t *slots;
+    uint8_t *kcache, *vcache;
+    int32_t num_rows, num_kv_heads, head_dim, block_size;
+    int64_t num_blocks;
+    int64_t src_row, src_head;  // strides in elements
+    int64_t kv_block, kv_slot, kv_head;
+};
+
+hipError_t launch_write_kv(const WriteKvArgs &a, hipStream_t s);
+
+struct WriteKeysArgs {
+    const uint8_t *src;
+    const int64_t *slots;
+    uint8_t *kcache;
+    float *kscale;
+    int32_t num_rows, head_dim, block_size, src_dtype, k_dtype, layout;
+    int64_t num_blocks, src_stride, block_bytes;
+};
+
+hipError_t launch_write_keys(const WriteKeysArgs &a, hipStream_t s);
+
+}  // namespace qsa

@@ -1,0 +1,146 @@
+// Batch plan: request lengths -> row starts, rows' requests, visible counts and
+// cache slots, and the block table's new entries taken from a free list.
+//
+// With n_i new tokens behind p_i cached ones, the rows of request i are
+// [s_i, s_i + n_i), s the exclusive prefix sum of n, and the row at token
+// t = p_i + (r - s_i) goes to slot t % B of table entry t / B.  The entries
+// [ceil(p_i / B), ceil((p_i + n_i) / B)) are new: entry e takes element
+// u_i + e - ceil(p_i / B) of the free list, u the exclusive prefix sum of the
+// requests' new block counts.
+//
+// What bounds it is latency: a few hundred KB move.  One launch does it all:
+// every workgroup builds both prefix sums in LDS for itself (at most 4,096
+// requests, 16 per thread, read from L2) and then takes its share of the rows
+// and of the new entries, found by binary search in LDS.  No workgroup reads
+// what another writes: the entry behind a row is computed from the free list
+// when it is new, and new entries are the only ones written.  The result does
+// not depend on the order of the workgroups.
+
+#include "attn_internal.h"
+#include "qsa_device.h"
+
+namespace qsa {
+namespace {
+
+constexpr int kPlanThreads = 256;
+
+// Exclusive prefix sum of the threads' totals over the workgroup, saturating at
+// `most` (saturating addition is associative, so the order does not matter).  Values are in [0, most], most < 2^31.
+__device__ __forceinline__ uint32_t block_offset(uint32_t own, uint32_t most, uint32_t *wave_sums) {
+    const int lane = lane_id(), w = threadIdx.x >> 6;
+    uint32_t inc = own;
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const uint32_t u = (uint32_t)shfl_i((int)inc, lane >= d ? lane - d : lane);
+        if (lane >= d) inc = min(inc + u, most);
+    }
+    if (lane == kWave - 1) wave_sums[w] = inc;
+    __syncthreads();
+    uint32_t off = (uint32_t)shfl_i((int)inc, lane > 0 ? lane - 1 : 0);
+    if (lane == 0) off = 0;
+    for (int i = 0; i < w; ++i) off = min(off + wave_sums[i], most);
+    __syncthreads();
+    return off;
+}
+
+// the i in [0, n) with starts[i] <= x < starts[i + 1]
+__device__ __forceinline__ int find(const uint32_t *starts, int n, uint32_t x) {
+    int lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] <= x) lo = mid;
+        else hi = mid;
+    }
+    return lo;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
+    __shared__ uint32_t starts[kPlanMaxReqs + 1];
+    __shared__ uint32_t taken[kPlanMaxReqs + 1];
+    __shared__ int32_t past[kPlanMaxReqs];
+    __shared__ uint32_t sums[kPlanThreads / kWave];
+    const int t = threadIdx.x, n = a.num_reqs;
+    const uint32_t B = (uint32_t)a.block_size, cap = (uint32_t)a.max_blocks * B;
+    const uint32_t most = (uint32_t)a.num_rows;
+    const int per = (n + kPlanThreads - 1) / kPlanThreads;
+    const int i0 = min(t * per, n), i1 = min(i0 + per, n);
+
+    uint32_t own = 0;
+    for (int i = i0; i < i1; ++i) own = min(own + (uint32_t)min(max(a.new_lens[i], 0), a.num_rows), most);
+    uint32_t at = block_offset(own, most, sums);
+    for (int i = i0; i < i1; ++i) {
+        starts[i] = at;
+        at = min(at + (uint32_t)min(max(a.new_lens[i], 0), a.num_rows), most);
+        past[i] = (int32_t)min((uint32_t)max(a.past_lens[i], 0), cap);
+        if (i == n - 1) starts[n] = at;
+    }
+    __syncthreads();
+    const auto blocks = [&](int i) {
+        const uint32_t p = (uint32_t)past[i], end = min(p + (starts[i + 1] - starts[i]), cap);
+        return (end + B - 1) / B - (p + B - 1) / B;
+    };
+    own = 0;
+    for (int i = i0; i < i1; ++i) own += blocks(i);
+    at = block_offset(own, 0x7FFFFFFFu, sums);
+    for (int i = i0; i < i1; ++i) {
+        taken[i] = at;
+        at += blocks(i);
+        if (i == n - 1) taken[n] = at;
+    }
+    __syncthreads();
+
+    const uint32_t live = starts[n], fresh = taken[n];
+    const uint32_t step = gridDim.x * kPlanThreads, first = blockIdx.x * kPlanThreads + t;
+    if (blockIdx.x == 0) {
+        for (int i = t; i <= n; i += kPlanThreads) a.q_starts[i] = (int32_t)starts[i];
+        if (t == 0 && a.blocks_used) a.blocks_used[0] = (int32_t)fresh;
+    }
+    for (uint32_t f = first; f < fresh; f += step) {
+        const int i = find(taken, n, f);
+        const uint32_t e = ((uint32_t)past[i] + B - 1) / B + (f - taken[i]);
+        a.block_table[(int64_t)i * a.max_blocks + e] = f < (uint32_t)a.num_free ? a.free_blocks[f] : -1;
+    }
+    const uint32_t ratio = (uint32_t)a.ratio;
+    for (uint32_t r = first; r < most; r += step) {
+        int req = 0;
+        uint32_t seen = 0;
+        int64_t slot = -1, col = -1;
+        if (r < live) {
+            req = find(starts, n, r);
+            const uint32_t p = (uint32_t)past[req], tok = p + (r - starts[req]);
+            seen = min(tok + 1, cap);
+            if (tok < cap) {
+                const uint32_t e = tok / B, in = tok - e * B, held = (p + B - 1) / B;
+                int64_t block;
+                if (e < held) {
+                    block = a.block_table[(int64_t)req * a.max_blocks + e];
+                } else {
+                    const uint32_t f = taken[req] + (e - held);
+                    block = f < (uint32_t)a.num_free ? a.free_blocks[f] : -1;
+                }
+                if (block >= 0 && block < a.num_blocks) {
+                    slot = block * B + in;
+                    if ((tok + 1) % ratio == 0) col = block * (B / ratio) + in / ratio;
+                }
+            }
+        }
+        a.row_to_req[r] = req;
+        a.ctx_lens[r] = (int32_t)seen;
+        a.slots[r] = slot;
+        if (a.col_lens) a.col_lens[r] = (int32_t)(seen / ratio);
+        if (a.col_slots) a.col_slots[r] = col;
+    }
+}
+
+}  // namespace
+
+hipError_t launch_plan(const PlanArgs &a, hipStream_t s) {
+    const int64_t items = a.num_rows;
+    int64_t groups = (items + kPlanThreads - 1) / kPlanThreads;
+    if (groups < 1) groups = 1;
+    if (groups > 256) groups = 256;
+    hipLaunchKernelGGL(plan_kernel, dim3((unsigned)groups), dim3(kPlanThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+}  // namespace qsa
