@@ -210,6 +210,14 @@ __device__ __forceinline__ float wave_sum_f(float v) {
     return v;
 }
 
+// The kernel's arguments where the launch put them.  A kernel that hands its own
+// parameter by reference to a function that is not inlined keeps a copy of it in
+// scratch memory and reads every field from there, in its loops too (the
+// streaming kernel took 262 us that way over 539 MB of cache).
+__device__ __forceinline__ const AttnArgs &launch_args() {
+    return *(const AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
 // One pair's softmax state over keys [k0, k1), by one wave with plain loads: the
 // key range of every pair is its own, where the tile kernels multiply a zero
 // weight with the value of a key that another row of the tile sees.  Taken only

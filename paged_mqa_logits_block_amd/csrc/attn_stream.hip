@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kStreamThreads, 1) void attn_stream_kernel(AttnArgs
                 const Pair x = pair_of(a, w, p);
                 if (!x.live) continue;
                 float pm2, pl2, po[D / 64];
-                own_range<DT, D>(a, w.req, static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
+                own_range<DT, D>(launch_args(), w.req, static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
                                  w.hk, t0 * kStreamKeys, min(t1 * kStreamKeys, visible<SPARSE>(a, x.row)), pm2, pl2,
                                  po);
                 for (int i = 0; i < D / 64; ++i) again[p * kPad + lane * (D / 64) + i] = po[i];
@@ -335,37 +335,49 @@ __global__ __launch_bounds__(kStreamThreads, 1) void attn_stream_kernel(AttnArgs
         a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
-// Joins the splits' states of 8 pairs of a tile: 32 threads to a pair.
-constexpr int kJoinPairs = 8;
+// Joins the splits' states, one wave to a pair: lane i reads split i's maximum
+// and sum, and the outputs are read 8 splits at a time, D / 64 elements per lane.
+constexpr int kJoinPairs = 4;
 
 template <int DT, int D, bool SPARSE>
-__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-    constexpr int kPer = D / 32;
+__global__ __launch_bounds__(64 * kJoinPairs) void attn_join_kernel(AttnArgs a) {
+    constexpr int kPer = D / 64, kBatch = 8;
+    typedef float Vec __attribute__((ext_vector_type(kPer)));
     TileWork w;
     if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
-    const int pm = blockIdx.z * kJoinPairs + (threadIdx.x >> 5), d0 = (threadIdx.x & 31) * kPer;
+    const int lane = threadIdx.x & 63;
+    const int pm = __builtin_amdgcn_readfirstlane(blockIdx.z * kJoinPairs + (threadIdx.x >> 6));
     const Pair pp = pair_of(a, w, pm);
     if (!pp.live) return;
-    const int keys = tile_keys<SPARSE>(a, w);
-    const float *part = a.part + (int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.splits * (kAttnTile * (D + 2));
+    const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w));
+    constexpr int kPart = kAttnTile * (D + 2);
+    const float *part = a.part + (int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.splits * kPart;
     const int steps = (keys + kStreamKeys - 1) / kStreamKeys, per = split_steps(steps, a.splits);
     const int used = (steps + per - 1) / per;
-    float top = kNegInf, total = 0.0f, r[kPer] = {};
-    for (int i = 0; i < used; ++i) top = fmaxf(top, part[(int64_t)i * kAttnTile * (D + 2) + kAttnTile * D + pm]);
-    const float ref = top == kNegInf ? 0.0f : top;
-    for (int i = 0; i < used; ++i) {
-        const float *p = part + (int64_t)i * kAttnTile * (D + 2);
-        const float f = __builtin_amdgcn_exp2f(p[kAttnTile * D + pm] - ref);
-        total += p[kAttnTile * (D + 1) + pm] * f;
+    float m = kNegInf, l = 0.0f;
+    if (lane < used) {
+        m = part[lane * kPart + kAttnTile * D + pm];
+        l = part[lane * kPart + kAttnTile * (D + 1) + pm];
+    }
+    const float top = wave_max_f(m), ref = top == kNegInf ? 0.0f : top;
+    const float f = __builtin_amdgcn_exp2f(m - ref);
+    const float total = wave_sum_f(l * f);
+    Vec r = {};
+    const float *src = part + pm * D + kPer * lane;
+    for (int i = 0; i < used; i += kBatch) {
+        Vec v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) r[j] += p[pm * D + d0 + j] * f;
+        for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const Vec *>(src + min(i + j, used - 1) * kPart);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            if (i + j < used) r += v[j] * readlane_f(f, i + j);
     }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     typedef typename Half<DT>::T T;
-    T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + d0;
+    T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + kPer * lane;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) out[j] = (T)(r[j] * inv);
-    if (a.lse && (threadIdx.x & 31) == 0)
+    if (a.lse && lane == 0)
         a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
@@ -376,7 +388,7 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
                        dim3(kStreamThreads), 0, s, a);
     if (a.splits > 1)
         hipLaunchKernelGGL((attn_join_kernel<DT, D, SPARSE>),
-                           dim3((unsigned)a.slots, heads, kAttnTile / kJoinPairs), dim3(256), 0, s, a);
+                           dim3((unsigned)a.slots, heads, kAttnTile / kJoinPairs), dim3(64 * kJoinPairs), 0, s, a);
     return hipGetLastError();
 }
 

@@ -19,15 +19,16 @@ constexpr int kTileKeys = 64;
 
 // The wave's pairs, each over its own visible keys (see own_range).
 template <int DT, int D>
-__device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, const RowTile &w, int wave, int hk) {
+__device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, int row0, int rows, int wave,
+                                                    int hk) {
     typedef typename Half<DT>::T T;
     const int lane = lane_id();
     for (int p = 0; p < kAttnTile; ++p) {
         const int m = wave * kAttnTile + p, r = m / a.group;
-        if (r >= w.rows) break;
-        const int row = w.row0 + r, head = hk * a.group + (m - r * a.group);
+        if (r >= rows) break;
+        const int row = row0 + r, head = hk * a.group + (m - r * a.group);
         float top, total, o[D / 64];
-        own_range<DT, D>(a, w.req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk, 0,
+        own_range<DT, D>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk, 0,
                          min(max(a.ctx_lens[row], 0), a.cap), top, total, o);
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
 #pragma unroll
             for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
         if (ballot(nan && live)) {
-            own_pairs<DT, D>(a, w, wave, hk);
+            own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk);
             return;
         }
     }
