@@ -111,15 +111,18 @@ qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *
 // The requests that the streaming kernel takes: up to this many stacked pairs
 // per kv head.
 constexpr int kStreamPairs = 64;
-// Workgroups that a split launch aims at, and the most splits
-constexpr int kSplitGroups = 1024, kMaxSplits = 64;
+// Stacked pairs per kv head of a batch that is streamed whole.
+constexpr int kSmallBatch = 512;
+// Tiles up to which a streamed launch cuts the keys into equal parts; with more,
+// every tile's workgroup takes all of its keys.
+constexpr int kBalancedTiles = 2048;
 
 struct AttnPlan {
     int sub_heads, num_subs, stream_rows;  // heads per workgroup, workgroups per kv head, rows per streaming tile
     int few_rows;                          // requests of up to this many rows are streamed
-    int slots, slots_per_req, splits;
+    int slots, slots_per_req;
     bool stream, tile;
-    int64_t bytes;
+    int64_t bytes;                         // workspace, 0: none used
 };
 
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
@@ -130,34 +133,30 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     p.num_subs = (group + p.sub_heads - 1) / p.sub_heads;
     p.stream_rows = sparse ? 1 : qsa::kAttnTile / p.sub_heads;
     p.few_rows = group >= kStreamPairs ? 1 : kStreamPairs / group;
-    int64_t tiles;
     if (sparse) {
         p.stream = true;
         p.slots = s->num_rows;
-        tiles = s->num_rows;
     } else {
+        const int T = p.stream_rows;
+        // A small batch of few rows per request (on average: the lengths are on the
+        // device) is streamed whole; a launch of the tile kernel that finds nothing
+        // to do costs 5 us.
+        if (s->num_rows > p.few_rows && (int64_t)s->num_rows <= (int64_t)p.few_rows * s->num_reqs &&
+            (int64_t)s->num_rows * group <= kSmallBatch &&
+            (int64_t)s->num_reqs * ((s->num_rows + T - 1) / T) <= qsa::kMaxSlots)
+            p.few_rows = s->num_rows;
         // with one request its rows are the call's rows, but for padding behind them
         p.stream = s->num_reqs > 1 || s->num_rows <= p.few_rows;
         p.tile = s->num_rows > p.few_rows;
-        const int T = p.stream_rows;
         const int rows = p.few_rows < s->num_rows ? p.few_rows : s->num_rows;
         const int64_t all = (int64_t)s->num_rows / T + s->num_reqs, per = (rows + T - 1) / T;
-        p.slots_per_req = per * s->num_reqs <= all ? (int)per : 0;
+        p.slots_per_req = per * s->num_reqs <= all || per * s->num_reqs <= qsa::kMaxSlots ? (int)per : 0;
         p.slots = (int)(p.slots_per_req ? per * s->num_reqs : all);
-        tiles = (s->num_rows + T - 1) / T;
-        const int64_t least = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
-        if (tiles < least) tiles = least;
-        if (tiles > p.slots) tiles = p.slots;
     }
-    const int64_t groups = tiles * s->num_kv_heads * p.num_subs;
-    int64_t splits = groups > 0 ? (kSplitGroups + groups - 1) / groups : 1;
-    const int64_t most = keys / (qsa::kStreamKeys * qsa::kStreamWaves);
-    if (splits > most) splits = most;
-    if (splits > kMaxSplits) splits = kMaxSplits;
-    p.splits = splits < 1 || !p.stream ? 1 : (int)splits;
-    p.bytes = p.splits > 1 ? (int64_t)p.slots * s->num_kv_heads * p.num_subs * p.splits * qsa::kAttnTile *
-                                 (s->head_dim + 2) * 4
-                           : 0;
+    const int64_t tiles = (int64_t)p.slots * s->num_kv_heads * p.num_subs;
+    if (p.stream && tiles > 0 && tiles <= kBalancedTiles && p.slots <= qsa::kMaxSlots &&
+        (sparse || p.slots_per_req) && keys > qsa::kStreamKeys * qsa::kStreamWaves)
+        p.bytes = qsa::attn_workspace_bytes(s->head_dim, tiles);
     return p;
 }
 
@@ -255,8 +254,7 @@ void stream_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.tile_rows = p.stream_rows;
     a.slots = p.slots;
     a.slots_per_req = p.slots_per_req;
-    a.splits = workspace ? p.splits : 1;
-    a.part = static_cast<float *>(workspace);
+    a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
 }
 
 }  // namespace

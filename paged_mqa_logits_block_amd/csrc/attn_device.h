@@ -91,6 +91,20 @@ __device__ __forceinline__ void copy16(const void *src, uint32_t lds_wave) {
         : "memory");
 }
 
+// the same with 4 bytes per lane, at lds_wave + 4 * lane
+__device__ __forceinline__ void copy4(const void *src, uint32_t lds_wave) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %2\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dword %1, off\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(src), "s"(lds_wave)
+        : "memory");
+}
+
 __device__ __forceinline__ void wait_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ uint32_t lds_offset(const void *p) {
@@ -117,12 +131,14 @@ __device__ __forceinline__ int swz_v(int row) {
 template <int DT, int D>
 __device__ __forceinline__ f32x16 score_tile(const uint8_t *kbase, const i32x4 (&q)[D / 16], int lane) {
     const int row = lane & 31, h = lane >> 5;
+    i32x4 k[D / 16];
+#pragma unroll
+    for (int c = 0; c < D / 16; ++c)
+        k[c] = *reinterpret_cast<const i32x4 *>(kbase + row * 2 * D + (((2 * c + h) ^ swz_k<D>(row)) << 4));
+    __builtin_amdgcn_sched_barrier(0);  // all reads on their way before the first product waits for one
     f32x16 s = {};
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-        const i32x4 k = *reinterpret_cast<const i32x4 *>(kbase + row * 2 * D + (((2 * c + h) ^ swz_k<D>(row)) << 4));
-        s = mfma32<DT>(k, q[c], s);
-    }
+    for (int c = 0; c < D / 16; ++c) s = mfma32<DT>(k[c], q[c], s);
     return s;
 }
 
@@ -139,24 +155,23 @@ __device__ __forceinline__ void output_tile(const uint8_t *vbase, const f32x16 &
     const int h = lane >> 5, half = (lane >> 4) & 1, i = lane & 15;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        const i32x4 b = pack8<DT>(p, 8 * t);
+        i32x4 v[D / 32];
 #pragma unroll
         for (int m = 0; m < D / 32; ++m) {
             const int chunk = 4 * m + 2 * half + ((i & 3) >> 1);
-            s16x4 v[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 const int row = 16 * t + 8 * u + 4 * h + (i >> 2);
-                v[u] = read_tr(vbase + row * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1));
+                const auto x = __builtin_bit_cast(
+                    i32x2, read_tr(vbase + row * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1)));
+                v[m][2 * u] = x[0];
+                v[m][2 * u + 1] = x[1];
             }
-            i32x4 a;
-            const auto v0 = __builtin_bit_cast(i32x2, v[0]), v1 = __builtin_bit_cast(i32x2, v[1]);
-            a[0] = v0[0];
-            a[1] = v0[1];
-            a[2] = v1[0];
-            a[3] = v1[1];
-            o[m] = mfma32<DT>(a, b, o[m]);
         }
+        const i32x4 b = pack8<DT>(p, 8 * t);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < D / 32; ++m) o[m] = mfma32<DT>(v[m], b, o[m]);
     }
 }
 
@@ -173,35 +188,39 @@ __device__ __forceinline__ int score_key(int i, int lane) { return 8 * (i >> 2) 
 struct RowTile {
     int req, row0, rows;
 };
-__device__ __forceinline__ bool find_tile(const AttnArgs &a, int slot, RowTile &t) {
-    const int n = a.num_reqs, T = a.tile_rows, lane = lane_id();
-    const auto start = [&](int i) { return min(max(a.q_starts[i], 0), a.num_rows); };
-    int lo = 0, j;
-    if (a.slots_per_req > 0) {
-        lo = slot / a.slots_per_req;
-        j = slot - lo * a.slots_per_req;
-    } else {
-        // 64-way search for the last i in [0, n) with start(i) / T + i <= slot
-        int len = n;
-        while (len > 1) {
-            const int step = (len + kWave - 1) / kWave;
-            const int off = lane * step, i = lo + off;
-            const bool le = off < len && start(i) / T + i <= slot;
-            const uint64_t b = ballot(le);
-            const int last = b ? 63 - __builtin_clzll(b) : 0;
-            lo += last * step;
-            len = min(step, len - last * step);
-        }
-        j = slot - (start(lo) / T + lo);
-    }
-    const int s0 = start(lo), s1 = start(lo + 1);
-    const int64_t row0 = (int64_t)s0 + (int64_t)j * T;
-    const int rows = s1 - s0;
+__device__ __forceinline__ int request_start(const AttnArgs &a, int i) { return min(max(a.q_starts[i], 0), a.num_rows); }
+
+// tile j of request `req`
+__device__ __forceinline__ bool request_tile(const AttnArgs &a, int req, int j, RowTile &t) {
+    const int s0 = request_start(a, req), s1 = request_start(a, req + 1), rows = s1 - s0;
+    const int64_t row0 = (int64_t)s0 + (int64_t)j * a.tile_rows;
     if (j < 0 || row0 >= s1 || rows < a.min_rows || rows > a.max_rows) return false;
-    t.req = lo;
+    t.req = req;
     t.row0 = (int)row0;
-    t.rows = min(T, s1 - (int)row0);
+    t.rows = min(a.tile_rows, s1 - (int)row0);
     return true;
+}
+// slots_per_req > 0
+__device__ __forceinline__ bool slot_tile(const AttnArgs &a, int slot, RowTile &t) {
+    const int req = slot / a.slots_per_req;
+    return request_tile(a, req, slot - req * a.slots_per_req, t);
+}
+
+__device__ __forceinline__ bool find_tile(const AttnArgs &a, int slot, RowTile &t) {
+    if (a.slots_per_req > 0) return slot_tile(a, slot, t);
+    const int T = a.tile_rows, lane = lane_id();
+    // 64-way search for the last i in [0, num_reqs) with start(i) / T + i <= slot
+    int lo = 0, len = a.num_reqs;
+    while (len > 1) {
+        const int step = (len + kWave - 1) / kWave;
+        const int off = lane * step, i = lo + off;
+        const bool le = off < len && request_start(a, i) / T + i <= slot;
+        const uint64_t b = ballot(le);
+        const int last = b ? 63 - __builtin_clzll(b) : 0;
+        lo += last * step;
+        len = min(step, len - last * step);
+    }
+    return request_tile(a, lo, slot - (request_start(a, lo) / T + lo), t);
 }
 
 __device__ __forceinline__ float wave_sum_f(float v) {

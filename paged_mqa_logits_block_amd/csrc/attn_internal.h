@@ -11,7 +11,10 @@ namespace qsa {
 constexpr int kAttnTile = 32;
 // Keys per step of a streaming wave, and waves per streaming workgroup.
 constexpr int kStreamKeys = 32;
-constexpr int kStreamWaves = 4;
+constexpr int kStreamWaves = 8;
+// Workgroups of a balanced launch (one per CU), and the most row tiles of one.
+constexpr int kStreamGroups = 256;
+constexpr int kMaxSlots = 1024;
 
 struct AttnArgs {
     const void *q;
@@ -24,7 +27,7 @@ struct AttnArgs {
     const int32_t *idx;         // sparse: [num_rows][k]
     void *out;
     float *lse;                 // or null
-    float *part;                // split partials, or null when splits == 1
+    float *part;                // workspace of a balanced launch, or null
     int32_t num_rows;
     int32_t num_kv_heads;
     int32_t group;              // query heads per kv head
@@ -46,11 +49,12 @@ struct AttnArgs {
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile
-    int32_t splits;
     int32_t min_rows, max_rows; // dense: the requests this launch takes, by their row count
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
+// bytes of a balanced launch's workspace
+int64_t attn_workspace_bytes(int head_dim, int64_t tiles);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s);
 
 struct PlanArgs {

@@ -3,18 +3,28 @@
 //
 //   o = sum_c softmax_c(scale q . k_c) v_c,  lse = log sum_c exp(scale q . k_c)
 //
-// One workgroup takes up to 32 (row, head) pairs that share a kv head and a
-// range of keys; its four waves take the range's 32-key steps in turn, each
-// with a softmax state of its own, joined in LDS at the end.  Where the row
-// tiles do not fill the chip, the keys are split over several workgroups, which
-// leave their states (32-bit maximum, sum and unnormalised output) in the
-// workspace for a joining kernel.
+// A tile is up to 32 (row, head) pairs that share a kv head.  A workgroup works
+// on one tile's keys (or a range of them) with 8 waves that take 32-key steps in
+// turn, each with a softmax state of its own, joined in LDS at the end.
 //
-// What bounds it is the cache's bytes: 32 keys and values of one head are 16 KB
-// at D = 128, against 16 MFMAs.  Each wave owns two 16 KB buffers and copies the
-// next step straight to LDS while it works on the current one, so the loads
-// need no registers and no barriers; the table entries (and selected columns)
-// behind the copies are loaded one step (two steps) further ahead.
+// What bounds it is the bytes of keys and values: a step is 16 KB at D = 128
+// against 16 MFMAs.  Each wave owns a key and a value buffer in LDS, filled
+// straight from global memory; the next step's keys are fetched as soon as the
+// scores are taken and the next values as soon as the output is, so that about
+// 128 KB are on their way to a CU at any time, without registers or barriers.
+// Table entries and selected columns reach the wave the same way, one and two
+// steps ahead.  Every load of the loop is such a copy, so the waits can count
+// them: copies complete in order, and the newest are always one buffer's.
+//
+// Balanced launches (few tiles, a workspace): the tiles' key ranges are laid end
+// to end and cut into kStreamGroups equal parts, one per workgroup and CU, so
+// requests of mixed lengths keep the whole chip busy to the end.  A tile that is
+// cut leaves its parts' states (32-bit maximum, sum, unnormalised output) in the
+// workspace and a second kernel joins them; part (workgroup, tile) has place
+// workgroup + tile, as both only grow along the line.  With many tiles each gets
+// a workgroup.
+// (A verify step of 9 requests, 16,000 to 65,600 tokens, 539 MB of cache: see the
+// figures at launch_attn_stream.)
 
 #include "attn_device.h"
 
@@ -22,6 +32,7 @@ namespace qsa {
 namespace {
 
 constexpr int kStreamThreads = 64 * kStreamWaves;
+constexpr int kUnitKeys = kStreamKeys * kStreamWaves;  // one step of every wave
 
 struct TileWork {
     int req, row0, rows;  // dense: a request's tile; sparse: one row
@@ -42,6 +53,7 @@ __device__ __forceinline__ Pair pair_of(const AttnArgs &a, const TileWork &w, in
     return p;
 }
 
+// the tile of row tile `slot` and head part `hs`; false for a slot without rows
 template <bool SPARSE>
 __device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, TileWork &w) {
     w.hk = hs / a.num_subs;
@@ -63,315 +75,475 @@ __device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, T
     return true;
 }
 
+__device__ __forceinline__ int visible(const AttnArgs &a, int row) { return min(max(a.ctx_lens[row], 0), a.cap); }
+
 // keys the tile works through: the largest visible count of its rows, or the
 // selected tokens
 template <bool SPARSE>
-__device__ __forceinline__ int visible(const AttnArgs &a, int row) {
-    if (SPARSE) return a.k * a.ratio;
-    return min(max(a.ctx_lens[row], 0), a.cap);
-}
-
-template <bool SPARSE>
-__device__ __forceinline__ int tile_keys(const AttnArgs &a, const TileWork &w) {
+__device__ __forceinline__ int tile_keys(const AttnArgs &a, int row0, int rows) {
     if (SPARSE) return a.k * a.ratio;
     int most = 0;
-    for (int r = 0; r < w.rows; ++r) most = max(most, visible<SPARSE>(a, w.row0 + r));
+    for (int r = 0; r < rows; ++r) most = max(most, visible(a, row0 + r));
     return most;
 }
 
-// 32-key steps of a split: one for each wave at least
-__device__ __forceinline__ int split_steps(int steps, int splits) {
-    return max((steps + splits - 1) / splits, kStreamWaves);
+// 8 (D = 128) or 4 copies fill a buffer; wait until at most one buffer's are
+// outstanding
+template <int N>
+__device__ __forceinline__ void wait_all_but() {
+    static_assert(N == 8 || N == 4, "copies of a buffer");
+    if constexpr (N == 8) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+    else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+}
+
+// this wave's reads of LDS are done: what they read may be overwritten by copies
+__device__ __forceinline__ void wait_reads() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+// where a cut tile's state lies in the workspace
+template <int D>
+__device__ __forceinline__ float *part_of(const AttnArgs &a, int group, int tile) {
+    return a.part + (int64_t)(group + tile) * (kAttnTile * (D + 2));
 }
 
 template <int DT, int D, bool SPARSE>
-__global__ __launch_bounds__(kStreamThreads, 1) void attn_stream_kernel(AttnArgs a) {
-    constexpr int kTileBytes = kStreamKeys * D * 2;          // keys (or values) of one step
-    constexpr int kWaveBytes = 4 * kTileBytes;               // two buffers of keys and values
-    constexpr int kCopies = kTileBytes / (16 * kWave);       // copy instructions for each of the two
-    constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
-    constexpr int kPad = D + 4;                              // floats between rows of the waves' outputs
-    __shared__ __align__(16) uint8_t ring[kStreamWaves * kWaveBytes];
-    __shared__ float top_of[kStreamWaves][kAttnTile], sum_of[kStreamWaves][kAttnTile];
+struct Stream {
+    static constexpr int kTileBytes = kStreamKeys * D * 2;  // one buffer of keys or values
+    static constexpr int kCopies = kTileBytes / (16 * kWave);
+    static constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
 
-    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int slot = blockIdx.x, hs = blockIdx.y, split = blockIdx.z;
-    TileWork w;
-    if (!tile_work<SPARSE>(a, slot, hs, w)) return;
-    const Pair pair = pair_of(a, w, lane & 31);
-    const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w));
-    const int steps = (keys + kStreamKeys - 1) / kStreamKeys;
-    const int per = a.splits > 1 ? split_steps(steps, a.splits) : steps;
-    const int t0 = min(split * per, steps), t1 = min(t0 + per, steps);
-    if (a.splits > 1 && t0 >= t1) return;
-
-    const int ctx = SPARSE ? 0 : (pair.live ? visible<SPARSE>(a, pair.row) : 0);
-    int least = 0, limit = 0;
-    if (SPARSE) {
-        limit = a.ctx_lens ? min(max(a.ctx_lens[w.row0], 0), a.cap) : a.cap;
-    } else {
-        least = keys;  // the smallest visible count: steps below it need no mask
-        for (int r = 0; r < w.rows; ++r) least = min(least, visible<SPARSE>(a, w.row0 + r));
-    }
-
-    i32x4 q[D / 16];
-    const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + pair.row * a.q_row + pair.head * a.q_head;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-        q[c] = i32x4{0, 0, 0, 0};
-        if (pair.live) q[c] = *reinterpret_cast<const i32x4 *>(qrow + 16 * c + 8 * (lane >> 5));
-    }
-
-    uint8_t *mine = ring + wave * kWaveBytes;
-    const uint32_t mine_lds = lds_offset(mine);
-    const int32_t *table = a.block_table + (int64_t)max(w.req, 0) * a.max_blocks;
-    const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
-
-    // a step's tokens, one per lane of each half wave
-    struct Token {
-        int32_t entry, in;
-        bool seen;
-    };
-    const auto load_column = [&](int s) -> int32_t {
-        if constexpr (!SPARSE) return 0;
-        const int pos = s * kStreamKeys + (lane & 31);
-        return s < t1 && pos < keys ? idx[pos / a.ratio] : -1;
-    };
-    const auto load_entry = [&](int s, int32_t column) -> Token {
-        Token k = {0, 0, false};
-        if (s >= t1) return k;
-        const int pos = s * kStreamKeys + (lane & 31);
-        uint32_t tok;
-        if constexpr (SPARSE) {
-            const int64_t wide = (int64_t)column * a.ratio + pos % a.ratio;
-            k.seen = column >= 0 && wide < limit;
-            tok = k.seen ? (uint32_t)wide : 0u;
-        } else {
-            // behind the last visible key the copies take that key again
-            k.seen = true;
-            tok = (uint32_t)min(pos, keys - 1);
-        }
-        const uint32_t e = tok / (uint32_t)a.block_size;
-        k.in = (int32_t)(tok - e * (uint32_t)a.block_size);
-        if (k.seen && w.req >= 0) k.entry = table[e];
-        if (w.req < 0) k.entry = -1;
-        return k;
-    };
-    // starts the copies of a step; returns which keys take part and which are
-    // behind table entries outside the pool
-    struct Masks {
-        uint32_t seen, bad;
-    };
-    const auto start_copies = [&](const Token &k, int buf) -> Masks {
-        Masks mk;
-        mk.seen = (uint32_t)ballot(k.seen);
-        const bool bad = k.entry < 0 || k.entry >= a.num_blocks;
-        mk.bad = (uint32_t)ballot(bad && k.seen);
-        if (SPARSE && mk.seen == 0) return mk;
-        int64_t off = (bad ? 0 : (int64_t)k.entry * a.kv_block) + (int64_t)k.in * a.kv_slot + (int64_t)w.hk * a.kv_head;
-        int lo = (int)off, hi = (int)(off >> 32);
-        if (SPARSE && mk.seen != 0xFFFFFFFFu) {  // places without a token take the first seen token's key
-            const int first = __builtin_ctz(mk.seen);
-            const int flo = readlane(lo, first), fhi = readlane(hi, first);
-            lo = k.seen ? lo : flo;
-            hi = k.seen ? hi : fhi;
-        }
-        const uint32_t lds = mine_lds + buf * 2 * kTileBytes;
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int row = i * kKeysPerCopy + lane / kLanesPerKey, chunk = lane % kLanesPerKey;
-            const int64_t at = ((int64_t)shfl_i(hi, row) << 32) | (uint32_t)shfl_i(lo, row);
-            copy16(a.kcache + 2 * (at + 8 * (chunk ^ swz_k<D>(row))), lds + i * 16 * kWave);
-            copy16(a.vcache + 2 * (at + 8 * (chunk ^ swz_v<D>(row))), lds + kTileBytes + i * 16 * kWave);
-        }
-        return mk;
+    struct Shared {
+        __align__(16) uint8_t ring[kStreamWaves][2 * kTileBytes];
+        int32_t entry[kStreamWaves][2][kWave];
+        int32_t column[kStreamWaves][2][kWave];
+        float top_of[kStreamWaves][kAttnTile], sum_of[kStreamWaves][kAttnTile];
     };
 
-    f32x16 o[D / 32] = {};
-    float m = kNegInf, l = 0.0f;  // l: this lane's half of the sum
-    int s = t0 + wave, buf = 0;
-    Masks now = {0, 0};
-    Token next;
-    int32_t column;
-    {
-        const Token first = load_entry(s, load_column(s));
-        const int32_t c1 = load_column(s + kStreamWaves);
-        if (s < t1) now = start_copies(first, 0);
-        next = load_entry(s + kStreamWaves, c1);
-        column = load_column(s + 2 * kStreamWaves);
-    }
-    for (; s < t1; s += kStreamWaves) {
-        wait_copies();
-        const Masks cur = now;
-        if (s + kStreamWaves < t1) {
-            now = start_copies(next, buf ^ 1);
-            next = load_entry(s + 2 * kStreamWaves, column);
-            column = load_column(s + 3 * kStreamWaves);
-        }
-        const uint8_t *kb = mine + buf * 2 * kTileBytes;
-        buf ^= 1;
-        if (SPARSE && cur.seen == 0) continue;
-        f32x16 z = score_tile<DT, D>(kb, q, lane);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) z[i] *= a.scale_log2;
-        if (cur.bad) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = (cur.bad >> score_key(i, lane)) & 1 ? __builtin_nanf("") : z[i];
-        }
+    // where f32 output chunk c (4 elements) of pair p lies in a wave's buffers,
+    // which hold exactly the 32 x D outputs: chunks permuted so that neither the
+    // lanes of a pair nor those of a chunk meet in one bank
+    static __device__ __forceinline__ int left_at(int p, int c) { return p * D + 4 * (c ^ (p & (D / 4 - 1))); }
+
+    // keys [32 t0, 32 t1) of tile w (of its `keys`); dest: the workspace place of
+    // the state, or null to write the outputs
+    static __device__ __forceinline__ void run(const AttnArgs &a, Shared &sh, const TileWork &w, int keys, int t0,
+                                               int t1, float *dest) {
+        int t = threadIdx.x;
+        asm volatile("" : "+v"(t));  // addresses are made anew for each range, not kept live across them
+        const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
+        const Pair pair = pair_of(a, w, lane & 31);
+        const int ctx = SPARSE ? 0 : (pair.live ? visible(a, pair.row) : 0);
+        int least = 0, limit = 0;
         if (SPARSE) {
-            if (cur.seen != 0xFFFFFFFFu) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] = (cur.seen >> score_key(i, lane)) & 1 ? z[i] : kNegInf;
-            }
-        } else if ((s + 1) * kStreamKeys > least) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[i] = s * kStreamKeys + score_key(i, lane) < ctx ? z[i] : kNegInf;
+            limit = a.ctx_lens ? visible(a, w.row0) : a.cap;
+        } else {
+            least = keys;  // the smallest visible count: steps below it need no mask
+            for (int r = 0; r < w.rows; ++r) least = min(least, visible(a, w.row0 + r));
         }
-        float top = z[0];
+        i32x4 q[D / 16];
+        const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + pair.row * a.q_row + pair.head * a.q_head;
 #pragma unroll
-        for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-        top = fmaxf(m, xor32_max(top));
-        const float ref = top == kNegInf ? 0.0f : top;
-        const float keep = __builtin_amdgcn_exp2f(m - ref);
-        m = top;
-        float sum = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            z[i] = __builtin_amdgcn_exp2f(z[i] - ref);
-            sum += z[i];
+        for (int c = 0; c < D / 16; ++c) {
+            q[c] = i32x4{0, 0, 0, 0};
+            if (pair.live) q[c] = *reinterpret_cast<const i32x4 *>(qrow + 16 * c + 8 * (lane >> 5));
+            // waited for here: the compiler would wait for them, and for every copy, in the loop
+            asm volatile("" : "+v"(q[c]));
         }
-        l = l * keep + sum;
-        if (ballot(keep != 1.0f)) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] *= keep;
-        }
-        output_tile<DT, D>(kb + kTileBytes, z, o, lane);
-    }
-    l = xor32_sum(l);
 
-    // join the waves' states: each leaves its output in its own part of the ring
-    float *left = reinterpret_cast<float *>(mine);
+        uint8_t *mine = sh.ring[wave];
+        const uint32_t mine_lds = lds_offset(mine);
+        const uint32_t entry_lds = lds_offset(sh.entry[wave]), column_lds = lds_offset(sh.column[wave]);
+        const int32_t *table = a.block_table + (int64_t)max(w.req, 0) * a.max_blocks;
+        const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
+        // the wave's step j, and this lane's place in it (both half waves alike)
+        const auto place = [&](int j) { return (t0 + wave + j * kStreamWaves) * kStreamKeys + (lane & 31); };
+        const auto have = [&](int j) { return t0 + wave + j * kStreamWaves < t1; };
+
+        struct Token {
+            uint32_t entry, in;  // table column, place in the block
+            bool seen;
+        };
+        const auto copy_column = [&](int j) {
+            const int pos = min(place(j), keys - 1);
+            copy4(idx + pos / a.ratio, column_lds + (j & 1) * 4 * kWave);
+        };
+        const auto token = [&](int j) {
+            Token k;
+            const int pos = place(j);
+            uint32_t tok;
+            if constexpr (SPARSE) {
+                const int column = sh.column[wave][j & 1][lane];
+                const int64_t wide = (int64_t)column * a.ratio + pos % a.ratio;
+                k.seen = pos < keys && column >= 0 && wide < limit;
+                tok = k.seen ? (uint32_t)wide : 0u;
+            } else {
+                // behind the last visible key the copies take that key again
+                k.seen = true;
+                tok = (uint32_t)max(min(pos, keys - 1), 0);
+            }
+            k.entry = tok / (uint32_t)a.block_size;
+            k.in = tok - k.entry * (uint32_t)a.block_size;
+            return k;
+        };
+        const auto copy_entry = [&](int j, const Token &k) {
+            copy4(table + k.entry, entry_lds + (j & 1) * 4 * kWave);
+        };
+        // byte offsets of the keys that this lane copies parts of, which keys take part, and which lie
+        // behind table entries outside the pool
+        struct Step {
+            int64_t at[kCopies];
+            uint32_t seen, bad;
+        };
+        const auto locate = [&](int j, const Token &k) {
+            Step s;
+            const int entry = sh.entry[wave][j & 1][lane];
+            const bool bad = entry < 0 || entry >= a.num_blocks || w.req < 0;
+            s.seen = (uint32_t)ballot(k.seen);
+            s.bad = (uint32_t)ballot(bad && k.seen);
+            const int64_t off =
+                2 * ((bad ? 0 : (int64_t)entry * a.kv_block) + (int64_t)k.in * a.kv_slot + (int64_t)w.hk * a.kv_head);
+            int lo = (int)off, hi = (int)(off >> 32);
+            if (SPARSE && s.seen != 0xFFFFFFFFu && s.seen != 0) {
+                // places without a token take the first seen token's key
+                const int first = __builtin_ctz(s.seen);
+                const int flo = readlane(lo, first), fhi = readlane(hi, first);
+                lo = k.seen ? lo : flo;
+                hi = k.seen ? hi : fhi;
+            }
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c)
+            for (int i = 0; i < kCopies; ++i) {
+                const int row = i * kKeysPerCopy + lane / kLanesPerKey;
+                s.at[i] = ((int64_t)shfl_i(hi, row) << 32) | (uint32_t)shfl_i(lo, row);
+            }
+            return s;
+        };
+        const auto copy_rows = [&](const uint8_t *cache, const Step &s, bool values) {
+            const uint32_t lds = mine_lds + (values ? kTileBytes : 0);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            const f32x4 v = {o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
-            *reinterpret_cast<f32x4 *>(left + (lane & 31) * kPad + 32 * c + 8 * g + 4 * (lane >> 5)) = v;
-        }
-    if (lane < kAttnTile) {
-        top_of[wave][lane] = m;
-        sum_of[wave][lane] = l;
-    }
-    __syncthreads();
-    constexpr int kPer = D / 8;  // outputs per thread: 8 threads to a pair
-    const int pm = t >> 3, d0 = (t & 7) * kPer;
-    float top = kNegInf, total = 0.0f, r[kPer];
+            for (int i = 0; i < kCopies; ++i) {
+                const int row = i * kKeysPerCopy + lane / kLanesPerKey, chunk = lane % kLanesPerKey;
+                copy16(cache + s.at[i] + 16 * (chunk ^ (values ? swz_v<D>(row) : swz_k<D>(row))),
+                       lds + i * 16 * kWave);
+            }
+        };
+
+        f32x16 o[D / 32] = {};
+        float m = kNegInf, l = 0.0f;  // l: this lane's half of the sum
+        if (have(0)) {
+            if constexpr (SPARSE) {
+                copy_column(0);
+                copy_column(1);
+                wait_copies();
+            }
+            Token k0 = token(0), next = token(1);
+            copy_entry(0, k0);
+            wait_copies();
+            Step cur = locate(0, k0), ahead = cur;
+            copy_rows(a.kcache, cur, false);
+            copy_entry(1, next);
+            if constexpr (SPARSE) copy_column(2);
+            copy_rows(a.vcache, cur, true);
+            for (int j = 0; have(j); ++j) {
+                const bool more = have(j + 1);
+                const int s = t0 + wave + j * kStreamWaves;
+                wait_all_but<kCopies>();
+                f32x16 z = score_tile<DT, D>(mine, q, lane);
+                if (more) {
+                    ahead = locate(j + 1, next);
+                    wait_reads();
+                    copy_rows(a.kcache, ahead, false);
+                }
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) r[i] = 0.0f;
+                for (int i = 0; i < 16; ++i) z[i] *= a.scale_log2;
+                if (cur.bad) {
 #pragma unroll
-    for (int i = 0; i < kStreamWaves; ++i) top = fmaxf(top, top_of[i][pm]);
-    const float ref = top == kNegInf ? 0.0f : top;
+                    for (int i = 0; i < 16; ++i) z[i] = (cur.bad >> score_key(i, lane)) & 1 ? __builtin_nanf("") : z[i];
+                }
+                if (SPARSE) {
+                    if (cur.seen != 0xFFFFFFFFu) {
 #pragma unroll
-    for (int i = 0; i < kStreamWaves; ++i) {
-        const float f = __builtin_amdgcn_exp2f(top_of[i][pm] - ref);
-        total += sum_of[i][pm] * f;
-        const float *src = reinterpret_cast<const float *>(ring + i * kWaveBytes) + pm * kPad + d0;
+                        for (int i = 0; i < 16; ++i) z[i] = (cur.seen >> score_key(i, lane)) & 1 ? z[i] : kNegInf;
+                    }
+                } else if ((s + 1) * kStreamKeys > least) {
 #pragma unroll
-        for (int j = 0; j < kPer; ++j) r[j] += src[j] * f;
-    }
-    const Pair pp = pair_of(a, w, pm);
-    if (!SPARSE && least < keys) {
-        // A NaN can come from a value that only other rows of the tile see (zero
-        // weight times a value that is not finite): then every pair is done
-        // again over its own keys.
-        bool nan = false;
+                    for (int i = 0; i < 16; ++i) z[i] = s * kStreamKeys + score_key(i, lane) < ctx ? z[i] : kNegInf;
+                }
+                float top = z[0];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
-        if (__syncthreads_or(nan && pp.live)) {
-            float *again = reinterpret_cast<float *>(ring);
-            for (int p = wave; p < kAttnTile; p += kStreamWaves) {
-                const Pair x = pair_of(a, w, p);
-                if (!x.live) continue;
-                float pm2, pl2, po[D / 64];
-                own_range<DT, D>(launch_args(), w.req, static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
-                                 w.hk, t0 * kStreamKeys, min(t1 * kStreamKeys, visible<SPARSE>(a, x.row)), pm2, pl2,
-                                 po);
-                for (int i = 0; i < D / 64; ++i) again[p * kPad + lane * (D / 64) + i] = po[i];
-                if (lane == 0) {
-                    top_of[0][p] = pm2;
-                    sum_of[0][p] = pl2;
+                for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
+                top = fmaxf(m, xor32_max(top));
+                const float ref = top == kNegInf ? 0.0f : top;
+                const float keep = __builtin_amdgcn_exp2f(m - ref);
+                m = top;
+                float sum = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    z[i] = __builtin_amdgcn_exp2f(z[i] - ref);
+                    sum += z[i];
+                }
+                l = l * keep + sum;
+                if (ballot(keep != 1.0f)) {
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) o[c] *= keep;
+                }
+                if (more) wait_all_but<kCopies>();
+                else wait_copies();
+                // a step without tokens holds the values of block 0, whatever they are
+                if (!SPARSE || cur.seen != 0) output_tile<DT, D>(mine + kTileBytes, z, o, lane);
+                if (more) {
+                    next = token(j + 2);
+                    wait_reads();
+                    copy_entry(j + 2, next);
+                    if constexpr (SPARSE) copy_column(j + 3);
+                    copy_rows(a.vcache, ahead, true);
+                    cur = ahead;
                 }
             }
-            __syncthreads();
-            top = top_of[0][pm];
-            total = sum_of[0][pm];
+            wait_copies();
+        }
+        l = xor32_sum(l);
+
+        // join the waves' states: each leaves its output in its own buffers
+        float *left = reinterpret_cast<float *>(mine);
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) r[i] = again[pm * kPad + d0 + i];
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const f32x4 v = {o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
+                *reinterpret_cast<f32x4 *>(left + left_at(lane & 31, 8 * c + 2 * g + (lane >> 5))) = v;
+            }
+        if (lane < kAttnTile) {
+            sh.top_of[wave][lane] = m;
+            sh.sum_of[wave][lane] = l;
+        }
+        __syncthreads();
+        constexpr int kThreadsPer = kStreamThreads / kAttnTile, kPer = D / kThreadsPer;  // outputs per thread
+        const int pm = t / kThreadsPer, d0 = (t % kThreadsPer) * kPer;
+        float top = kNegInf, total = 0.0f, r[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) r[i] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kStreamWaves; ++i) top = fmaxf(top, sh.top_of[i][pm]);
+        const float ref = top == kNegInf ? 0.0f : top;
+#pragma unroll
+        for (int i = 0; i < kStreamWaves; ++i) {
+            const float f = __builtin_amdgcn_exp2f(sh.top_of[i][pm] - ref);
+            total += sh.sum_of[i][pm] * f;
+            const float *src = reinterpret_cast<const float *>(sh.ring[i]);
+#pragma unroll
+            for (int j = 0; j < kPer; j += 4) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(src + left_at(pm, (d0 + j) / 4));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[j + e] += v[e] * f;
+            }
+        }
+        const Pair pp = pair_of(a, w, pm);
+        if (!SPARSE && least < keys) {
+            // A NaN can come from a value that only other rows of the tile see (zero
+            // weight times a value that is not finite): then every pair is done
+            // again over its own keys.
+            bool nan = false;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
+            if (__syncthreads_or(nan && pp.live)) {
+                float *again = reinterpret_cast<float *>(sh.ring[0]);
+                for (int p = wave; p < kAttnTile; p += kStreamWaves) {
+                    const Pair x = pair_of(a, w, p);
+                    if (!x.live) continue;
+                    float pm2, pl2, po[D / 64];
+                    own_range<DT, D>(launch_args(), w.req,
+                                     static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head, w.hk,
+                                     t0 * kStreamKeys, min(t1 * kStreamKeys, visible(a, x.row)), pm2, pl2, po);
+                    for (int i = 0; i < D / 64; ++i) again[p * D + lane * (D / 64) + i] = po[i];
+                    if (lane == 0) {
+                        sh.top_of[0][p] = pm2;
+                        sh.sum_of[0][p] = pl2;
+                    }
+                }
+                __syncthreads();
+                top = sh.top_of[0][pm];
+                total = sh.sum_of[0][pm];
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) r[i] = again[pm * D + d0 + i];
+            }
+        }
+        if (pp.live && dest) {
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4)
+                *reinterpret_cast<f32x4 *>(dest + pm * D + d0 + i) = f32x4{r[i], r[i + 1], r[i + 2], r[i + 3]};
+            if (d0 == 0) {
+                dest[kAttnTile * D + pm] = top;
+                dest[kAttnTile * (D + 1) + pm] = total;
+            }
+        } else if (pp.live) {
+            const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+            typedef typename Half<DT>::T T;
+            typedef T V4 __attribute__((ext_vector_type(4)));
+            T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + d0;
+#pragma unroll
+            for (int i = 0; i < kPer; i += 4) {
+                V4 v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = (T)(r[i + j] * inv);
+                *reinterpret_cast<V4 *>(out + i) = v;
+            }
+            if (a.lse && d0 == 0)
+                a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] =
+                    (top + __builtin_amdgcn_logf(total)) * kLn2;
         }
     }
-    if (!pp.live) return;
-    if (a.splits > 1) {
-        float *part = a.part + ((int64_t)(slot * gridDim.y + hs) * a.splits + split) * (kAttnTile * (D + 2));
-#pragma unroll
-        for (int i = 0; i < kPer; i += 4)
-            *reinterpret_cast<f32x4 *>(part + pm * D + d0 + i) = f32x4{r[i], r[i + 1], r[i + 2], r[i + 3]};
-        if ((t & 7) == 0) {
-            part[kAttnTile * D + pm] = top;
-            part[kAttnTile * (D + 1) + pm] = total;
-        }
-        return;
-    }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    typedef typename Half<DT>::T T;
-    T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + d0;
-#pragma unroll
-    for (int i = 0; i < kPer; i += 8) {
-        typename Half<DT>::V8 v;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = (T)(r[i + j] * inv);
-        *reinterpret_cast<i32x4 *>(out + i) = __builtin_bit_cast(i32x4, v);
-    }
-    if (a.lse && (t & 7) == 0)
-        a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
+};
+
+// one workgroup per tile
+template <int DT, int D, bool SPARSE>
+__global__ __launch_bounds__(kStreamThreads, 2) void attn_stream_kernel(AttnArgs a) {
+    typedef Stream<DT, D, SPARSE> S;
+    __shared__ typename S::Shared sh;
+    TileWork w;
+    if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
+    const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w.row0, w.rows));
+    S::run(a, sh, w, keys, 0, (keys + kStreamKeys - 1) / kStreamKeys, nullptr);
 }
 
-// Joins the splits' states, one wave to a pair: lane i reads split i's maximum
-// and sum, and the outputs are read 8 splits at a time, D / 64 elements per lane.
+// Work in units of kUnitKeys keys: a tile with rows has one at least, so that
+// rows that see nothing are written too.
+__device__ __forceinline__ int units_of(int keys) { return max((keys + kUnitKeys - 1) / kUnitKeys, 1); }
+
+// the workgroups that the line of `total` units is cut for: each has one at least
+__device__ __forceinline__ int groups_of(int64_t total) { return (int)min(total, (int64_t)kStreamGroups); }
+// the first unit of workgroup g, and the workgroup that has unit u: the last g with
+// first_unit(g) <= u
+__device__ __forceinline__ int64_t first_unit(int g, int64_t total) { return g * total / groups_of(total); }
+__device__ __forceinline__ int group_of(int64_t u, int64_t total) {
+    return (int)(((u + 1) * groups_of(total) + total - 1) / total) - 1;
+}
+
+// Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
+// units of a slot are the same for every hs.
+template <int DT, int D, bool SPARSE>
+__global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnArgs a) {
+    typedef Stream<DT, D, SPARSE> S;
+    __shared__ typename S::Shared sh;
+    __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
+    __shared__ int32_t wave_sums[kStreamWaves];
+    const int t = threadIdx.x, lane = t & 63, g = blockIdx.x;
+    const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
+    if (SPARSE) {
+        const int u = units_of(a.k * a.ratio);
+        for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
+    } else {
+        constexpr int kPer = kMaxSlots / kStreamThreads;
+        int u[kPer], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const int slot = t * kPer + i;
+            RowTile w;
+            u[i] = slot < slots && slot_tile(a, slot, w) ? units_of(tile_keys<false>(a, w.row0, w.rows)) : 0;
+            sum += u[i];
+        }
+        const int inc = wave_incl_sum(sum);
+        if (lane == 63) wave_sums[t >> 6] = inc;
+        __syncthreads();
+        int at = inc - sum;
+        for (int i = 0; i < (t >> 6); ++i) at += wave_sums[i];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (t * kPer + i <= slots) before[t * kPer + i] = at;
+            at += u[i];
+        }
+        if (t == kStreamThreads - 1 && slots == kMaxSlots) before[slots] = at;
+    }
+    __syncthreads();
+    const int per_head = before[slots];
+    const int64_t total = (int64_t)per_head * hss;
+    if (g >= groups_of(total)) return;
+    if (g == 0) {  // which workgroups have parts of each tile
+        int2 *spans = reinterpret_cast<int2 *>(part_of<D>(a, kStreamGroups, slots * hss));
+        for (int i = t; i < slots * hss; i += kStreamThreads) {
+            const int hs = i / slots, slot = i - hs * slots;
+            const int64_t u0 = (int64_t)hs * per_head + before[slot], u1 = (int64_t)hs * per_head + before[slot + 1];
+            int2 s;
+            s.x = u1 > u0 ? group_of(u0, total) : 0;
+            s.y = u1 > u0 ? group_of(u1 - 1, total) : 0;
+            spans[i] = s;
+        }
+    }
+    int64_t u = first_unit(g, total);
+    const int64_t end = first_unit(g + 1, total);
+    while (u < end) {
+        const int hs = __builtin_amdgcn_readfirstlane((int)(u / per_head));
+        const int in_head = (int)(u - (int64_t)hs * per_head);
+        int slot = 0, hi = slots;  // the slot with before[slot] <= in_head < before[slot + 1]
+        while (hi - slot > 1) {
+            const int mid = (slot + hi) >> 1;
+            if (before[mid] <= in_head) slot = mid;
+            else hi = mid;
+        }
+        slot = __builtin_amdgcn_readfirstlane(slot);
+        const int64_t tile0 = (int64_t)hs * per_head + before[slot], tile1 = (int64_t)hs * per_head + before[slot + 1];
+        const int64_t stop = min(end, tile1);
+        TileWork w;
+        tile_work<SPARSE>(a, slot, hs, w);
+        const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w.row0, w.rows));
+        const int steps = (keys + kStreamKeys - 1) / kStreamKeys;
+        const int t0 = __builtin_amdgcn_readfirstlane((int)(u - tile0) * kStreamWaves);
+        const int t1 = __builtin_amdgcn_readfirstlane(min((int)(stop - tile0) * kStreamWaves, steps));
+        float *dest = u == tile0 && stop == tile1 ? nullptr : part_of<D>(a, g, hs * slots + slot);
+        S::run(a, sh, w, keys, t0, t1, dest);
+        u = stop;
+        __syncthreads();  // the joined states have been read before the next copies land
+    }
+}
+
+// Joins the parts of a cut tile, one wave to a pair: lane i reads the maxima and
+// sums of parts i, i + 64, ..., and the outputs are read 8 parts at a time, D / 64
+// elements per lane.
 constexpr int kJoinPairs = 4;
 
 template <int DT, int D, bool SPARSE>
 __global__ __launch_bounds__(64 * kJoinPairs) void attn_join_kernel(AttnArgs a) {
-    constexpr int kPer = D / 64, kBatch = 8;
+    constexpr int kPer = D / 64, kBatch = 8, kRounds = kStreamGroups / kWave, kPart = kAttnTile * (D + 2);
     typedef float Vec __attribute__((ext_vector_type(kPer)));
+    const int slot = blockIdx.x, hs = blockIdx.y, slots = a.slots, tile = hs * slots + slot;
     TileWork w;
-    if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
+    const bool rows = tile_work<SPARSE>(a, slot, hs, w);
+    const int2 span = reinterpret_cast<const int2 *>(part_of<D>(a, kStreamGroups, slots * gridDim.y))[tile];
     const int lane = threadIdx.x & 63;
     const int pm = __builtin_amdgcn_readfirstlane(blockIdx.z * kJoinPairs + (threadIdx.x >> 6));
+    if (!rows || span.y <= span.x) return;
     const Pair pp = pair_of(a, w, pm);
     if (!pp.live) return;
-    const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w));
-    constexpr int kPart = kAttnTile * (D + 2);
-    const float *part = a.part + (int64_t)(blockIdx.x * gridDim.y + blockIdx.y) * a.splits * kPart;
-    const int steps = (keys + kStreamKeys - 1) / kStreamKeys, per = split_steps(steps, a.splits);
-    const int used = (steps + per - 1) / per;
-    float m = kNegInf, l = 0.0f;
-    if (lane < used) {
-        m = part[lane * kPart + kAttnTile * D + pm];
-        l = part[lane * kPart + kAttnTile * (D + 1) + pm];
+    const float *part = part_of<D>(a, span.x, tile);
+    const int used = __builtin_amdgcn_readfirstlane(span.y - span.x + 1);
+    float m[kRounds], l[kRounds], top = kNegInf, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) {
+        const int p = i * kWave + lane;
+        m[i] = kNegInf;
+        l[i] = 0.0f;
+        if (p < used) {
+            m[i] = part[p * kPart + kAttnTile * D + pm];
+            l[i] = part[p * kPart + kAttnTile * (D + 1) + pm];
+        }
+        top = fmaxf(top, m[i]);
     }
-    const float top = wave_max_f(m), ref = top == kNegInf ? 0.0f : top;
-    const float f = __builtin_amdgcn_exp2f(m - ref);
-    const float total = wave_sum_f(l * f);
+    top = wave_max_f(top);
+    const float ref = top == kNegInf ? 0.0f : top;
     Vec r = {};
     const float *src = part + pm * D + kPer * lane;
-    for (int i = 0; i < used; i += kBatch) {
-        Vec v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const Vec *>(src + min(i + j, used - 1) * kPart);
+    for (int i = 0; i < kRounds; ++i) {
+        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
+        total += l[i] * f;
+        for (int b = i * kWave; b < min(used, (i + 1) * kWave); b += kBatch) {
+            Vec v[kBatch];
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j)
-            if (i + j < used) r += v[j] * readlane_f(f, i + j);
+            for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const Vec *>(src + min(b + j, used - 1) * kPart);
+#pragma unroll
+            for (int j = 0; j < kBatch; ++j)
+                if (b + j < used) r += v[j] * readlane_f(f, b + j - i * kWave);
+        }
     }
+    total = wave_sum_f(total);
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     typedef typename Half<DT>::T T;
     T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + kPer * lane;
@@ -384,11 +556,16 @@ __global__ __launch_bounds__(64 * kJoinPairs) void attn_join_kernel(AttnArgs a) 
 template <int DT, int D, bool SPARSE>
 hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     const unsigned heads = (unsigned)(a.num_kv_heads * a.num_subs);
-    hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE>), dim3((unsigned)a.slots, heads, (unsigned)a.splits),
-                       dim3(kStreamThreads), 0, s, a);
-    if (a.splits > 1)
-        hipLaunchKernelGGL((attn_join_kernel<DT, D, SPARSE>),
-                           dim3((unsigned)a.slots, heads, kAttnTile / kJoinPairs), dim3(64 * kJoinPairs), 0, s, a);
+    if (!a.part) {
+        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
+                           0, s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((attn_balanced_kernel<DT, D, SPARSE>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attn_join_kernel<DT, D, SPARSE>), dim3((unsigned)a.slots, heads, kAttnTile / kJoinPairs),
+                       dim3(64 * kJoinPairs), 0, s, a);
     return hipGetLastError();
 }
 
@@ -402,6 +579,10 @@ hipError_t run_dim(const AttnArgs &a, bool sparse, hipStream_t s) {
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s) {
     return a.dtype == kBF16 ? run_dim<kBF16>(a, sparse, s) : run_dim<kFP16>(a, sparse, s);
+}
+
+int64_t attn_workspace_bytes(int head_dim, int64_t tiles) {
+    return (kStreamGroups + tiles) * (kAttnTile * (head_dim + 2) * 4) + 8 * tiles;
 }
 
 }  // namespace qsa
