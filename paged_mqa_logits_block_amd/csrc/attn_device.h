@@ -178,6 +178,41 @@ __device__ __forceinline__ void output_tile(const uint8_t *vbase, const f32x16 &
 // the key (0..31) that register i of a score tile holds in this lane
 __device__ __forceinline__ int score_key(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
+// One step of a pair's softmax over U score tiles: the weights
+// 2^(c z - ref) in place of the scores z (c = scale log2 e), their sum added to
+// `total`.  `ref` (in log2 units, -inf before the first key) is a value near the
+// running maximum: it follows the maximum only where that has risen by more than
+// 8, for then every weight is still below 2^8 and the outputs need no rescaling
+// in most steps (with the exact maximum some of a wave's 32 pairs rises in nearly
+// every step).  Sums and outputs are relative to ref throughout, so it cancels.
+template <int U, int N>
+__device__ __forceinline__ void softmax_step(f32x16 (&z)[U], float c, float &ref, float &total, f32x16 (&o)[N]) {
+    float top = z[0][0];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, z[u][i]);
+    top = xor32_max(top) * c;
+    if (ballot(top > ref + 8.0f)) {
+        const float next = fmaxf(ref, top);
+        const float keep = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
+        ref = next;
+        total *= keep;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] *= keep;
+    }
+    const float use = ref == kNegInf ? 0.0f : -ref;
+    float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            z[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[u][i], c, use));
+            sum[i & 1] += z[u][i];
+        }
+    total += sum[0] + sum[1];
+}
+
 // The request that takes row tile `slot`, and the tile's first row: request i,
 // rows [s_i, s_{i+1}), owns the slots from s_i / T + i on.  These are strictly
 // increasing in i and leave room for ceil(len / T) tiles each, so no prefix sum

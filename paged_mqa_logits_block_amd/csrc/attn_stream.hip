@@ -145,8 +145,6 @@ struct Stream {
         for (int c = 0; c < D / 16; ++c) {
             q[c] = i32x4{0, 0, 0, 0};
             if (pair.live) q[c] = *reinterpret_cast<const i32x4 *>(qrow + 16 * c + 8 * (lane >> 5));
-            // waited for here: the compiler would wait for them, and for every copy, in the loop
-            asm volatile("" : "+v"(q[c]));
         }
 
         uint8_t *mine = sh.ring[wave];
@@ -237,6 +235,10 @@ struct Stream {
             Token k0 = token(0), next = token(1);
             copy_entry(0, k0);
             wait_copies();
+            // q is waited for here: the compiler would wait for it, and with it for
+            // every copy, in the loop
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) asm volatile("" : "+v"(q[c]));
             Step cur = locate(0, k0), ahead = cur;
             copy_rows(a.kcache, cur, false);
             copy_entry(1, next);
@@ -246,49 +248,31 @@ struct Stream {
                 const bool more = have(j + 1);
                 const int s = t0 + wave + j * kStreamWaves;
                 wait_all_but<kCopies>();
-                f32x16 z = score_tile<DT, D>(mine, q, lane);
+                f32x16 z[1] = {score_tile<DT, D>(mine, q, lane)};
                 if (more) {
                     ahead = locate(j + 1, next);
                     wait_reads();
                     copy_rows(a.kcache, ahead, false);
                 }
-#pragma unroll
-                for (int i = 0; i < 16; ++i) z[i] *= a.scale_log2;
                 if (cur.bad) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = (cur.bad >> score_key(i, lane)) & 1 ? __builtin_nanf("") : z[i];
+                    for (int i = 0; i < 16; ++i)
+                        z[0][i] = (cur.bad >> score_key(i, lane)) & 1 ? __builtin_nanf("") : z[0][i];
                 }
                 if (SPARSE) {
                     if (cur.seen != 0xFFFFFFFFu) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) z[i] = (cur.seen >> score_key(i, lane)) & 1 ? z[i] : kNegInf;
+                        for (int i = 0; i < 16; ++i) z[0][i] = (cur.seen >> score_key(i, lane)) & 1 ? z[0][i] : kNegInf;
                     }
                 } else if ((s + 1) * kStreamKeys > least) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[i] = s * kStreamKeys + score_key(i, lane) < ctx ? z[i] : kNegInf;
+                    for (int i = 0; i < 16; ++i) z[0][i] = s * kStreamKeys + score_key(i, lane) < ctx ? z[0][i] : kNegInf;
                 }
-                float top = z[0];
-#pragma unroll
-                for (int i = 1; i < 16; ++i) top = fmaxf(top, z[i]);
-                top = fmaxf(m, xor32_max(top));
-                const float ref = top == kNegInf ? 0.0f : top;
-                const float keep = __builtin_amdgcn_exp2f(m - ref);
-                m = top;
-                float sum = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    z[i] = __builtin_amdgcn_exp2f(z[i] - ref);
-                    sum += z[i];
-                }
-                l = l * keep + sum;
-                if (ballot(keep != 1.0f)) {
-#pragma unroll
-                    for (int c = 0; c < D / 32; ++c) o[c] *= keep;
-                }
+                softmax_step(z, a.scale_log2, m, l, o);
                 if (more) wait_all_but<kCopies>();
                 else wait_copies();
                 // a step without tokens holds the values of block 0, whatever they are
-                if (!SPARSE || cur.seen != 0) output_tile<DT, D>(mine + kTileBytes, z, o, lane);
+                if (!SPARSE || cur.seen != 0) output_tile<DT, D>(mine + kTileBytes, z[0], o, lane);
                 if (more) {
                     next = token(j + 2);
                     wait_reads();

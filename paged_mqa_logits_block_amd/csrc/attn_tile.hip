@@ -135,10 +135,6 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
         f32x16 z[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) z[u] = score_tile<DT, D>(kb + u * kStepBytes / 2, q, lane);
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) z[u][i] *= a.scale_log2;
         uint64_t bad = 0;
 #pragma unroll
         for (int i = 0; i < kTileKeys / kKeysPerCopy; ++i)
@@ -157,28 +153,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
                 for (int i = 0; i < 16; ++i)
                     z[u][i] = s * kTileKeys + 32 * u + score_key(i, lane) < ctx ? z[u][i] : kNegInf;
         }
-        float mx = z[0][0];
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, z[u][i]);
-        mx = fmaxf(top, xor32_max(mx));
-        const float ref = mx == kNegInf ? 0.0f : mx;
-        const float keep = __builtin_amdgcn_exp2f(top - ref);
-        top = mx;
-        float sum = 0.0f;
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                z[u][i] = __builtin_amdgcn_exp2f(z[u][i] - ref);
-                sum += z[u][i];
-            }
-        total = total * keep + sum;
-        if (ballot(keep != 1.0f)) {
-#pragma unroll
-            for (int c = 0; c < D / 32; ++c) o[c] *= keep;
-        }
+        softmax_step(z, a.scale_log2, top, total, o);
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             output_tile<DT, D>(kb + kStepBytes + u * kStepBytes / 2, z[u], o, lane);
