@@ -197,9 +197,9 @@ qsa_status check_attn(const void *q, const void *kcache, const void *vcache, con
         return fail(QSA_E_RANGE, "max_blocks * block_size = %lld > 2^30", (long long)s->max_blocks * s->block_size);
     if (sparse && (int64_t)k * ratio > (1 << 24))
         return fail(QSA_E_RANGE, "k * ratio = %lld > 2^24", (long long)k * ratio);
-    const int64_t most = (int64_t)1 << 38;
+    const int64_t most = (int64_t)1 << 34;
     if (s->num_blocks > ((int64_t)1 << 50) || s->kv_block_stride > ((int64_t)1 << 50) / s->num_blocks ||
-        s->kv_slot_stride > most || s->kv_head_stride > most || s->q_row_stride > most || s->q_head_stride > most ||
+        s->kv_block_stride > most || s->kv_slot_stride > most || s->kv_head_stride > most || s->q_row_stride > most || s->q_head_stride > most ||
         s->out_row_stride > most || s->out_head_stride > most)
         return fail(QSA_E_RANGE, "a stride or the cache is too large");
     if (s->num_rows > 0 && (!aligned16(q) || !aligned16(kcache) || !aligned16(vcache) || !aligned16(out)))
@@ -242,9 +242,13 @@ qsa::AttnArgs attn_args(const void *q, const void *kcache, const void *vcache, c
     a.q_head = s->q_head_stride;
     a.o_row = s->out_row_stride;
     a.o_head = s->out_head_stride;
-    a.kv_block = s->kv_block_stride;
-    a.kv_slot = s->kv_slot_stride;
-    a.kv_head = s->kv_head_stride;
+    a.kv_block = (uint32_t)(s->kv_block_stride / 8);
+    a.kv_slot = (uint32_t)(s->kv_slot_stride / 8);
+    a.kv_head = (uint32_t)(s->kv_head_stride / 8);
+    int bits = 0;
+    while ((1 << bits) < s->block_size) ++bits;
+    a.div_shift = bits > 0 ? bits - 1 : 0;
+    a.div_mul = (uint32_t)((((uint64_t)1 << (31 + a.div_shift)) + s->block_size - 1) / s->block_size);
     return a;
 }
 

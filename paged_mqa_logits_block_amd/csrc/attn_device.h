@@ -91,6 +91,20 @@ __device__ __forceinline__ void copy16(const void *src, uint32_t lds_wave) {
         : "memory");
 }
 
+// the same from base + off, base wave-uniform
+__device__ __forceinline__ void copy16(const uint8_t *base, uint32_t off, uint32_t lds_wave) {
+    uint32_t saved;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\t"
+        "s_mov_b32 m0, %3\n\t"
+        "s_nop 0\n\t"
+        "global_load_lds_dwordx4 %1, %2\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(saved)
+        : "v"(off), "s"(base), "s"(lds_wave)
+        : "memory");
+}
+
 // the same with 4 bytes per lane, at lds_wave + 4 * lane
 __device__ __forceinline__ void copy4(const void *src, uint32_t lds_wave) {
     uint32_t saved;
@@ -148,26 +162,40 @@ __device__ __forceinline__ s16x4 read_tr(const uint8_t *p) {
     return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)p);
 }
 
+// The output element (0..D - 1) of register i of output tile m: the tile's rows 0..15
+// are elements of the lower half of the head, rows 16..31 of the upper half, so
+// that the two 16-lane groups that read V together read different banks.
+template <int D>
+__device__ __forceinline__ int out_element(int m, int i, int lane) {
+    return D / 2 * (i >> 3) + 16 * m + 8 * ((i >> 2) & 1) + 4 * (lane >> 5) + (i & 3);
+}
+
+// V^T operands of 16 keys (rows `row0` on of the LDS rows at vbase), output tiles 0.. D / 32 - 1
+template <int D>
+__device__ __forceinline__ void read_values(const uint8_t *vbase, int row0, i32x4 (&v)[D / 32], int lane) {
+    const int h = lane >> 5, half = (lane >> 4) & 1, i = lane & 15;
+#pragma unroll
+    for (int m = 0; m < D / 32; ++m) {
+        const int chunk = D / 16 * half + 2 * m + ((i & 3) >> 1);
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int row = 8 * u + 4 * h + (i >> 2);  // swz_v depends on the low bits only
+            const auto x = __builtin_bit_cast(
+                i32x2, read_tr(vbase + (row0 + row) * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1)));
+            v[m][2 * u] = x[0];
+            v[m][2 * u + 1] = x[1];
+        }
+    }
+}
+
 // O^T += V^T P^T over 32 keys (LDS rows from vbase), p the weights of score_tile's
 // layout
 template <int DT, int D>
 __device__ __forceinline__ void output_tile(const uint8_t *vbase, const f32x16 &p, f32x16 (&o)[D / 32], int lane) {
-    const int h = lane >> 5, half = (lane >> 4) & 1, i = lane & 15;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         i32x4 v[D / 32];
-#pragma unroll
-        for (int m = 0; m < D / 32; ++m) {
-            const int chunk = 4 * m + 2 * half + ((i & 3) >> 1);
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int row = 16 * t + 8 * u + 4 * h + (i >> 2);
-                const auto x = __builtin_bit_cast(
-                    i32x2, read_tr(vbase + row * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1)));
-                v[m][2 * u] = x[0];
-                v[m][2 * u + 1] = x[1];
-            }
-        }
+        read_values<D>(vbase, 16 * t, v, lane);
         const i32x4 b = pack8<DT>(p, 8 * t);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -211,6 +239,16 @@ __device__ __forceinline__ void softmax_step(f32x16 (&z)[U], float c, float &ref
             sum[i & 1] += z[u][i];
         }
     total += sum[0] + sum[1];
+}
+
+// tok / block_size for tok < 2^30 (see AttnArgs)
+__device__ __forceinline__ uint32_t block_index(const AttnArgs &a, uint32_t tok) {
+    return __umulhi(2 * tok, a.div_mul) >> a.div_shift;
+}
+
+// byte offset of place `in` of pool block `block`, kv head hk
+__device__ __forceinline__ int64_t kv_offset(const AttnArgs &a, uint32_t block, uint32_t in, int hk) {
+    return (int64_t)(((uint64_t)block * a.kv_block + (uint64_t)in * a.kv_slot + (uint64_t)(uint32_t)hk * a.kv_head) << 4);
 }
 
 // The request that takes row tile `slot`, and the tile's first row: request i,
@@ -288,10 +326,11 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
         float s = kNegInf;
         int64_t off = 0;
         if (key < k1) {
-            const int e = a.block_table[(int64_t)req * a.max_blocks + key / a.block_size];
+            const uint32_t at = block_index(a, (uint32_t)key);
+            const int e = a.block_table[(int64_t)req * a.max_blocks + at];
             const bool bad = e < 0 || e >= a.num_blocks;
-            off = (bad ? 0 : (int64_t)e * a.kv_block) + (int64_t)(key % a.block_size) * a.kv_slot + hk * a.kv_head;
-            const uint16_t *k = reinterpret_cast<const uint16_t *>(a.kcache) + off;
+            off = kv_offset(a, bad ? 0 : e, (uint32_t)key - at * (uint32_t)a.block_size, hk);
+            const uint16_t *k = reinterpret_cast<const uint16_t *>(a.kcache + off);
             float dot = 0.0f;
             for (int d = 0; d < D; ++d) dot += to_f32<DT>(q[d]) * to_f32<DT>(k[d]);
             s = bad ? __builtin_nanf("") : dot * a.scale_log2;
@@ -305,7 +344,7 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
         for (int j = 0; j < min(kWave, k1 - base); ++j) {
             const float pj = readlane_f(p, j);
             const int64_t oj = ((int64_t)readlane((int)(off >> 32), j) << 32) | (uint32_t)readlane((int)off, j);
-            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache) + oj;
+            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache + oj);
             for (int i = 0; i < D / 64; ++i) o[i] += pj * to_f32<DT>(v[lane * (D / 64) + i]);
         }
     }

@@ -42,7 +42,12 @@ struct AttnArgs {
     int64_t num_blocks;
     int64_t q_row, q_head;      // strides in elements
     int64_t o_row, o_head;
-    int64_t kv_block, kv_slot, kv_head;
+    uint32_t kv_block, kv_slot, kv_head;  // strides in 16 bytes
+    // tok / block_size = high word of (2 tok) div_mul, shifted right by div_shift: with
+    // l = ceil(log2 block_size), div_shift = max(l - 1, 0) and
+    // div_mul = ceil(2^(31 + div_shift) / block_size), exact for tok < 2^30
+    uint32_t div_mul;
+    int32_t div_shift;
     // launch shape
     int32_t slots;              // row tiles of the grid
     int32_t slots_per_req;      // dense: > 0 where every request has that many

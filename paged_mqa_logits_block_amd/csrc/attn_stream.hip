@@ -178,7 +178,7 @@ struct Stream {
                 k.seen = true;
                 tok = (uint32_t)max(min(pos, keys - 1), 0);
             }
-            k.entry = tok / (uint32_t)a.block_size;
+            k.entry = block_index(a, tok);
             k.in = tok - k.entry * (uint32_t)a.block_size;
             return k;
         };
@@ -197,8 +197,7 @@ struct Stream {
             const bool bad = entry < 0 || entry >= a.num_blocks || w.req < 0;
             s.seen = (uint32_t)ballot(k.seen);
             s.bad = (uint32_t)ballot(bad && k.seen);
-            const int64_t off =
-                2 * ((bad ? 0 : (int64_t)entry * a.kv_block) + (int64_t)k.in * a.kv_slot + (int64_t)w.hk * a.kv_head);
+            const int64_t off = kv_offset(a, bad ? 0 : entry, k.in, w.hk);
             int lo = (int)off, hi = (int)(off >> 32);
             if (SPARSE && s.seen != 0xFFFFFFFFu && s.seen != 0) {
                 // places without a token take the first seen token's key
@@ -293,7 +292,7 @@ struct Stream {
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
                 const f32x4 v = {o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
-                *reinterpret_cast<f32x4 *>(left + left_at(lane & 31, 8 * c + 2 * g + (lane >> 5))) = v;
+                *reinterpret_cast<f32x4 *>(left + left_at(lane & 31, out_element<D>(c, 4 * g, lane) / 4)) = v;
             }
         if (lane < kAttnTile) {
             sh.top_of[wave][lane] = m;
