@@ -116,13 +116,18 @@ constexpr int kSmallBatch = 512;
 // Tiles up to which a streamed launch cuts the keys into equal parts; with more,
 // every tile's workgroup takes all of its keys.
 constexpr int kBalancedTiles = 2048;
+// The same for the tile kernel, and the rows up to which its workgroups find their
+// parts (each reads every row's visible count).
+constexpr int kBalancedBig = 1024, kBalancedRows = 8192;
 
 struct AttnPlan {
     int sub_heads, num_subs, stream_rows;  // heads per workgroup, workgroups per kv head, rows per streaming tile
     int few_rows;                          // requests of up to this many rows are streamed
     int slots, slots_per_req;
+    int tile_rows, tile_slots;             // the same of the tile kernel
     bool stream, tile;
-    int64_t bytes;                         // workspace, 0: none used
+    int64_t stream_bytes, tile_bytes;      // workspace, 0: none used
+    int64_t bytes() const { return stream_bytes > tile_bytes ? stream_bytes : tile_bytes; }
 };
 
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
@@ -156,7 +161,22 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     const int64_t tiles = (int64_t)p.slots * s->num_kv_heads * p.num_subs;
     if (p.stream && tiles > 0 && tiles <= kBalancedTiles && p.slots <= qsa::kMaxSlots &&
         (sparse || p.slots_per_req) && keys > qsa::kStreamKeys * qsa::kStreamWaves)
-        p.bytes = qsa::attn_workspace_bytes(s->head_dim, tiles);
+        p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, tiles);
+    if (p.tile) {
+        p.tile_rows = 256 / group;
+        p.tile_slots = s->num_rows / p.tile_rows + s->num_reqs;
+        const int64_t all = (int64_t)p.tile_slots * s->num_kv_heads;
+        // One request's tiles are nearly alike: they are cut only where whole ones would
+        // leave more than 15% of the CUs' time unused (256 tiles: 515 us whole, 555 + 28
+        // cut).  Requests of several lengths are cut up to kBalancedBig tiles (104 tiles
+        // of 17 requests: 92 us whole, 39 + 13 cut).
+        const int64_t tiles = (int64_t)((s->num_rows + p.tile_rows - 1) / p.tile_rows) * s->num_kv_heads;
+        const int64_t rounds = (tiles + qsa::kStreamGroups - 1) / qsa::kStreamGroups;
+        const bool uneven = s->num_reqs > 1 || tiles * 100 < rounds * qsa::kStreamGroups * 85;
+        if (uneven && all <= kBalancedBig && p.tile_slots <= qsa::kMaxSlots && s->num_reqs <= qsa::kMaxSlots &&
+            s->num_rows <= kBalancedRows)
+            p.tile_bytes = qsa::attn_tile_workspace_bytes(s->head_dim, all);
+    }
     return p;
 }
 
@@ -258,7 +278,7 @@ void stream_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.tile_rows = p.stream_rows;
     a.slots = p.slots;
     a.slots_per_req = p.slots_per_req;
-    a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.part = p.stream_bytes > 0 ? static_cast<float *>(workspace) : nullptr;
 }
 
 }  // namespace
@@ -320,7 +340,7 @@ qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, 
 
 int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *s) {
     if (!s || s->num_rows <= 0 || s->num_reqs < 1 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads) return 0;
-    return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes;
+    return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes();
 }
 
 qsa_status qsa_paged_attention_check(const void *q, const void *kcache, const void *vcache,
@@ -346,8 +366,9 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
     hipError_t e = hipSuccess;
     if (p.tile) {
         qsa::AttnArgs b = a;
-        b.tile_rows = 256 / b.group;
-        b.slots = s->num_rows / b.tile_rows + s->num_reqs;
+        b.tile_rows = p.tile_rows;
+        b.slots = p.tile_slots;
+        b.part = p.tile_bytes > 0 ? static_cast<float *>(workspace) : nullptr;
         b.min_rows = p.stream ? p.few_rows + 1 : 1;
         b.max_rows = s->num_rows;
         e = qsa::launch_attn_tile(b, static_cast<hipStream_t>(stream));
@@ -363,7 +384,7 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
 
 int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *s, int32_t k, int32_t ratio) {
     if (!s || s->num_rows <= 0 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads || k < 1 || ratio < 1) return 0;
-    return plan_attn(s, true, (int64_t)k * ratio).bytes;
+    return plan_attn(s, true, (int64_t)k * ratio).bytes();
 }
 
 qsa_status qsa_sparse_attention_check(const void *q, const void *kcache, const void *vcache,

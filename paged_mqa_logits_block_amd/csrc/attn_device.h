@@ -350,4 +350,53 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
     }
 }
 
+// Joins the parts of a cut tile for one pair, D / 4 threads to a pair with 4 output
+// elements each: the parts' states (outputs [PAIRS][D], references, sums) are read 8
+// parts at a time, all of a batch on their way at once.  Part 0 is at p0, part i at
+// p1 + (i - 1) stride.
+template <int DT, int D, int PAIRS>
+__device__ __forceinline__ void join_parts(const float *p0, const float *p1, int64_t stride, int used, int m, int d0,
+                                           typename Half<DT>::T *out, float *lse) {
+    constexpr int kBatch = 8;
+    typedef typename Half<DT>::T T;
+    typedef T V4 __attribute__((ext_vector_type(4)));
+    float top = kNegInf, total = 0.0f;
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < used; i += kBatch) {
+        float ref[kBatch], l[kBatch];
+        f32x4 x[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const int k = min(i + j, used - 1);
+            const float *p = k == 0 ? p0 : p1 + (k - 1) * stride;
+            ref[j] = p[PAIRS * D + m];
+            l[j] = p[PAIRS * (D + 1) + m];
+            x[j] = *reinterpret_cast<const f32x4 *>(p + m * D + d0);
+        }
+        float next = top;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) next = fmaxf(next, ref[j]);
+        const float use = next == kNegInf ? 0.0f : next;
+        const float keep = __builtin_amdgcn_exp2f(top - use);
+        top = next;
+        total *= keep;
+        v *= keep;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const float f = i + j < used ? __builtin_amdgcn_exp2f(ref[j] - use) : 0.0f;
+            if (i + j < used) {
+                total += l[j] * f;
+                v += x[j] * f;
+            }
+        }
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    V4 r;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) r[j] = (T)(v[j] * inv);
+    *reinterpret_cast<V4 *>(out + d0) = r;
+    if (lse && d0 == 0) *lse = (top + __builtin_amdgcn_logf(total)) * kLn2;
+}
+constexpr int kJoinThreads = 256;
+
 }  // namespace qsa

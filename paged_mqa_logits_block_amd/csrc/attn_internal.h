@@ -60,6 +60,7 @@ struct AttnArgs {
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
 // bytes of a balanced launch's workspace
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles);
+int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s);
 
 struct PlanArgs {

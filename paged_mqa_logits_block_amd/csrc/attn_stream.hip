@@ -53,13 +53,18 @@ __device__ __forceinline__ Pair pair_of(const AttnArgs &a, const TileWork &w, in
     return p;
 }
 
-// the tile of row tile `slot` and head part `hs`; false for a slot without rows
-template <bool SPARSE>
-__device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, TileWork &w) {
+// the query heads of head part `hs`
+__device__ __forceinline__ void part_heads(const AttnArgs &a, int hs, TileWork &w) {
     w.hk = hs / a.num_subs;
     const int sub = hs - w.hk * a.num_subs;
     w.head0 = w.hk * a.group + sub * a.sub_heads;
     w.heads = min(a.sub_heads, a.group - sub * a.sub_heads);
+}
+
+// the tile of row tile `slot` and head part `hs`; false for a slot without rows
+template <bool SPARSE>
+__device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, TileWork &w) {
+    part_heads(a, hs, w);
     if (SPARSE) {
         w.row0 = slot;
         w.rows = 1;
@@ -400,6 +405,11 @@ __device__ __forceinline__ int group_of(int64_t u, int64_t total) {
     return (int)(((u + 1) * groups_of(total) + total - 1) / total) - 1;
 }
 
+// the workgroups with parts of a tile, and its rows
+struct TileSpan {
+    int first, last, row0, rows;
+};
+
 // Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
 // units of a slot are the same for every hs.
 template <int DT, int D, bool SPARSE>
@@ -438,18 +448,26 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
     __syncthreads();
     const int per_head = before[slots];
     const int64_t total = (int64_t)per_head * hss;
-    if (g >= groups_of(total)) return;
+    if (g > 0 && g >= groups_of(total)) return;
     if (g == 0) {  // which workgroups have parts of each tile
-        int2 *spans = reinterpret_cast<int2 *>(part_of<D>(a, kStreamGroups, slots * hss));
+        TileSpan *spans = reinterpret_cast<TileSpan *>(part_of<D>(a, kStreamGroups, slots * hss));
         for (int i = t; i < slots * hss; i += kStreamThreads) {
             const int hs = i / slots, slot = i - hs * slots;
             const int64_t u0 = (int64_t)hs * per_head + before[slot], u1 = (int64_t)hs * per_head + before[slot + 1];
-            int2 s;
-            s.x = u1 > u0 ? group_of(u0, total) : 0;
-            s.y = u1 > u0 ? group_of(u1 - 1, total) : 0;
+            TileSpan s = {0, 0, slot, 1};
+            if (u1 > u0) {
+                s.first = group_of(u0, total);
+                s.last = group_of(u1 - 1, total);
+                RowTile w;
+                if (!SPARSE && slot_tile(a, slot, w)) {
+                    s.row0 = w.row0;
+                    s.rows = w.rows;
+                }
+            }
             spans[i] = s;
         }
     }
+    if (total == 0) return;
     int64_t u = first_unit(g, total);
     const int64_t end = first_unit(g + 1, total);
     while (u < end) {
@@ -477,63 +495,25 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
     }
 }
 
-// Joins the parts of a cut tile, one wave to a pair: lane i reads the maxima and
-// sums of parts i, i + 64, ..., and the outputs are read 8 parts at a time, D / 64
-// elements per lane.
-constexpr int kJoinPairs = 4;
-
-template <int DT, int D, bool SPARSE>
-__global__ __launch_bounds__(64 * kJoinPairs) void attn_join_kernel(AttnArgs a) {
-    constexpr int kPer = D / 64, kBatch = 8, kRounds = kStreamGroups / kWave, kPart = kAttnTile * (D + 2);
-    typedef float Vec __attribute__((ext_vector_type(kPer)));
-    const int slot = blockIdx.x, hs = blockIdx.y, slots = a.slots, tile = hs * slots + slot;
+template <int DT, int D>
+__global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
+    const int hss = a.num_kv_heads * a.num_subs, tile = blockIdx.x, hs = tile / a.slots;
+    const TileSpan s = reinterpret_cast<const TileSpan *>(part_of<D>(a, kStreamGroups, a.slots * hss))[tile];
+    if (s.last <= s.first) return;
+    constexpr int kPairs = kJoinThreads / (D / 4);
+    const int m = blockIdx.y * kPairs + threadIdx.x / (D / 4);
     TileWork w;
-    const bool rows = tile_work<SPARSE>(a, slot, hs, w);
-    const int2 span = reinterpret_cast<const int2 *>(part_of<D>(a, kStreamGroups, slots * gridDim.y))[tile];
-    const int lane = threadIdx.x & 63;
-    const int pm = __builtin_amdgcn_readfirstlane(blockIdx.z * kJoinPairs + (threadIdx.x >> 6));
-    if (!rows || span.y <= span.x) return;
-    const Pair pp = pair_of(a, w, pm);
+    part_heads(a, hs, w);
+    w.row0 = s.row0;
+    w.rows = s.rows;
+    const Pair pp = pair_of(a, w, m);
     if (!pp.live) return;
-    const float *part = part_of<D>(a, span.x, tile);
-    const int used = __builtin_amdgcn_readfirstlane(span.y - span.x + 1);
-    float m[kRounds], l[kRounds], top = kNegInf, total = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const int p = i * kWave + lane;
-        m[i] = kNegInf;
-        l[i] = 0.0f;
-        if (p < used) {
-            m[i] = part[p * kPart + kAttnTile * D + pm];
-            l[i] = part[p * kPart + kAttnTile * (D + 1) + pm];
-        }
-        top = fmaxf(top, m[i]);
-    }
-    top = wave_max_f(top);
-    const float ref = top == kNegInf ? 0.0f : top;
-    Vec r = {};
-    const float *src = part + pm * D + kPer * lane;
-#pragma unroll
-    for (int i = 0; i < kRounds; ++i) {
-        const float f = __builtin_amdgcn_exp2f(m[i] - ref);
-        total += l[i] * f;
-        for (int b = i * kWave; b < min(used, (i + 1) * kWave); b += kBatch) {
-            Vec v[kBatch];
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j) v[j] = *reinterpret_cast<const Vec *>(src + min(b + j, used - 1) * kPart);
-#pragma unroll
-            for (int j = 0; j < kBatch; ++j)
-                if (b + j < used) r += v[j] * readlane_f(f, b + j - i * kWave);
-        }
-    }
-    total = wave_sum_f(total);
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    typedef typename Half<DT>::T T;
-    T *out = static_cast<T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head + kPer * lane;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) out[j] = (T)(r[j] * inv);
-    if (a.lse && lane == 0)
-        a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
+    const float *p = part_of<D>(a, s.first, tile);
+    constexpr int kPart = kAttnTile * (D + 2);
+    join_parts<DT, D, kAttnTile>(
+        p, p + kPart, kPart, s.last - s.first + 1, m, 4 * (threadIdx.x % (D / 4)),
+        static_cast<typename Half<DT>::T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head,
+        a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }
 
 template <int DT, int D, bool SPARSE>
@@ -547,8 +527,8 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     hipLaunchKernelGGL((attn_balanced_kernel<DT, D, SPARSE>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_join_kernel<DT, D, SPARSE>), dim3((unsigned)a.slots, heads, kAttnTile / kJoinPairs),
-                       dim3(64 * kJoinPairs), 0, s, a);
+    hipLaunchKernelGGL((attn_join_kernel<DT, D>),
+                       dim3((unsigned)a.slots * heads, kAttnTile * (D / 4) / kJoinThreads), dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 
@@ -565,7 +545,7 @@ hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s) {
 }
 
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles) {
-    return (kStreamGroups + tiles) * (kAttnTile * (head_dim + 2) * 4) + 8 * tiles;
+    return (kStreamGroups + tiles) * (kAttnTile * (head_dim + 2) * 4) + (int64_t)sizeof(TileSpan) * tiles;
 }
 
 }  // namespace qsa

@@ -24,11 +24,17 @@ namespace {
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kTileKeys = 64;
+constexpr int kTilePairs = kAttnTile * kTileWaves;
 
-// The wave's pairs, each over its own visible keys (see own_range).
+// A cut tile's state: the outputs of its 256 pairs relative to their references,
+// the references, the sums.
+template <int D>
+constexpr int kTilePart = kTilePairs * (D + 2);
+
+// The wave's pairs, each over its own visible keys of [k0, k1) (see own_range).
 template <int DT, int D>
-__device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, int row0, int rows, int wave,
-                                                    int hk) {
+__device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, int row0, int rows, int wave, int hk,
+                                                    int k0, int k1, float *dest) {
     typedef typename Half<DT>::T T;
     const int lane = lane_id();
     for (int p = 0; p < kAttnTile; ++p) {
@@ -36,8 +42,16 @@ __device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, 
         if (r >= rows) break;
         const int row = row0 + r, head = hk * a.group + (m - r * a.group);
         float top, total, o[D / 64];
-        own_range<DT, D>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk, 0,
-                         min(max(a.ctx_lens[row], 0), a.cap), top, total, o);
+        own_range<DT, D>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk, k0,
+                         min(k1, min(max(a.ctx_lens[row], 0), a.cap)), top, total, o);
+        if (dest) {
+            for (int i = 0; i < D / 64; ++i) dest[m * D + lane * (D / 64) + i] = o[i];
+            if (lane == 0) {
+                dest[kTilePairs * D + m] = top;
+                dest[kTilePairs * (D + 1) + m] = total;
+            }
+            continue;
+        }
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
         for (int i = 0; i < D / 64; ++i) out[lane * (D / 64) + i] = (T)(o[i] * inv);
@@ -97,24 +111,44 @@ __device__ __forceinline__ void multiply(const uint8_t *vb, const uint8_t *kb, c
     }
 }
 
+// Workgroups go to the 8 XCDs in turn, and each XCD has an L2 of its own: the kv
+// heads are dealt to the XCDs (as far as their number shares a factor with 8), so
+// that an L2 sees the keys of few heads.  Within a head the tiles are taken from
+// the last on: a chunk's last rows see the most keys.
+constexpr int kXcds = 8;
+__host__ __device__ __forceinline__ int head_classes(int heads) { return heads % 8 == 0 ? 8 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1; }
+__device__ __forceinline__ bool place_of(const AttnArgs &a, int id, int &hk, int &slot) {
+    const int classes = head_classes(a.num_kv_heads), x = id % kXcds, j = id / kXcds * (kXcds / classes) + x / classes;
+    const int i = j / a.slots;
+    hk = x % classes + classes * i;
+    slot = a.slots - 1 - (j - i * a.slots);
+    return hk < a.num_kv_heads;
+}
+
 // WHOLE: the block size is a multiple of 8, so that the 8 keys that a wave copies in
 // a step lie in one block: its table entry is read by a scalar load and the copies
 // take a scalar base, with offsets that stay the same from step to step.  (With a
 // table load and address per lane the copies' part of a turn took as long as the
 // softmax: 1,100 cycles against 1,000.)
+template <int D>
+struct TileShared {
+    __align__(16) uint8_t kring[3][kTileKeys * D * 2], vring[3][kTileKeys * D * 2];
+    int most_of[kTileWaves], any_bad;
+};
+
+// steps [s0, min(s1, the tile's steps)) of tile w and kv head hk; dest: the place of
+// the state, or null to write the outputs
 template <int DT, int D, bool WHOLE>
-__global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) {
+__device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, const RowTile &w, int hk, int s0, int s1,
+                                          float *dest) {
     constexpr int kStepBytes = kTileKeys * D * 2;  // keys (or values) of one step
     constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
     constexpr int kCopies = kTileKeys / kKeysPerCopy / kTileWaves;  // copies of each kind per wave
-    __shared__ __align__(16) uint8_t kring[3][kStepBytes], vring[3][kStepBytes];
-    __shared__ int most_of[kTileWaves], any_bad;
-
-    const int t = threadIdx.x, lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    const int hk = blockIdx.y;
-    RowTile w;
-    if (!find_tile(a, blockIdx.x, w)) return;
-    w.req = __builtin_amdgcn_readfirstlane(w.req);
+    auto &kring = sh.kring;
+    auto &vring = sh.vring;
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));  // addresses are made anew for each range, not kept live across them
+    const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
     const int m = wave * kAttnTile + (lane & 31), r = m / a.group;
     const bool live = r < w.rows;
     const int row = w.row0 + r, head = hk * a.group + (m - r * a.group);
@@ -123,8 +157,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
     const int ctx = live ? min(max(a.ctx_lens[row], 0), a.cap) : 0;
     const int wave_most = __builtin_amdgcn_readfirstlane(wave_max_i(ctx));
     const int wave_least = -__builtin_amdgcn_readfirstlane(wave_max_i(live ? -ctx : -0x7FFFFFFF));
-    if (lane == 0) most_of[wave] = wave_most;
-    if (t == 0) any_bad = 0;
+    if (lane == 0) sh.most_of[wave] = wave_most;
+    if (t == 0) sh.any_bad = 0;
 
     i32x4 q[D / 16];
     const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head;
@@ -136,10 +170,10 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
     __syncthreads();
     int keys = 0;
 #pragma unroll
-    for (int i = 0; i < kTileWaves; ++i) keys = max(keys, most_of[i]);
+    for (int i = 0; i < kTileWaves; ++i) keys = max(keys, sh.most_of[i]);
     keys = __builtin_amdgcn_readfirstlane(keys);
-    const int steps = (keys + kTileKeys - 1) / kTileKeys;
-    const bool active = wave_most > 0;
+    const int steps = min(s1, (keys + kTileKeys - 1) / kTileKeys);
+    const bool active = wave_most > s0 * kTileKeys;
 
     const uint32_t kring_lds = lds_offset(kring), vring_lds = lds_offset(vring);
     const int32_t *table = a.block_table + (int64_t)w.req * a.max_blocks;
@@ -220,17 +254,17 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
 
     f32x16 o[D / 32] = {};
     float ref = kNegInf, total = 0.0f;  // total: this lane's half of the sum
-    if (steps > 0) {
-        load_entries(0);
+    if (steps > s0) {
+        load_entries(s0);
         pin_entries();
-        locate(0);
+        locate(s0);
         copy_keys(0);
         copy_values(0);
-        load_entries(1);
+        load_entries(s0 + 1);
         pin_entries();
-        locate(1);  // past the end: the last key once more, never used
+        locate(s0 + 1);  // past the end: the last key once more, never used
         copy_keys(1);
-        load_entries(2);
+        load_entries(s0 + 2);
         wait_copies();
         pin_entries();
 #pragma unroll
@@ -273,8 +307,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
             b2 = b;
         };
         if (active) multiply<DT, D, false, true>(vring[0], kring[0], p, q, o, z, lane);
-        softmax_turn(0);
-        for (int s = 1; s < steps; ++s) {
+        softmax_turn(s0);
+        for (int s = s0 + 1; s < steps; ++s) {
             if (active) multiply<DT, D, true, true>(vring[b2], kring[b0], p, q, o, z, lane);
             softmax_turn(s);
         }
@@ -287,9 +321,9 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
     // The wave's pairs are done again, each over its own keys, where the tile met a
     // table entry outside the pool, or where a NaN can come from a value that only
     // other rows of the wave see (zero weight times a value that is not finite).
-    if (ballot(met_bad) && lane == 0) any_bad = 1;
+    if (ballot(met_bad) && lane == 0) sh.any_bad = 1;
     __syncthreads();
-    bool again = any_bad != 0;
+    bool again = sh.any_bad != 0;
     if (wave_least < wave_most) {
         bool nan = false;
 #pragma unroll
@@ -299,10 +333,23 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
         again |= ballot(nan && live) != 0;
     }
     if (again) {
-        own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk);
+        own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, dest);
         return;
     }
     if (!live) return;
+    if (dest) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<f32x4 *>(dest + m * D + out_element<D>(c, 4 * g, lane)) =
+                    f32x4{o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
+        if (lane < kAttnTile) {
+            dest[kTilePairs * D + m] = ref;
+            dest[kTilePairs * (D + 1) + m] = total;
+        }
+        return;
+    }
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
     typedef typename Half<DT>::T T;
     typedef T V4 __attribute__((ext_vector_type(4)));
@@ -320,21 +367,202 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
         a.lse[(int64_t)row * (a.num_kv_heads * a.group) + head] = (ref + __builtin_amdgcn_logf(total)) * kLn2;
 }
 
+// one workgroup per tile
+template <int DT, int D, bool WHOLE>
+__global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) {
+    __shared__ TileShared<D> sh;
+    int hk, slot;
+    RowTile w;
+    if (!place_of(a, blockIdx.x, hk, slot) || !find_tile(a, slot, w)) return;
+    w.req = __builtin_amdgcn_readfirstlane(w.req);
+    run_steps<DT, D, WHOLE>(a, sh, w, hk, 0, 0x7FFFFFFF, nullptr);
+}
+
+// Balanced launch: the tiles' steps laid end to end, kv head by kv head, and cut
+// into equal parts for one workgroup per CU, of kLeastSteps steps at least.  A
+// workgroup has at most two cut tiles, its first and its last: part 2 g of the
+// workspace is the state of workgroup g's first tile, part 2 g + 1 that of a last
+// tile that begins in its range.
+constexpr int kLeastSteps = 4;
+__device__ __forceinline__ int tile_groups(int64_t total) {
+    return (int)min((total + kLeastSteps - 1) / kLeastSteps, (int64_t)kStreamGroups);
+}
+__device__ __forceinline__ int64_t first_step(int g, int64_t total) { return g * total / tile_groups(total); }
+
+struct TileSpan {
+    int first, last;  // workgroups with parts of the tile
+    int place;        // 0 or 1: its state is the first or the second part of workgroup `first`
+    int row0, rows;
+    int unused;
+};
+
+template <int DT, int D, bool WHOLE>
+__global__ __launch_bounds__(kTileThreads, 2) void attn_tile_balanced_kernel(AttnArgs a) {
+    __shared__ TileShared<D> sh;
+    __shared__ int32_t before[kMaxSlots + 1];  // steps of the slots before; while they are made, keys of the slot
+    __shared__ int32_t starts[kMaxSlots + 1];  // first row of each request
+    __shared__ int32_t wave_sums[kTileWaves];
+    const int t = threadIdx.x, lane = t & 63, slots = a.slots, n = a.num_reqs, T = a.tile_rows;
+    // workgroup ids go to the XCDs in turn: each XCD takes one stretch of the line
+    const int g = (int)(blockIdx.x % kXcds) * (kStreamGroups / kXcds) + (int)(blockIdx.x / kXcds);
+    for (int i = t; i <= n; i += kTileThreads) starts[i] = request_start(a, i);
+    for (int i = t; i <= slots; i += kTileThreads) before[i] = -1;
+    __syncthreads();
+    const auto request_of_slot = [&](int slot) {  // the last i with starts[i] / T + i <= slot
+        int lo = 0, hi = n;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (starts[mid] / T + mid <= slot) lo = mid;
+            else hi = mid;
+        }
+        return lo;
+    };
+    {  // each slot's largest visible count, from a run of rows per thread
+        const int per = (a.num_rows + kTileThreads - 1) / kTileThreads;
+        const int r0 = t * per, r1 = min(r0 + per, a.num_rows);
+        int req = 0;
+        if (r0 < r1) {
+            int hi = n;  // the last request with starts[req] <= r0
+            while (hi - req > 1) {
+                const int mid = (req + hi) >> 1;
+                if (starts[mid] <= r0) req = mid;
+                else hi = mid;
+            }
+        }
+        for (int r = r0; r < r1; ++r) {
+            while (req < n && r >= starts[req + 1]) ++req;
+            if (req >= n) break;
+            const int s = starts[req], len = starts[req + 1] - s;
+            if (r >= s && len >= a.min_rows && len <= a.max_rows)
+                atomicMax(&before[s / T + req + (r - s) / T], min(max(a.ctx_lens[r], 0), a.cap));
+        }
+    }
+    __syncthreads();
+    constexpr int kPer = kMaxSlots / kTileThreads;
+    int u[kPer], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
+        u[i] = keys < 0 ? 0 : max((keys + kTileKeys - 1) / kTileKeys, 1);  // rows that see nothing are written too
+        sum += u[i];
+    }
+    const int inc = wave_incl_sum(sum);
+    if (lane == 63) wave_sums[t >> 6] = inc;
+    __syncthreads();
+    int at = inc - sum;
+    for (int i = 0; i < (t >> 6); ++i) at += wave_sums[i];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (t * kPer + i <= slots) before[t * kPer + i] = at;
+        at += u[i];
+    }
+    if (t == kTileThreads - 1 && slots == kMaxSlots) before[slots] = at;
+    __syncthreads();
+    const int per_head = before[slots];
+    const int64_t total = (int64_t)per_head * a.num_kv_heads;
+    const int groups = tile_groups(total);
+    const auto tile_of = [&](int slot) {
+        RowTile w;
+        const int req = request_of_slot(slot);
+        w.req = req;
+        const int j = slot - (starts[req] / T + req);
+        w.row0 = starts[req] + j * T;
+        w.rows = j < 0 ? 0 : min(T, starts[req + 1] - w.row0);
+        return w;
+    };
+    TileSpan *spans = reinterpret_cast<TileSpan *>(a.part + (int64_t)2 * kStreamGroups * kTilePart<D>);
+    for (int i = (int)blockIdx.x * kTileThreads + t; i < slots * a.num_kv_heads; i += (int)gridDim.x * kTileThreads) {
+        const int hk = i / slots, slot = i - hk * slots;
+        const int64_t u0 = (int64_t)hk * per_head + before[slot], u1 = (int64_t)hk * per_head + before[slot + 1];
+        TileSpan s = {0, 0, 0, 0, 0, 0};
+        if (u1 > u0) {
+            s.first = (int)(((u0 + 1) * groups + total - 1) / total) - 1;
+            s.last = (int)((u1 * groups + total - 1) / total) - 1;
+            s.place = first_step(s.first, total) < u0;
+            const RowTile w = tile_of(slot);
+            s.row0 = w.row0;
+            s.rows = w.rows;
+        }
+        spans[i] = s;
+    }
+    if (g >= groups) return;
+    int64_t at_step = first_step(g, total);
+    const int64_t begin = at_step, end = first_step(g + 1, total);
+    while (at_step < end) {
+        const int hk = __builtin_amdgcn_readfirstlane((int)(at_step / per_head));
+        const int in_head = (int)(at_step - (int64_t)hk * per_head);
+        int slot = 0, hi = slots;  // the slot with before[slot] <= in_head < before[slot + 1]
+        while (hi - slot > 1) {
+            const int mid = (slot + hi) >> 1;
+            if (before[mid] <= in_head) slot = mid;
+            else hi = mid;
+        }
+        slot = __builtin_amdgcn_readfirstlane(slot);
+        const int64_t tile0 = (int64_t)hk * per_head + before[slot], tile1 = (int64_t)hk * per_head + before[slot + 1];
+        const int64_t stop = min(end, tile1);
+        RowTile w = tile_of(slot);
+        w.req = __builtin_amdgcn_readfirstlane(w.req);
+        w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
+        w.rows = __builtin_amdgcn_readfirstlane(w.rows);
+        float *dest = at_step == tile0 && stop == tile1
+                          ? nullptr
+                          : a.part + (int64_t)(2 * g + (tile0 > begin)) * kTilePart<D>;
+        run_steps<DT, D, WHOLE>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)(at_step - tile0)),
+                                __builtin_amdgcn_readfirstlane((int)(stop - tile0)), dest);
+        at_step = stop;
+        __syncthreads();  // all waves are done with the shared parts
+    }
+}
+
 template <int DT, int D>
+__global__ __launch_bounds__(kJoinThreads) void attn_tile_join_kernel(AttnArgs a) {
+    const TileSpan s = reinterpret_cast<const TileSpan *>(a.part + (int64_t)2 * kStreamGroups * kTilePart<D>)[blockIdx.x];
+    if (s.last <= s.first) return;
+    constexpr int kPairs = kJoinThreads / (D / 4);
+    const int hk = blockIdx.x / a.slots, m = blockIdx.y * kPairs + threadIdx.x / (D / 4), r = m / a.group;
+    if (r >= s.rows) return;
+    const int row = s.row0 + r, head = hk * a.group + (m - r * a.group);
+    const float *p0 = a.part + (int64_t)(2 * s.first + s.place) * kTilePart<D>;
+    const float *p1 = a.part + (int64_t)(2 * s.first + 2) * kTilePart<D>;
+    join_parts<DT, D, kTilePairs>(
+        p0, p1, 2 * kTilePart<D>, s.last - s.first + 1, m, 4 * (threadIdx.x % (D / 4)),
+        static_cast<typename Half<DT>::T *>(a.out) + row * a.o_row + head * a.o_head,
+        a.lse ? a.lse + (int64_t)row * (a.num_kv_heads * a.group) + head : nullptr);
+}
+
+template <int DT, int D, bool WHOLE>
 hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
-    const dim3 grid((unsigned)a.slots, (unsigned)a.num_kv_heads);
-    if (a.block_size % 8 == 0 && a.kv_slot < (1u << 25))
-        hipLaunchKernelGGL((attn_tile_kernel<DT, D, true>), grid, dim3(kTileThreads), 0, s, a);
-    else
-        hipLaunchKernelGGL((attn_tile_kernel<DT, D, false>), grid, dim3(kTileThreads), 0, s, a);
+    if (!a.part) {
+        const int classes = head_classes(a.num_kv_heads), share = kXcds / classes;  // XCDs per class of heads
+        const int64_t tiles = (int64_t)a.slots * (a.num_kv_heads / classes);
+        hipLaunchKernelGGL((attn_tile_kernel<DT, D, WHOLE>), dim3((unsigned)((tiles + share - 1) / share * kXcds)),
+                           dim3(kTileThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL((attn_tile_balanced_kernel<DT, D, WHOLE>), dim3(kStreamGroups), dim3(kTileThreads), 0, s, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL((attn_tile_join_kernel<DT, D>),
+                       dim3((unsigned)(a.slots * a.num_kv_heads), kTilePairs * (D / 4) / kJoinThreads),
+                       dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
+}
+
+template <int DT>
+hipError_t run_dim(const AttnArgs &a, hipStream_t s) {
+    const bool whole = a.block_size % 8 == 0 && a.kv_slot < (1u << 25);
+    if (a.head_dim == 128) return whole ? run_tile<DT, 128, true>(a, s) : run_tile<DT, 128, false>(a, s);
+    return whole ? run_tile<DT, 64, true>(a, s) : run_tile<DT, 64, false>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s) {
-    if (a.dtype == kBF16) return a.head_dim == 128 ? run_tile<kBF16, 128>(a, s) : run_tile<kBF16, 64>(a, s);
-    return a.head_dim == 128 ? run_tile<kFP16, 128>(a, s) : run_tile<kFP16, 64>(a, s);
+    return a.dtype == kBF16 ? run_dim<kBF16>(a, s) : run_dim<kFP16>(a, s);
+}
+
+int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles) {
+    return (int64_t)2 * kStreamGroups * kTilePairs * (head_dim + 2) * 4 + (int64_t)sizeof(TileSpan) * tiles;
 }
 
 }  // namespace qsa
