@@ -476,8 +476,9 @@ typedef struct qsa_attn_shape {
  * sums, maxima and lse are 32-bit.
  *
  * Compiled set: Hq / Hk <= 128, Hq <= 8192, B <= 1024.  Range: max_blocks * B <=
- * 2^30, R and num_reqs <= 2^22.  Alignment: pointers 16 bytes, strides multiples
- * of 8 elements.
+ * 2^30, R and num_reqs <= 2^21, and (R * Hq / (256 Hk) + num_reqs) * Hk tiles <= 2^22.
+ * Alignment: pointers 16 bytes, strides multiples of 8 elements.  out and lse must
+ * not overlap the inputs.
  */
 QSA_API qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vcache,
                                        const int32_t *block_table, const int32_t *ctx_lens,

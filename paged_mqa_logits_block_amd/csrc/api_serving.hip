@@ -99,6 +99,7 @@ qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *
     if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
     if (s->kv_layout == QSA_KV_COPACKED_SHUFFLED && s->block_size % 16 != 0)
         return fail(QSA_E_UNSUPPORTED, "the preshuffled layout needs block_size %% 16 == 0");
+    if (s->num_rows > (1 << 27)) return fail(QSA_E_RANGE, "num_rows = %d > 2^27", s->num_rows);
     if (s->num_blocks > ((int64_t)1 << 40) || s->src_stride > ((int64_t)1 << 30))
         return fail(QSA_E_RANGE, "cache or source too large");
     if (s->num_rows > 0 && (!aligned16(keys) || !aligned16(kcache)))
@@ -108,81 +109,88 @@ qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *
     return ok();
 }
 
-// The requests that the streaming kernel takes: up to this many stacked pairs
-// per kv head.
+// Which kernel takes a request: up to this many stacked pairs per kv head it is
+// streamed.  (One request, 4 kv heads of 8 query heads at D = 128, us streamed / by
+// the tile kernel: 16 rows of 2,048 tokens 14.9 / 19.5, of 16,384 22.1 / 26.6, of
+// 65,536 48.8 / 43.5; 12 rows 14.7 / 18.3, 31.2 / 25.2, 70.3 / 39.7; 8 rows
+// 14.3 / 17.1, 20.8 / 24.0, 38.0 / 38.0.)
 constexpr int kStreamPairs = 64;
-// Stacked pairs per kv head of a batch that is streamed whole.
-constexpr int kSmallBatch = 512;
-// Tiles up to which a streamed launch cuts the keys into equal parts; with more,
-// every tile's workgroup takes all of its keys.
-constexpr int kBalancedTiles = 2048;
-// The same for the tile kernel, and the rows up to which its workgroups find their
-// parts (each reads every row's visible count).
-constexpr int kBalancedBig = 1024, kBalancedRows = 8192;
+// Stacked pairs per kv head, and row tiles, of a batch that is streamed whole
+constexpr int kSmallBatch = 512, kSmallSlots = 256;
+// Tiles up to which tiles of uneven length are cut into equal parts of their keys,
+// and the rows up to which the tile kernel's workgroups find their parts (each
+// reads every row's visible count).  (1,024 decode tiles of 1,000 to 4,000 tokens: 222
+// us cut, 212 whole; 256 of 8,000 to 16,000 run at 5.6 TB/s cut, where whole ones
+// wait for the longest.)
+constexpr int kCutTiles = 1024, kCutRows = 8192;
+
+// Tiles of one length are cut only where whole ones would leave more than 15% of
+// the CUs' time unused.  (Selected tokens of 1,024 tiles: 97 us cut, 78 whole; 256
+// tiles of a 2,048-row chunk 555 + 28 cut, 515 whole; 104 uneven tiles of 17
+// requests 39 + 8 cut, 92 whole.)
+bool fills_badly(int64_t tiles) {
+    const int64_t rounds = (tiles + qsa::kStreamGroups - 1) / qsa::kStreamGroups;
+    return tiles * 100 < rounds * qsa::kStreamGroups * 85;
+}
 
 struct AttnPlan {
     int sub_heads, num_subs, stream_rows;  // heads per workgroup, workgroups per kv head, rows per streaming tile
     int few_rows;                          // requests of up to this many rows are streamed
-    int slots, slots_per_req;
-    int tile_rows, tile_slots;             // the same of the tile kernel
+    int64_t slots;                         // row tiles of the streaming kernel's plain grid
+    int64_t cut_slots;                     // the same of its cut launch
+    int slots_per_req;                     // of the cut launch, dense
+    int tile_rows;                         // the tile kernel's
+    int64_t tile_slots;
     bool stream, tile;
-    int64_t stream_bytes, tile_bytes;      // workspace, 0: none used
+    int64_t stream_bytes, tile_bytes;      // workspace of a cut launch, 0: not cut
     int64_t bytes() const { return stream_bytes > tile_bytes ? stream_bytes : tile_bytes; }
 };
 
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     AttnPlan p = {};
     const int group = s->num_heads / s->num_kv_heads;
+    const int64_t R = s->num_rows, n = s->num_reqs;
     p.num_subs = (group + qsa::kAttnTile - 1) / qsa::kAttnTile;
     p.sub_heads = (group + p.num_subs - 1) / p.num_subs;
     p.num_subs = (group + p.sub_heads - 1) / p.sub_heads;
     p.stream_rows = sparse ? 1 : qsa::kAttnTile / p.sub_heads;
     p.few_rows = group >= kStreamPairs ? 1 : kStreamPairs / group;
+    const int64_t heads = (int64_t)s->num_kv_heads * p.num_subs, T = p.stream_rows;
+    const bool long_keys = keys > qsa::kStreamKeys * qsa::kStreamWaves;
     if (sparse) {
         p.stream = true;
-        p.slots = s->num_rows;
-    } else {
-        const int T = p.stream_rows;
-        // A small batch of few rows per request (on average: the lengths are on the
-        // device) is streamed whole; a launch of the tile kernel that finds nothing
-        // to do costs 5 us.
-        if (s->num_rows > p.few_rows && (int64_t)s->num_rows <= (int64_t)p.few_rows * s->num_reqs &&
-            (int64_t)s->num_rows * group <= kSmallBatch &&
-            (int64_t)s->num_reqs * ((s->num_rows + T - 1) / T) <= qsa::kMaxSlots)
-            p.few_rows = s->num_rows;
-        // with one request its rows are the call's rows, but for padding behind them
-        p.stream = s->num_reqs > 1 || s->num_rows <= p.few_rows;
-        p.tile = s->num_rows > p.few_rows;
-        const int rows = p.few_rows < s->num_rows ? p.few_rows : s->num_rows;
-        const int64_t all = (int64_t)s->num_rows / T + s->num_reqs, per = (rows + T - 1) / T;
-        p.slots_per_req = per * s->num_reqs <= all || per * s->num_reqs <= qsa::kMaxSlots ? (int)per : 0;
-        p.slots = (int)(p.slots_per_req ? per * s->num_reqs : all);
+        p.slots = p.cut_slots = R;
+        if (R <= qsa::kMaxSlots && R * heads <= kCutTiles && fills_badly(R * heads) && long_keys)
+            p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, R * heads);
+        return p;
     }
-    const int64_t tiles = (int64_t)p.slots * s->num_kv_heads * p.num_subs;
-    if (p.stream && tiles > 0 && tiles <= kBalancedTiles && p.slots <= qsa::kMaxSlots &&
-        (sparse || p.slots_per_req) && keys > qsa::kStreamKeys * qsa::kStreamWaves)
-        p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, tiles);
-    if (p.tile) {
-        p.tile_rows = 256 / group;
-        p.tile_slots = s->num_rows / p.tile_rows + s->num_reqs;
-        const int64_t all = (int64_t)p.tile_slots * s->num_kv_heads;
-        // One request's tiles are nearly alike: they are cut only where whole ones would
-        // leave more than 15% of the CUs' time unused (256 tiles: 515 us whole, 555 + 28
-        // cut).  Requests of several lengths are cut up to kBalancedBig tiles (104 tiles
-        // of 17 requests: 92 us whole, 39 + 13 cut).
-        const int64_t tiles = (int64_t)((s->num_rows + p.tile_rows - 1) / p.tile_rows) * s->num_kv_heads;
-        const int64_t rounds = (tiles + qsa::kStreamGroups - 1) / qsa::kStreamGroups;
-        const bool uneven = s->num_reqs > 1 || tiles * 100 < rounds * qsa::kStreamGroups * 85;
-        if (uneven && all <= kBalancedBig && p.tile_slots <= qsa::kMaxSlots && s->num_reqs <= qsa::kMaxSlots &&
-            s->num_rows <= kBalancedRows)
-            p.tile_bytes = qsa::attn_tile_workspace_bytes(s->head_dim, all);
-    }
+    // A small batch of few rows per request (on average: the lengths are on the
+    // device) is streamed whole; a launch of the tile kernel that finds nothing to do
+    // costs 5 us.
+    if (R > p.few_rows && R <= p.few_rows * n && R * group <= kSmallBatch && n * ((R + T - 1) / T) <= kSmallSlots)
+        p.few_rows = (int)R;
+    // with one request its rows are the call's rows, but for padding behind them
+    p.stream = n > 1 || R <= p.few_rows;
+    p.tile = R > p.few_rows;
+    p.slots = R / T + n;
+    const int64_t rows = p.few_rows < R ? p.few_rows : R, least = n < R ? n : R;
+    p.slots_per_req = (int)((rows + T - 1) / T);
+    p.cut_slots = p.slots_per_req * n;
+    const int64_t tiles = ((R + T - 1) / T > least ? (R + T - 1) / T : least) * heads;
+    if (p.stream && p.cut_slots <= qsa::kMaxSlots && tiles <= kCutTiles && long_keys)
+        p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, p.cut_slots * heads);
+    p.tile_rows = qsa::kTilePairs / group;
+    p.tile_slots = R / p.tile_rows + n;
+    const int64_t all = p.tile_slots * s->num_kv_heads;
+    const int64_t big = (R + p.tile_rows - 1) / p.tile_rows * s->num_kv_heads;
+    if (p.tile && (n > 1 || fills_badly(big)) && all <= kCutTiles && p.tile_slots <= qsa::kMaxSlots &&
+        n <= qsa::kMaxSlots && R <= kCutRows)
+        p.tile_bytes = qsa::attn_tile_workspace_bytes(s->head_dim, all);
     return p;
 }
 
-qsa_status check_attn(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
-                      const int32_t *per_row, const int32_t *starts_or_idx, const void *out,
-                      const qsa_attn_shape *s, bool sparse, int32_t k, int32_t ratio) {
+// the sizes that plan_attn and the launches take
+qsa_status check_attn_sizes(const qsa_attn_shape *s, bool sparse, int32_t k, int32_t ratio) {
     if (!s) return fail(QSA_E_INVALID, "shape is NULL");
     if (s->num_rows < 0) return fail(QSA_E_INVALID, "num_rows = %d < 0", s->num_rows);
     if (s->num_heads < 1 || s->num_kv_heads < 1 || s->head_dim < 1 || s->block_size < 1 || s->num_reqs < 1 ||
@@ -191,32 +199,44 @@ qsa_status check_attn(const void *q, const void *kcache, const void *vcache, con
                                    "num_blocks must be >= 1");
     if (s->num_heads % s->num_kv_heads != 0)
         return fail(QSA_E_INVALID, "num_heads = %d is not a multiple of num_kv_heads = %d", s->num_heads, s->num_kv_heads);
+    if (sparse) {
+        if (k < 1) return fail(QSA_E_INVALID, "k = %d < 1", k);
+        if (ratio < 1) return fail(QSA_E_INVALID, "ratio = %d < 1", ratio);
+    }
+    if (s->head_dim != 64 && s->head_dim != 128)
+        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
+    if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
+    const int group = s->num_heads / s->num_kv_heads;
+    if (group > 128) return fail(QSA_E_UNSUPPORTED, "%d heads per kv head (built: 1 to 128)", group);
+    if (s->num_heads > 8192) return fail(QSA_E_UNSUPPORTED, "num_heads = %d (built: up to 8192)", s->num_heads);
+    if (s->num_rows > (1 << 21) || s->num_reqs > (1 << 21))
+        return fail(QSA_E_RANGE, "num_rows = %d or num_reqs = %d > 2^21", s->num_rows, s->num_reqs);
+    if ((int64_t)s->max_blocks * s->block_size > (1 << 30))
+        return fail(QSA_E_RANGE, "max_blocks * block_size = %lld > 2^30", (long long)s->max_blocks * s->block_size);
+    if (sparse && (int64_t)k * ratio > (1 << 24))
+        return fail(QSA_E_RANGE, "k * ratio = %lld > 2^24", (long long)k * ratio);
+    // workgroups of the tile kernel
+    const int64_t tiles = ((int64_t)s->num_rows / (qsa::kTilePairs / group) + s->num_reqs) * s->num_kv_heads;
+    if (!sparse && tiles > (1 << 22))
+        return fail(QSA_E_RANGE, "too many tiles (%lld > 2^22) of rows, requests and kv heads", (long long)tiles);
+    return ok();
+}
+
+qsa_status check_attn(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
+                      const int32_t *per_row, const int32_t *starts_or_idx, const void *out,
+                      const qsa_attn_shape *s, bool sparse, int32_t k, int32_t ratio) {
+    qsa_status st = check_attn_sizes(s, sparse, k, ratio);
+    if (st != QSA_OK) return st;
     if (!(s->scale > 0.0f) || isinf(s->scale)) return fail(QSA_E_INVALID, "scale must be positive and finite");
     if (s->q_row_stride < 0 || s->q_head_stride < 0 || s->out_row_stride < 0 || s->out_head_stride < 0 ||
         s->kv_block_stride < 0 || s->kv_slot_stride < 0 || s->kv_head_stride < 0)
         return fail(QSA_E_INVALID, "strides must be >= 0");
     if ((s->num_rows > 1 && s->out_row_stride < s->head_dim) || (s->num_heads > 1 && s->out_head_stride < s->head_dim))
         return fail(QSA_E_INVALID, "the strides of out must be at least head_dim");
-    if (sparse) {
-        if (k < 1) return fail(QSA_E_INVALID, "k = %d < 1", k);
-        if (ratio < 1) return fail(QSA_E_INVALID, "ratio = %d < 1", ratio);
-    }
     if (s->num_rows > 0 && (!q || !kcache || !vcache || !block_table || !per_row || !starts_or_idx || !out))
         return fail(QSA_E_INVALID, "q, kcache, vcache, block_table, %s and out must be non-NULL",
                     sparse ? "row_to_req, idx" : "ctx_lens, q_starts");
     if (s->dtype != QSA_BF16 && s->dtype != QSA_FP16) return fail(QSA_E_DTYPE, "dtype = %d (built: bf16, fp16)", s->dtype);
-    if (s->head_dim != 64 && s->head_dim != 128)
-        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
-    if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
-    if (s->num_heads / s->num_kv_heads > 128)
-        return fail(QSA_E_UNSUPPORTED, "%d heads per kv head (built: 1 to 128)", s->num_heads / s->num_kv_heads);
-    if (s->num_heads > 8192) return fail(QSA_E_UNSUPPORTED, "num_heads = %d (built: up to 8192)", s->num_heads);
-    if (s->num_rows > (1 << 22) || s->num_reqs > (1 << 22))
-        return fail(QSA_E_RANGE, "num_rows = %d or num_reqs = %d > 2^22", s->num_rows, s->num_reqs);
-    if ((int64_t)s->max_blocks * s->block_size > (1 << 30))
-        return fail(QSA_E_RANGE, "max_blocks * block_size = %lld > 2^30", (long long)s->max_blocks * s->block_size);
-    if (sparse && (int64_t)k * ratio > (1 << 24))
-        return fail(QSA_E_RANGE, "k * ratio = %lld > 2^24", (long long)k * ratio);
     const int64_t most = (int64_t)1 << 34;
     if (s->num_blocks > ((int64_t)1 << 50) || s->kv_block_stride > ((int64_t)1 << 50) / s->num_blocks ||
         s->kv_block_stride > most || s->kv_slot_stride > most || s->kv_head_stride > most || s->q_row_stride > most || s->q_head_stride > most ||
@@ -276,9 +296,12 @@ void stream_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.sub_heads = p.sub_heads;
     a.num_subs = p.num_subs;
     a.tile_rows = p.stream_rows;
-    a.slots = p.slots;
-    a.slots_per_req = p.slots_per_req;
-    a.part = p.stream_bytes > 0 ? static_cast<float *>(workspace) : nullptr;
+    // a cut launch gives every request as many slots as the longest needs; a plain
+    // one packs them, or its live workgroups would meet on a few XCDs
+    const bool cut = workspace && p.stream_bytes > 0;
+    a.part = cut ? static_cast<float *>(workspace) : nullptr;
+    a.slots = (int32_t)(cut ? p.cut_slots : p.slots);
+    a.slots_per_req = cut ? p.slots_per_req : 0;
 }
 
 }  // namespace
@@ -339,7 +362,7 @@ qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, 
 }
 
 int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *s) {
-    if (!s || s->num_rows <= 0 || s->num_reqs < 1 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads) return 0;
+    if (check_attn_sizes(s, false, 0, 0) != QSA_OK || s->num_rows == 0) return 0;
     return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes();
 }
 
@@ -367,7 +390,7 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
     if (p.tile) {
         qsa::AttnArgs b = a;
         b.tile_rows = p.tile_rows;
-        b.slots = p.tile_slots;
+        b.slots = (int32_t)p.tile_slots;
         b.part = p.tile_bytes > 0 ? static_cast<float *>(workspace) : nullptr;
         b.min_rows = p.stream ? p.few_rows + 1 : 1;
         b.max_rows = s->num_rows;
@@ -383,7 +406,7 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
 }
 
 int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *s, int32_t k, int32_t ratio) {
-    if (!s || s->num_rows <= 0 || s->num_kv_heads < 1 || s->num_heads < s->num_kv_heads || k < 1 || ratio < 1) return 0;
+    if (check_attn_sizes(s, true, k, ratio) != QSA_OK || s->num_rows == 0) return 0;
     return plan_attn(s, true, (int64_t)k * ratio).bytes();
 }
 

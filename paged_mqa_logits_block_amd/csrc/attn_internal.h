@@ -16,6 +16,9 @@ constexpr int kStreamWaves = 8;
 constexpr int kStreamGroups = 256;
 constexpr int kMaxSlots = 1024;
 
+// Stacked pairs of a workgroup of the tile kernel.
+constexpr int kTilePairs = 256;
+
 struct AttnArgs {
     const void *q;
     const uint8_t *kcache;
@@ -50,7 +53,7 @@ struct AttnArgs {
     int32_t div_shift;
     // launch shape
     int32_t slots;              // row tiles of the grid
-    int32_t slots_per_req;      // dense: > 0 where every request has that many
+    int32_t slots_per_req;      // dense: > 0 where every request has that many, else 0: packed
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile

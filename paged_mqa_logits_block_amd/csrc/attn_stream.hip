@@ -327,12 +327,12 @@ struct Stream {
         const Pair pp = pair_of(a, w, pm);
         if (!SPARSE && least < keys) {
             // A NaN can come from a value that only other rows of the tile see (zero
-            // weight times a value that is not finite): then every pair is done
-            // again over its own keys.
+            // weight times a value that is not finite; a pair whose own scores are NaN
+            // has a NaN sum): then every pair is done again over its own keys.
             bool nan = false;
 #pragma unroll
             for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
-            if (__syncthreads_or(nan && pp.live)) {
+            if (__syncthreads_or(nan && pp.live && total == total)) {
                 float *again = reinterpret_cast<float *>(sh.ring[0]);
                 for (int p = wave; p < kAttnTile; p += kStreamWaves) {
                     const Pair x = pair_of(a, w, p);

@@ -24,7 +24,7 @@ namespace {
 constexpr int kTileWaves = 8;
 constexpr int kTileThreads = 64 * kTileWaves;
 constexpr int kTileKeys = 64;
-constexpr int kTilePairs = kAttnTile * kTileWaves;
+static_assert(kTilePairs == kAttnTile * kTileWaves, "32 pairs to a wave");
 
 // A cut tile's state: the outputs of its 256 pairs relative to their references,
 // the references, the sums.
@@ -320,7 +320,8 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
 
     // The wave's pairs are done again, each over its own keys, where the tile met a
     // table entry outside the pool, or where a NaN can come from a value that only
-    // other rows of the wave see (zero weight times a value that is not finite).
+    // other rows of the wave see (zero weight times a value that is not finite; a pair
+    // whose own scores are NaN has a NaN sum).
     if (ballot(met_bad) && lane == 0) sh.any_bad = 1;
     __syncthreads();
     bool again = sh.any_bad != 0;
@@ -330,7 +331,7 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
             for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
-        again |= ballot(nan && live) != 0;
+        again |= ballot(nan && live && total == total) != 0;
     }
     if (again) {
         own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, dest);

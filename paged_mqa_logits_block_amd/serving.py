@@ -222,17 +222,19 @@ class PreparedWriteKv(_Prepared):
         code = _half_code("k", k)
         for name, t in (("v", v), ("kcache", kcache), ("vcache", vcache)):
             _require(t.dtype == k.dtype, f"{name} must have k's type")
-        _require(k.dim() == 3 and k.shape == v.shape and k.stride() == v.stride() and k.stride(2) == 1,
-                 "k and v must be [R, num_kv_heads, head_dim] with equal strides and a contiguous last dimension")
+        _require(k.dim() == 3 and k.shape == v.shape and k.stride(2) == 1 and v.stride(2) == 1,
+                 "k and v must be [R, num_kv_heads, head_dim] with a contiguous last dimension")
         R, hk, d = (int(x) for x in k.shape)
+        src = [[int(t.stride(0)) if R > 1 else d, int(t.stride(1)) if hk > 1 else d] for t in (k, v)]
+        _require(src[0] == src[1], "k and v must have equal strides")
         strides = _kv_strides("kcache", kcache)
         _require(kcache.shape == vcache.shape and strides == _kv_strides("vcache", vcache),
                  "kcache and vcache must have equal shapes and strides")
         _require((int(kcache.shape[2]), int(kcache.shape[3])) == (hk, d), "the caches' heads must be k's")
         _rows("slots", slots, R, torch.int64)
         shape = KvShape(num_rows=R, num_kv_heads=hk, head_dim=d, block_size=int(kcache.shape[1]), dtype=code,
-                        num_blocks=int(kcache.shape[0]), src_row_stride=int(k.stride(0)) if R > 1 else d,
-                        src_head_stride=int(k.stride(1)) if hk > 1 else d, kv_block_stride=strides[0],
+                        num_blocks=int(kcache.shape[0]), src_row_stride=src[0][0],
+                        src_head_stride=src[0][1], kv_block_stride=strides[0],
                         kv_slot_stride=strides[1], kv_head_stride=strides[2])
         args = (_ptr(k), _ptr(v), _ptr(slots), _ptr(kcache), _ptr(vcache), ctypes.byref(shape))
         _raise_on(lib.qsa_write_kv_check(*args))

@@ -129,6 +129,13 @@ def test_attention_workspace():
     assert m.sparse_attention_workspace_bytes(s, 2048, 4) > 0
     assert m.sparse_attention_workspace_bytes(attn_shape(num_rows=4096), 2048, 4) == 0
     assert m.sparse_attention_workspace_bytes(s, 0, 4) == 0
+    # shapes that the calls refuse need none, and the queries do not fail on them
+    for kw in (dict(num_heads=4096), dict(num_heads=2, num_kv_heads=4), dict(num_kv_heads=0), dict(head_dim=0),
+               dict(num_rows=-5), dict(num_rows=2 ** 31 - 1), dict(num_reqs=2 ** 31 - 1), dict(block_size=2 ** 31 - 1)):
+        assert m.paged_attention_workspace_bytes(attn_shape(**kw)) == 0, kw
+        assert m.sparse_attention_workspace_bytes(attn_shape(**kw), 64, 4) == 0, kw
+    assert check(A, A, A, A, A, A, A, attn_shape(num_rows=1 << 21, num_reqs=1 << 21, num_kv_heads=32), None,
+                 0) == m.E_RANGE
 
 
 def test_host_tensors_are_refused():

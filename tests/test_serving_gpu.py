@@ -305,6 +305,13 @@ PAGED = [
     ([10, 500, 0], [1, 100, 17], dict(group=7, hk=1, dim=64, dtype="fp16", block=100, order="head", pad=5)),
     ([40, 0], [70, 65], dict(group=33, hk=1)),
     ([17], [9], dict(group=128, hk=1, dim=64)),
+    # few tiles over many keys: parts of one tile from many workgroups
+    ([9000], [20], dict(group=4, hk=1)),
+    ([9000], [20], dict(group=4, hk=1, dim=64, dtype="fp16", block=1, order="head")),
+    ([9000, 30, 4000], [3, 1, 40], dict(group=16, hk=1, block=100)),
+    # requests without rows between others, one row each, more tiles than workgroups
+    ([0, 5, 9, 100] * 20, [0, 1, 0, 2] * 20, dict(group=8, hk=8)),
+    ([300] * 40, [1, 20] * 20, dict(group=8, hk=4, dim=64)),
 ]
 
 
@@ -316,9 +323,10 @@ def test_paged_attention(i):
     b.check(out, lse, lambda r: range(b.ctx[r]))
     # rows behind the last request are left as they were
     assert torch.all(out[b.rows:] == 3.0) and torch.all(lse[b.rows:] == 7.0)
-    if i < 10:  # without a workspace the keys of a tile are not split
-        out, lse = run_paged(b, workspace=None)
-        b.check(out, lse, lambda r: range(b.ctx[r]))
+    # without a workspace the keys of a tile are not cut
+    out, lse = run_paged(b, workspace=None)
+    b.check(out, lse, lambda r: range(b.ctx[r]))
+    assert torch.all(out[b.rows:] == 3.0) and torch.all(lse[b.rows:] == 7.0)
 
 
 @pytest.mark.parametrize("new", [[6, 5], [100, 90]], ids=["few", "chunk"])
@@ -393,6 +401,35 @@ def test_paged_attention_strides_and_stream():
     assert torch.equal(got, out)
 
 
+def test_paged_attention_long_context():
+    """3,000,001 tokens in blocks of 1,000, all entries of the table pointing at 7
+    blocks: the result is that of 7,000 keys with multiplicities."""
+    n, block, dim, group = 3_000_001, 1000, 64, 4
+    rng = np.random.default_rng(9)
+    kv = torch.from_numpy(rng.standard_normal((2, 7, block, 1, dim))).to(torch.bfloat16)
+    table = rng.integers(0, 7, (1, n // block + 1)).astype(np.int32)
+    q = torch.from_numpy(rng.standard_normal((1, group, dim))).to(torch.bfloat16)
+    lse = torch.empty(1, group, device="cuda")
+    out = m.paged_attention(q.cuda(), kv[0].cuda(), kv[1].cuda(), dev(table), dev(np.array([n], np.int32)),
+                            dev(np.array([0, 1], np.int32)), lse=lse)
+    count = np.zeros((7, block))
+    np.add.at(count, table[0, :n // block], 1)
+    count[table[0, -1], :n % block] += 1
+    k, v = (x.double().numpy().reshape(7 * block, dim) for x in kv)
+    z = q[0].double().numpy() @ k.T * dim ** -0.5
+    w = np.exp(z) * count.reshape(-1)
+    p = w / w.sum(axis=1, keepdims=True)
+    want = p @ v
+    # the longest chain of additions: the keys of one wave (n / (256 workgroups of 8
+    # waves)), the 8 waves and the 256 parts
+    size = dim ** -0.5 * (np.abs(q[0].double().numpy()) @ np.abs(k).T).max(axis=1)
+    u = torch.finfo(torch.bfloat16).eps / 2
+    lse_want = np.log(w.sum(axis=1))
+    to, tl = ref.bounds(want, lse_want, p @ np.abs(v), size, n // 2048 + 512, dim, u)
+    assert np.all(np.abs(out[0].double().cpu().numpy() - want) <= to)
+    assert np.all(np.abs(lse[0].double().cpu().numpy() - lse_want) <= tl)
+
+
 def test_paged_attention_far_blocks():
     """Pool offsets past 2^31 elements, in both kernels and the writes."""
     hk, dim, block = 4, 128, 64
@@ -428,6 +465,8 @@ SPARSE = [
     ([100], [1], 7, 5, dict(group=128, hk=1, dim=64, block=1)),
     ([20000], [1], 2048, 8, dict(group=8, hk=1)),
     ([300], [1], 1, 1, dict(group=1, hk=4)),
+    ([600, 40], [58, 2], 96, 4, dict(group=8, hk=4, dim=64)),   # as many tiles as workgroups, about
+    ([600, 40], [70, 2], 96, 4, dict(group=8, hk=4, dim=64)),   # some more
 ]
 
 
@@ -439,7 +478,7 @@ def sparse_idx(b, k, ratio):
     for r in range(b.rows):
         cols = -(-int(b.ctx[r]) // ratio)
         n = min(k, cols, k if r % 3 else max(1, k // 2))
-        if r == 5:
+        if r == 5 or r == 20:
             n = 0
         place = rng.permutation(k)[:n]
         idx[r, place] = rng.permutation(cols)[:n]
