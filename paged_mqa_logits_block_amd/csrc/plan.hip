@@ -66,12 +66,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs a) {
     const int i0 = min(t * per, n), i1 = min(i0 + per, n);
 
     uint32_t own = 0;
-    for (int i = i0; i < i1; ++i) own = min(own + (uint32_t)min(max(a.new_lens[i], 0), a.num_rows), most);
+    // both lengths are read at once; a thread's own places in LDS hold the new ones
+    // until its first row is known
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t fresh = (uint32_t)min(max(a.new_lens[i], 0), a.num_rows);
+        past[i] = (int32_t)min((uint32_t)max(a.past_lens[i], 0), cap);
+        starts[i] = fresh;
+        own = min(own + fresh, most);
+    }
     uint32_t at = block_offset(own, most, sums);
     for (int i = i0; i < i1; ++i) {
+        const uint32_t fresh = starts[i];
         starts[i] = at;
-        at = min(at + (uint32_t)min(max(a.new_lens[i], 0), a.num_rows), most);
-        past[i] = (int32_t)min((uint32_t)max(a.past_lens[i], 0), cap);
+        at = min(at + fresh, most);
         if (i == n - 1) starts[n] = at;
     }
     __syncthreads();
