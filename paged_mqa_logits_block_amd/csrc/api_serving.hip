@@ -109,19 +109,17 @@ qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *
     return ok();
 }
 
-// Which kernel takes a request: up to this many stacked pairs per kv head it is
-// streamed.  (One request, 4 kv heads of 8 query heads at D = 128, us streamed / by
-// the tile kernel: 16 rows of 2,048 tokens 14.9 / 19.5, of 16,384 22.1 / 26.6, of
-// 65,536 48.8 / 43.5; 12 rows 14.7 / 18.3, 31.2 / 25.2, 70.3 / 39.7; 8 rows
-// 14.3 / 17.1, 20.8 / 24.0, 38.0 / 38.0.)
-constexpr int kStreamPairs = 64;
-// Stacked pairs per kv head, and row tiles, of a batch that is streamed whole
-constexpr int kSmallBatch = 512, kSmallSlots = 256;
-// Tiles up to which tiles of uneven length are cut into equal parts of their keys,
-// and the rows up to which the tile kernel's workgroups find their parts (each
-// reads every row's visible count).  (1,024 decode tiles of 1,000 to 4,000 tokens: 222
-// us cut, 212 whole; 256 of 8,000 to 16,000 run at 5.6 TB/s cut, where whole ones
-// wait for the longest.)
+// Calls with up to this many stacked pairs per kv head and request on average are
+// streamed, small ones at least (the lengths are on the device).  One request, 4 kv
+// heads of 8 query heads at D = 128, us streamed / by the tile kernel: 16 rows of
+// 2,048 tokens 14.9 / 19.5, of 16,384 22.1 / 26.6, of 65,536 48.8 / 43.5; 12 rows
+// 14.7 / 18.3, 31.2 / 25.2, 70.3 / 39.7; 8 rows 14.3 / 17.1, 20.8 / 24.0, 38.0 /
+// 38.0.
+constexpr int kStreamPairs = 64, kSmallPairs = 512;
+// Tiles up to which tiles of uneven length are cut, and the rows up to which the
+// workgroups find their parts (each reads every row's visible count).  (1,024 decode
+// tiles of 1,000 to 4,000 tokens: 222 us cut, 212 whole; 256 of 8,000 to 16,000 run
+// at 5.6 TB/s cut, where whole ones wait for the longest.)
 constexpr int kCutTiles = 1024, kCutRows = 8192;
 
 // Tiles of one length are cut only where whole ones would leave more than 15% of
@@ -134,16 +132,11 @@ bool fills_badly(int64_t tiles) {
 }
 
 struct AttnPlan {
-    int sub_heads, num_subs, stream_rows;  // heads per workgroup, workgroups per kv head, rows per streaming tile
-    int few_rows;                          // requests of up to this many rows are streamed
-    int64_t slots;                         // row tiles of the streaming kernel's plain grid
-    int64_t cut_slots;                     // the same of its cut launch
-    int slots_per_req;                     // of the cut launch, dense
-    int tile_rows;                         // the tile kernel's
-    int64_t tile_slots;
-    bool stream, tile;
-    int64_t stream_bytes, tile_bytes;      // workspace of a cut launch, 0: not cut
-    int64_t bytes() const { return stream_bytes > tile_bytes ? stream_bytes : tile_bytes; }
+    bool stream;               // streaming kernel, else the tile kernel
+    int sub_heads, num_subs;   // streaming: heads per workgroup, workgroups per kv head
+    int tile_rows;             // query rows per tile
+    int64_t slots;             // row tiles
+    int64_t bytes;             // workspace of a cut launch, 0: not cut
 };
 
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
@@ -153,39 +146,30 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     p.num_subs = (group + qsa::kAttnTile - 1) / qsa::kAttnTile;
     p.sub_heads = (group + p.num_subs - 1) / p.num_subs;
     p.num_subs = (group + p.sub_heads - 1) / p.sub_heads;
-    p.stream_rows = sparse ? 1 : qsa::kAttnTile / p.sub_heads;
-    p.few_rows = group >= kStreamPairs ? 1 : kStreamPairs / group;
-    const int64_t heads = (int64_t)s->num_kv_heads * p.num_subs, T = p.stream_rows;
+    const int64_t heads = (int64_t)s->num_kv_heads * p.num_subs;
     const bool long_keys = keys > qsa::kStreamKeys * qsa::kStreamWaves;
     if (sparse) {
         p.stream = true;
-        p.slots = p.cut_slots = R;
+        p.tile_rows = 1;
+        p.slots = R;
         if (R <= qsa::kMaxSlots && R * heads <= kCutTiles && fills_badly(R * heads) && long_keys)
-            p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, R * heads);
+            p.bytes = qsa::attn_workspace_bytes(s->head_dim, R * heads);
         return p;
     }
-    // A small batch of few rows per request (on average: the lengths are on the
-    // device) is streamed whole; a launch of the tile kernel that finds nothing to do
-    // costs 5 us.
-    if (R > p.few_rows && R <= p.few_rows * n && R * group <= kSmallBatch && n * ((R + T - 1) / T) <= kSmallSlots)
-        p.few_rows = (int)R;
-    // with one request its rows are the call's rows, but for padding behind them
-    p.stream = n > 1 || R <= p.few_rows;
-    p.tile = R > p.few_rows;
+    // With at most four rows per request on average (a verify step), what one long
+    // request adds to a batch streamed whole stays below the others' part.  (64 requests
+    // of 4 rows, 8,000 to 16,000 tokens: 279 us streamed, 323 by the tile kernel.)
+    const int64_t few = group >= kStreamPairs ? 1 : kStreamPairs / group;
+    p.stream = R <= few * n && (R <= 4 * n || R * group <= kSmallPairs);
+    const int64_t T = p.tile_rows = p.stream ? qsa::kAttnTile / p.sub_heads : qsa::kTilePairs / group;
     p.slots = R / T + n;
-    const int64_t rows = p.few_rows < R ? p.few_rows : R, least = n < R ? n : R;
-    p.slots_per_req = (int)((rows + T - 1) / T);
-    p.cut_slots = p.slots_per_req * n;
-    const int64_t tiles = ((R + T - 1) / T > least ? (R + T - 1) / T : least) * heads;
-    if (p.stream && p.cut_slots <= qsa::kMaxSlots && tiles <= kCutTiles && long_keys)
-        p.stream_bytes = qsa::attn_workspace_bytes(s->head_dim, p.cut_slots * heads);
-    p.tile_rows = qsa::kTilePairs / group;
-    p.tile_slots = R / p.tile_rows + n;
-    const int64_t all = p.tile_slots * s->num_kv_heads;
-    const int64_t big = (R + p.tile_rows - 1) / p.tile_rows * s->num_kv_heads;
-    if (p.tile && (n > 1 || fills_badly(big)) && all <= kCutTiles && p.tile_slots <= qsa::kMaxSlots &&
-        n <= qsa::kMaxSlots && R <= kCutRows)
-        p.tile_bytes = qsa::attn_tile_workspace_bytes(s->head_dim, all);
+    const int64_t tile_heads = p.stream ? heads : s->num_kv_heads;
+    // tiles with rows: as many as requests or as full tiles, or some more
+    const int64_t least = n < R ? n : R, full = (R + T - 1) / T, tiles = (full > least ? full : least) * tile_heads;
+    if (p.slots > qsa::kMaxSlots || n > qsa::kMaxSlots || R > kCutRows || tiles > kCutTiles) return p;
+    if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.slots * heads);
+    if (!p.stream && (n > 1 || fills_badly(tiles)))
+        p.bytes = qsa::attn_tile_workspace_bytes(s->head_dim, p.slots * s->num_kv_heads);
     return p;
 }
 
@@ -292,16 +276,12 @@ qsa::AttnArgs attn_args(const void *q, const void *kcache, const void *vcache, c
     return a;
 }
 
-void stream_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
+void launch_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.sub_heads = p.sub_heads;
     a.num_subs = p.num_subs;
-    a.tile_rows = p.stream_rows;
-    // a cut launch gives every request as many slots as the longest needs; a plain
-    // one packs them, or its live workgroups would meet on a few XCDs
-    const bool cut = workspace && p.stream_bytes > 0;
-    a.part = cut ? static_cast<float *>(workspace) : nullptr;
-    a.slots = (int32_t)(cut ? p.cut_slots : p.slots);
-    a.slots_per_req = cut ? p.slots_per_req : 0;
+    a.tile_rows = p.tile_rows;
+    a.slots = (int32_t)p.slots;
+    a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
 }
 
 }  // namespace
@@ -363,7 +343,7 @@ qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, 
 
 int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *s) {
     if (check_attn_sizes(s, false, 0, 0) != QSA_OK || s->num_rows == 0) return 0;
-    return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes();
+    return plan_attn(s, false, (int64_t)s->max_blocks * s->block_size).bytes;
 }
 
 qsa_status qsa_paged_attention_check(const void *q, const void *kcache, const void *vcache,
@@ -386,28 +366,14 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
     qsa::AttnArgs a = attn_args(q, kcache, vcache, block_table, out, lse, s);
     a.ctx_lens = ctx_lens;
     a.q_starts = q_starts;
-    hipError_t e = hipSuccess;
-    if (p.tile) {
-        qsa::AttnArgs b = a;
-        b.tile_rows = p.tile_rows;
-        b.slots = (int32_t)p.tile_slots;
-        b.part = p.tile_bytes > 0 ? static_cast<float *>(workspace) : nullptr;
-        b.min_rows = p.stream ? p.few_rows + 1 : 1;
-        b.max_rows = s->num_rows;
-        e = qsa::launch_attn_tile(b, static_cast<hipStream_t>(stream));
-    }
-    if (e == hipSuccess && p.stream) {
-        stream_shape(a, p, workspace);
-        a.min_rows = 1;
-        a.max_rows = p.tile ? p.few_rows : s->num_rows;
-        e = qsa::launch_attn_stream(a, false, static_cast<hipStream_t>(stream));
-    }
-    return launched(e);
+    launch_shape(a, p, workspace);
+    return launched(p.stream ? qsa::launch_attn_stream(a, false, static_cast<hipStream_t>(stream))
+                             : qsa::launch_attn_tile(a, static_cast<hipStream_t>(stream)));
 }
 
 int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *s, int32_t k, int32_t ratio) {
     if (check_attn_sizes(s, true, k, ratio) != QSA_OK || s->num_rows == 0) return 0;
-    return plan_attn(s, true, (int64_t)k * ratio).bytes();
+    return plan_attn(s, true, (int64_t)k * ratio).bytes;
 }
 
 qsa_status qsa_sparse_attention_check(const void *q, const void *kcache, const void *vcache,
@@ -434,7 +400,7 @@ qsa_status qsa_sparse_attention(const void *q, const void *kcache, const void *v
     a.idx = idx;
     a.k = k;
     a.ratio = ratio;
-    stream_shape(a, p, workspace);
+    launch_shape(a, p, workspace);
     return launched(qsa::launch_attn_stream(a, true, static_cast<hipStream_t>(stream)));
 }
 

@@ -254,33 +254,24 @@ __device__ __forceinline__ int64_t kv_offset(const AttnArgs &a, uint32_t block, 
 // The request that takes row tile `slot`, and the tile's first row: request i,
 // rows [s_i, s_{i+1}), owns the slots from s_i / T + i on.  These are strictly
 // increasing in i and leave room for ceil(len / T) tiles each, so no prefix sum
-// over the requests is needed.  Returns false for a slot without rows.
-//
-// Where the launch takes only requests of few rows, slots_per_req > 0 gives
-// every request that many slots instead.
+// over the requests is needed.
 struct RowTile {
     int req, row0, rows;
 };
 __device__ __forceinline__ int request_start(const AttnArgs &a, int i) { return min(max(a.q_starts[i], 0), a.num_rows); }
+__device__ __forceinline__ int visible(const AttnArgs &a, int row) { return min(max(a.ctx_lens[row], 0), a.cap); }
 
-// tile j of request `req`
-__device__ __forceinline__ bool request_tile(const AttnArgs &a, int req, int j, RowTile &t) {
-    const int s0 = request_start(a, req), s1 = request_start(a, req + 1), rows = s1 - s0;
+// the tile of `slot` among the rows [s0, s1) of request req; rows 0: none
+__device__ __forceinline__ RowTile request_tile(const AttnArgs &a, int req, int s0, int s1, int slot) {
+    const int j = slot - (s0 / a.tile_rows + req);
     const int64_t row0 = (int64_t)s0 + (int64_t)j * a.tile_rows;
-    if (j < 0 || row0 >= s1 || rows < a.min_rows || rows > a.max_rows) return false;
-    t.req = req;
-    t.row0 = (int)row0;
-    t.rows = min(a.tile_rows, s1 - (int)row0);
-    return true;
-}
-// slots_per_req > 0
-__device__ __forceinline__ bool slot_tile(const AttnArgs &a, int slot, RowTile &t) {
-    const int req = slot / a.slots_per_req;
-    return request_tile(a, req, slot - req * a.slots_per_req, t);
+    RowTile t = {req, (int)row0, 0};
+    if (j >= 0 && row0 < s1) t.rows = min(a.tile_rows, s1 - t.row0);
+    return t;
 }
 
+// by one wave: false for a slot without rows
 __device__ __forceinline__ bool find_tile(const AttnArgs &a, int slot, RowTile &t) {
-    if (a.slots_per_req > 0) return slot_tile(a, slot, t);
     const int T = a.tile_rows, lane = lane_id();
     // 64-way search for the last i in [0, num_reqs) with start(i) / T + i <= slot
     int lo = 0, len = a.num_reqs;
@@ -293,7 +284,67 @@ __device__ __forceinline__ bool find_tile(const AttnArgs &a, int slot, RowTile &
         lo += last * step;
         len = min(step, len - last * step);
     }
-    return request_tile(a, lo, slot - (request_start(a, lo) / T + lo), t);
+    t = request_tile(a, lo, request_start(a, lo), request_start(a, lo + 1), slot);
+    return t.rows > 0;
+}
+
+// The same by one thread, from the requests' first rows in LDS.
+__device__ __forceinline__ RowTile find_tile(const AttnArgs &a, const int32_t *starts, int slot) {
+    int lo = 0, hi = a.num_reqs;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (starts[mid] / a.tile_rows + mid <= slot) lo = mid;
+        else hi = mid;
+    }
+    return request_tile(a, lo, starts[lo], starts[lo + 1], slot);
+}
+
+// By a whole workgroup: the requests' first rows into LDS, and each slot's largest
+// visible count, or -1 for a slot without rows.
+template <int THREADS>
+__device__ __forceinline__ void slot_counts(const AttnArgs &a, int32_t *starts, int32_t *counts) {
+    const int t = threadIdx.x, n = a.num_reqs, T = a.tile_rows;
+    for (int i = t; i <= n; i += THREADS) starts[i] = request_start(a, i);
+    for (int i = t; i <= a.slots; i += THREADS) counts[i] = -1;
+    __syncthreads();
+    const int per = (a.num_rows + THREADS - 1) / THREADS, r0 = t * per, r1 = min(r0 + per, a.num_rows);
+    int req = 0;
+    for (int hi = n; hi - req > 1;) {  // the last request with starts[req] <= r0
+        const int mid = (req + hi) >> 1;
+        if (starts[mid] <= r0) req = mid;
+        else hi = mid;
+    }
+    for (int r = r0; r < r1; ++r) {
+        while (req < n && r >= starts[req + 1]) ++req;
+        if (req >= n) break;
+        const int s = starts[req];
+        if (r >= s) atomicMax(&counts[s / T + req + (r - s) / T], visible(a, r));
+    }
+    __syncthreads();
+}
+
+// Exclusive prefix sums over the slots, kPer consecutive ones per thread: before[i]
+// is the sum of the slots before i, before[slots] the total.
+template <int THREADS>
+__device__ __forceinline__ void slot_sums(int32_t *before, int slots, const int32_t (&u)[kMaxSlots / THREADS],
+                                          int32_t *wave_sums) {
+    constexpr int kPer = kMaxSlots / THREADS;
+    const int t = threadIdx.x;
+    int sum = 0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) sum += u[i];
+    const int inc = wave_incl_sum(sum);
+    if ((t & 63) == 63) wave_sums[t >> 6] = inc;
+    __syncthreads();
+    int at = inc - sum;
+    for (int i = 0; i < (t >> 6); ++i) at += wave_sums[i];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (t * kPer + i <= slots) before[t * kPer + i] = at;
+        at += u[i];
+    }
+    if (t == THREADS - 1 && slots == kMaxSlots) before[slots] = at;
+    __syncthreads();
 }
 
 __device__ __forceinline__ float wave_sum_f(float v) {
@@ -352,10 +403,9 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
 
 // Joins the parts of a cut tile for one pair, D / 4 threads to a pair with 4 output
 // elements each: the parts' states (outputs [PAIRS][D], references, sums) are read 8
-// parts at a time, all of a batch on their way at once.  Part 0 is at p0, part i at
-// p1 + (i - 1) stride.
+// parts at a time, all of a batch on their way at once.  Part i is at p + i stride.
 template <int DT, int D, int PAIRS>
-__device__ __forceinline__ void join_parts(const float *p0, const float *p1, int64_t stride, int used, int m, int d0,
+__device__ __forceinline__ void join_parts(const float *parts, int64_t stride, int used, int m, int d0,
                                            typename Half<DT>::T *out, float *lse) {
     constexpr int kBatch = 8;
     typedef typename Half<DT>::T T;
@@ -367,8 +417,7 @@ __device__ __forceinline__ void join_parts(const float *p0, const float *p1, int
         f32x4 x[kBatch];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const int k = min(i + j, used - 1);
-            const float *p = k == 0 ? p0 : p1 + (k - 1) * stride;
+            const float *p = parts + min(i + j, used - 1) * stride;
             ref[j] = p[PAIRS * D + m];
             l[j] = p[PAIRS * (D + 1) + m];
             x[j] = *reinterpret_cast<const f32x4 *>(p + m * D + d0);

@@ -53,11 +53,9 @@ struct AttnArgs {
     int32_t div_shift;
     // launch shape
     int32_t slots;              // row tiles of the grid
-    int32_t slots_per_req;      // dense: > 0 where every request has that many, else 0: packed
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile
-    int32_t min_rows, max_rows; // dense: the requests this launch takes, by their row count
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);

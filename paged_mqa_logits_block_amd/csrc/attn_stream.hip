@@ -80,8 +80,6 @@ __device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, T
     return true;
 }
 
-__device__ __forceinline__ int visible(const AttnArgs &a, int row) { return min(max(a.ctx_lens[row], 0), a.cap); }
-
 // keys the tile works through: the largest visible count of its rows, or the
 // selected tokens
 template <bool SPARSE>
@@ -417,35 +415,25 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
     typedef Stream<DT, D, SPARSE> S;
     __shared__ typename S::Shared sh;
     __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
-    __shared__ int32_t wave_sums[kStreamWaves];
-    const int t = threadIdx.x, lane = t & 63, g = blockIdx.x;
+    __shared__ int32_t starts[SPARSE ? 1 : kMaxSlots + 1], wave_sums[kStreamWaves];
+    const int t = threadIdx.x, g = blockIdx.x;
     const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
-    if (SPARSE) {
+    if constexpr (SPARSE) {
         const int u = units_of(a.k * a.ratio);
         for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
-    } else {
-        constexpr int kPer = kMaxSlots / kStreamThreads;
-        int u[kPer], sum = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const int slot = t * kPer + i;
-            RowTile w;
-            u[i] = slot < slots && slot_tile(a, slot, w) ? units_of(tile_keys<false>(a, w.row0, w.rows)) : 0;
-            sum += u[i];
-        }
-        const int inc = wave_incl_sum(sum);
-        if (lane == 63) wave_sums[t >> 6] = inc;
         __syncthreads();
-        int at = inc - sum;
-        for (int i = 0; i < (t >> 6); ++i) at += wave_sums[i];
+    } else {
+        slot_counts<kStreamThreads>(a, starts, before);
+        constexpr int kPer = kMaxSlots / kStreamThreads;
+        int u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            if (t * kPer + i <= slots) before[t * kPer + i] = at;
-            at += u[i];
+            const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
+            u[i] = keys < 0 ? 0 : units_of(keys);
         }
-        if (t == kStreamThreads - 1 && slots == kMaxSlots) before[slots] = at;
+        __syncthreads();
+        slot_sums<kStreamThreads>(before, slots, u, wave_sums);
     }
-    __syncthreads();
     const int per_head = before[slots];
     const int64_t total = (int64_t)per_head * hss;
     if (g > 0 && g >= groups_of(total)) return;
@@ -458,8 +446,8 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
             if (u1 > u0) {
                 s.first = group_of(u0, total);
                 s.last = group_of(u1 - 1, total);
-                RowTile w;
-                if (!SPARSE && slot_tile(a, slot, w)) {
+                if constexpr (!SPARSE) {
+                    const RowTile w = find_tile(a, starts, slot);
                     s.row0 = w.row0;
                     s.rows = w.rows;
                 }
@@ -483,7 +471,15 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
         const int64_t tile0 = (int64_t)hs * per_head + before[slot], tile1 = (int64_t)hs * per_head + before[slot + 1];
         const int64_t stop = min(end, tile1);
         TileWork w;
-        tile_work<SPARSE>(a, slot, hs, w);
+        if constexpr (SPARSE) {
+            tile_work<SPARSE>(a, slot, hs, w);
+        } else {
+            part_heads(a, hs, w);
+            const RowTile r = find_tile(a, starts, slot);
+            w.req = __builtin_amdgcn_readfirstlane(r.req);
+            w.row0 = __builtin_amdgcn_readfirstlane(r.row0);
+            w.rows = __builtin_amdgcn_readfirstlane(r.rows);
+        }
         const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w.row0, w.rows));
         const int steps = (keys + kStreamKeys - 1) / kStreamKeys;
         const int t0 = __builtin_amdgcn_readfirstlane((int)(u - tile0) * kStreamWaves);
@@ -511,7 +507,7 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
     const float *p = part_of<D>(a, s.first, tile);
     constexpr int kPart = kAttnTile * (D + 2);
     join_parts<DT, D, kAttnTile>(
-        p, p + kPart, kPart, s.last - s.first + 1, m, 4 * (threadIdx.x % (D / 4)),
+        p, kPart, s.last - s.first + 1, m, 4 * (threadIdx.x % (D / 4)),
         static_cast<typename Half<DT>::T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head,
         a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }

@@ -117,12 +117,18 @@ __device__ __forceinline__ void multiply(const uint8_t *vb, const uint8_t *kb, c
 // the last on: a chunk's last rows see the most keys.
 constexpr int kXcds = 8;
 __host__ __device__ __forceinline__ int head_classes(int heads) { return heads % 8 == 0 ? 8 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1; }
-__device__ __forceinline__ bool place_of(const AttnArgs &a, int id, int &hk, int &slot) {
+// workgroup `id` of a launch with per_head workgroups for each kv head: its head and
+// its place among the head's
+__device__ __forceinline__ bool place_of(const AttnArgs &a, int per_head, int id, int &hk, int &at) {
     const int classes = head_classes(a.num_kv_heads), x = id % kXcds, j = id / kXcds * (kXcds / classes) + x / classes;
-    const int i = j / a.slots;
+    const int i = j / per_head;
     hk = x % classes + classes * i;
-    slot = a.slots - 1 - (j - i * a.slots);
+    at = per_head - 1 - (j - i * per_head);
     return hk < a.num_kv_heads;
+}
+inline unsigned place_grid(int num_kv_heads, int64_t per_head) {
+    const int classes = head_classes(num_kv_heads), share = kXcds / classes;  // XCDs per class of heads
+    return (unsigned)((per_head * (num_kv_heads / classes) + share - 1) / share * kXcds);
 }
 
 // WHOLE: the block size is a multiple of 8, so that the 8 keys that a wave copies in
@@ -374,159 +380,107 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) 
     __shared__ TileShared<D> sh;
     int hk, slot;
     RowTile w;
-    if (!place_of(a, blockIdx.x, hk, slot) || !find_tile(a, slot, w)) return;
+    if (!place_of(a, a.slots, blockIdx.x, hk, slot) || !find_tile(a, slot, w)) return;
     w.req = __builtin_amdgcn_readfirstlane(w.req);
     run_steps<DT, D, WHOLE>(a, sh, w, hk, 0, 0x7FFFFFFF, nullptr);
 }
 
-// Balanced launch: the tiles' steps laid end to end, kv head by kv head, and cut
-// into equal parts for one workgroup per CU, of kLeastSteps steps at least.  A
-// workgroup has at most two cut tiles, its first and its last: part 2 g of the
-// workspace is the state of workgroup g's first tile, part 2 g + 1 that of a last
-// tile that begins in its range.
+// Cut launch: every tile's steps are cut into pieces of about `piece` steps, one per
+// workgroup, with `piece` chosen from the tiles' total so that there are about as
+// many pieces as CUs; a tile of up to that many steps stays whole.  (Equal parts of
+// the whole line, as in the streaming kernel, would give most workgroups two
+// tiles here, each with the start and the end of a tile's work.)  Pieces of cut
+// tiles leave their states in the workspace, at most 2 kStreamGroups of them: a cut
+// tile's pieces are more than half of `piece` long.
 constexpr int kLeastSteps = 4;
-__device__ __forceinline__ int tile_groups(int64_t total) {
-    return (int)min((total + kLeastSteps - 1) / kLeastSteps, (int64_t)kStreamGroups);
-}
-__device__ __forceinline__ int64_t first_step(int g, int64_t total) { return g * total / tile_groups(total); }
 
 struct TileSpan {
-    int first, last;  // workgroups with parts of the tile
-    int place;        // 0 or 1: its state is the first or the second part of workgroup `first`
+    int first, pieces;  // places of a cut tile's states
     int row0, rows;
-    int unused;
 };
 
 template <int DT, int D, bool WHOLE>
-__global__ __launch_bounds__(kTileThreads, 2) void attn_tile_balanced_kernel(AttnArgs a) {
+__global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs a) {
     __shared__ TileShared<D> sh;
-    __shared__ int32_t before[kMaxSlots + 1];  // steps of the slots before; while they are made, keys of the slot
-    __shared__ int32_t starts[kMaxSlots + 1];  // first row of each request
-    __shared__ int32_t wave_sums[kTileWaves];
-    const int t = threadIdx.x, lane = t & 63, slots = a.slots, n = a.num_reqs, T = a.tile_rows;
-    // workgroup ids go to the XCDs in turn: each XCD takes one stretch of the line
-    const int g = (int)(blockIdx.x % kXcds) * (kStreamGroups / kXcds) + (int)(blockIdx.x / kXcds);
-    for (int i = t; i <= n; i += kTileThreads) starts[i] = request_start(a, i);
-    for (int i = t; i <= slots; i += kTileThreads) before[i] = -1;
-    __syncthreads();
-    const auto request_of_slot = [&](int slot) {  // the last i with starts[i] / T + i <= slot
-        int lo = 0, hi = n;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (starts[mid] / T + mid <= slot) lo = mid;
-            else hi = mid;
-        }
-        return lo;
-    };
-    {  // each slot's largest visible count, from a run of rows per thread
-        const int per = (a.num_rows + kTileThreads - 1) / kTileThreads;
-        const int r0 = t * per, r1 = min(r0 + per, a.num_rows);
-        int req = 0;
-        if (r0 < r1) {
-            int hi = n;  // the last request with starts[req] <= r0
-            while (hi - req > 1) {
-                const int mid = (req + hi) >> 1;
-                if (starts[mid] <= r0) req = mid;
-                else hi = mid;
-            }
-        }
-        for (int r = r0; r < r1; ++r) {
-            while (req < n && r >= starts[req + 1]) ++req;
-            if (req >= n) break;
-            const int s = starts[req], len = starts[req + 1] - s;
-            if (r >= s && len >= a.min_rows && len <= a.max_rows)
-                atomicMax(&before[s / T + req + (r - s) / T], min(max(a.ctx_lens[r], 0), a.cap));
-        }
-    }
-    __syncthreads();
+    __shared__ int32_t before[kMaxSlots + 1];      // pieces of the slots before
+    __shared__ int32_t cut_before[kMaxSlots + 1];  // pieces of cut tiles in the slots before
+    __shared__ int32_t steps_of[kMaxSlots + 1];    // steps of the slot; first its largest visible count
+    __shared__ int32_t starts[kMaxSlots + 1], wave_sums[kTileWaves], sums[2];
+    const int t = threadIdx.x, slots = a.slots;
     constexpr int kPer = kMaxSlots / kTileThreads;
-    int u[kPer], sum = 0;
+    if (t < 2) sums[t] = 0;
+    slot_counts<kTileThreads>(a, starts, steps_of);
+    int u[kPer], steps = 0, tiles = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
+        const int slot = t * kPer + i, keys = slot < slots ? steps_of[slot] : -1;
         u[i] = keys < 0 ? 0 : max((keys + kTileKeys - 1) / kTileKeys, 1);  // rows that see nothing are written too
-        sum += u[i];
+        steps += u[i];
+        tiles += keys >= 0;
     }
-    const int inc = wave_incl_sum(sum);
-    if (lane == 63) wave_sums[t >> 6] = inc;
+    steps = wave_total_sum(steps);
+    tiles = wave_total_sum(tiles);
+    if ((t & 63) == 0) {
+        atomicAdd(&sums[0], steps);
+        atomicAdd(&sums[1], tiles);
+    }
     __syncthreads();
-    int at = inc - sum;
-    for (int i = 0; i < (t >> 6); ++i) at += wave_sums[i];
+    // pieces are total / piece and about half a piece more per tile
+    const int64_t total = (int64_t)sums[0] * a.num_kv_heads, half = (int64_t)sums[1] * a.num_kv_heads / 2;
+    const int room = (int)max((int64_t)kStreamGroups - half, (int64_t)kStreamGroups / 4);
+    const int piece = (int)max((total + room - 1) / room, (int64_t)kLeastSteps);
+    int c[kPer], cut[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        if (t * kPer + i <= slots) before[t * kPer + i] = at;
-        at += u[i];
+        const int slot = t * kPer + i;
+        if (slot < slots) steps_of[slot] = u[i];
+        c[i] = (u[i] + piece - 1) / piece;
+        cut[i] = c[i] > 1 ? c[i] : 0;
     }
-    if (t == kTileThreads - 1 && slots == kMaxSlots) before[slots] = at;
-    __syncthreads();
-    const int per_head = before[slots];
-    const int64_t total = (int64_t)per_head * a.num_kv_heads;
-    const int groups = tile_groups(total);
-    const auto tile_of = [&](int slot) {
-        RowTile w;
-        const int req = request_of_slot(slot);
-        w.req = req;
-        const int j = slot - (starts[req] / T + req);
-        w.row0 = starts[req] + j * T;
-        w.rows = j < 0 ? 0 : min(T, starts[req + 1] - w.row0);
-        return w;
-    };
+    slot_sums<kTileThreads>(before, slots, c, wave_sums);
+    slot_sums<kTileThreads>(cut_before, slots, cut, wave_sums);
+    const int per_head = before[slots], cut_per_head = cut_before[slots];
+
     TileSpan *spans = reinterpret_cast<TileSpan *>(a.part + (int64_t)2 * kStreamGroups * kTilePart<D>);
     for (int i = (int)blockIdx.x * kTileThreads + t; i < slots * a.num_kv_heads; i += (int)gridDim.x * kTileThreads) {
         const int hk = i / slots, slot = i - hk * slots;
-        const int64_t u0 = (int64_t)hk * per_head + before[slot], u1 = (int64_t)hk * per_head + before[slot + 1];
-        TileSpan s = {0, 0, 0, 0, 0, 0};
-        if (u1 > u0) {
-            s.first = (int)(((u0 + 1) * groups + total - 1) / total) - 1;
-            s.last = (int)((u1 * groups + total - 1) / total) - 1;
-            s.place = first_step(s.first, total) < u0;
-            const RowTile w = tile_of(slot);
+        TileSpan s = {hk * cut_per_head + cut_before[slot], cut_before[slot + 1] - cut_before[slot], 0, 0};
+        if (s.pieces > 0) {
+            const RowTile w = find_tile(a, starts, slot);
             s.row0 = w.row0;
             s.rows = w.rows;
         }
         spans[i] = s;
     }
-    if (g >= groups) return;
-    int64_t at_step = first_step(g, total);
-    const int64_t begin = at_step, end = first_step(g + 1, total);
-    while (at_step < end) {
-        const int hk = __builtin_amdgcn_readfirstlane((int)(at_step / per_head));
-        const int in_head = (int)(at_step - (int64_t)hk * per_head);
-        int slot = 0, hi = slots;  // the slot with before[slot] <= in_head < before[slot + 1]
-        while (hi - slot > 1) {
-            const int mid = (slot + hi) >> 1;
-            if (before[mid] <= in_head) slot = mid;
-            else hi = mid;
-        }
-        slot = __builtin_amdgcn_readfirstlane(slot);
-        const int64_t tile0 = (int64_t)hk * per_head + before[slot], tile1 = (int64_t)hk * per_head + before[slot + 1];
-        const int64_t stop = min(end, tile1);
-        RowTile w = tile_of(slot);
-        w.req = __builtin_amdgcn_readfirstlane(w.req);
-        w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
-        w.rows = __builtin_amdgcn_readfirstlane(w.rows);
-        float *dest = at_step == tile0 && stop == tile1
-                          ? nullptr
-                          : a.part + (int64_t)(2 * g + (tile0 > begin)) * kTilePart<D>;
-        run_steps<DT, D, WHOLE>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)(at_step - tile0)),
-                                __builtin_amdgcn_readfirstlane((int)(stop - tile0)), dest);
-        at_step = stop;
-        __syncthreads();  // all waves are done with the shared parts
+    int hk, at;
+    if (per_head == 0 || !place_of(a, per_head, blockIdx.x, hk, at)) return;
+    int slot = 0, hi = slots;  // the slot with before[slot] <= at < before[slot + 1]
+    while (hi - slot > 1) {
+        const int mid = (slot + hi) >> 1;
+        if (before[mid] <= at) slot = mid;
+        else hi = mid;
     }
+    slot = __builtin_amdgcn_readfirstlane(slot);
+    const int n = before[slot + 1] - before[slot], j = at - before[slot], all = steps_of[slot];
+    RowTile w = find_tile(a, starts, slot);
+    w.req = __builtin_amdgcn_readfirstlane(w.req);
+    w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
+    w.rows = __builtin_amdgcn_readfirstlane(w.rows);
+    float *dest = n > 1 ? a.part + (int64_t)(hk * cut_per_head + cut_before[slot] + j) * kTilePart<D> : nullptr;
+    run_steps<DT, D, WHOLE>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)((int64_t)all * j / n)),
+                            __builtin_amdgcn_readfirstlane((int)((int64_t)all * (j + 1) / n)), dest);
 }
 
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void attn_tile_join_kernel(AttnArgs a) {
     const TileSpan s = reinterpret_cast<const TileSpan *>(a.part + (int64_t)2 * kStreamGroups * kTilePart<D>)[blockIdx.x];
-    if (s.last <= s.first) return;
+    if (s.pieces <= 1) return;
     constexpr int kPairs = kJoinThreads / (D / 4);
     const int hk = blockIdx.x / a.slots, m = blockIdx.y * kPairs + threadIdx.x / (D / 4), r = m / a.group;
     if (r >= s.rows) return;
     const int row = s.row0 + r, head = hk * a.group + (m - r * a.group);
-    const float *p0 = a.part + (int64_t)(2 * s.first + s.place) * kTilePart<D>;
-    const float *p1 = a.part + (int64_t)(2 * s.first + 2) * kTilePart<D>;
     join_parts<DT, D, kTilePairs>(
-        p0, p1, 2 * kTilePart<D>, s.last - s.first + 1, m, 4 * (threadIdx.x % (D / 4)),
+        a.part + (int64_t)s.first * kTilePart<D>, kTilePart<D>, s.pieces, m, 4 * (threadIdx.x % (D / 4)),
         static_cast<typename Half<DT>::T *>(a.out) + row * a.o_row + head * a.o_head,
         a.lse ? a.lse + (int64_t)row * (a.num_kv_heads * a.group) + head : nullptr);
 }
@@ -534,13 +488,14 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tile_join_kernel(AttnArgs a
 template <int DT, int D, bool WHOLE>
 hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
     if (!a.part) {
-        const int classes = head_classes(a.num_kv_heads), share = kXcds / classes;  // XCDs per class of heads
-        const int64_t tiles = (int64_t)a.slots * (a.num_kv_heads / classes);
-        hipLaunchKernelGGL((attn_tile_kernel<DT, D, WHOLE>), dim3((unsigned)((tiles + share - 1) / share * kXcds)),
+        hipLaunchKernelGGL((attn_tile_kernel<DT, D, WHOLE>), dim3(place_grid(a.num_kv_heads, a.slots)),
                            dim3(kTileThreads), 0, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((attn_tile_balanced_kernel<DT, D, WHOLE>), dim3(kStreamGroups), dim3(kTileThreads), 0, s, a);
+    // at most kStreamGroups pieces and one more per tile
+    const int64_t per_head = a.slots + kStreamGroups / a.num_kv_heads + 1;
+    hipLaunchKernelGGL((attn_tile_cut_kernel<DT, D, WHOLE>), dim3(place_grid(a.num_kv_heads, per_head)),
+                       dim3(kTileThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_tile_join_kernel<DT, D>),
