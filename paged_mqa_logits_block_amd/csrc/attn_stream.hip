@@ -415,15 +415,16 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
     typedef Stream<DT, D, SPARSE> S;
     __shared__ typename S::Shared sh;
     __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
-    __shared__ int32_t starts[SPARSE ? 1 : kMaxSlots + 1], wave_sums[kStreamWaves];
+    __shared__ int32_t wave_sums[kStreamWaves];
     const int t = threadIdx.x, g = blockIdx.x;
     const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
+    __shared__ Requests requests;  // dense only
     if constexpr (SPARSE) {
         const int u = units_of(a.k * a.ratio);
         for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
         __syncthreads();
     } else {
-        slot_counts<kStreamThreads>(a, starts, before);
+        slot_counts<kStreamThreads>(a, requests, before);
         constexpr int kPer = kMaxSlots / kStreamThreads;
         int u[kPer];
 #pragma unroll
@@ -447,7 +448,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
                 s.first = group_of(u0, total);
                 s.last = group_of(u1 - 1, total);
                 if constexpr (!SPARSE) {
-                    const RowTile w = find_tile(a, starts, slot);
+                    const RowTile w = find_tile(a, requests, slot);
                     s.row0 = w.row0;
                     s.rows = w.rows;
                 }
@@ -475,7 +476,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_balanced_kernel(AttnAr
             tile_work<SPARSE>(a, slot, hs, w);
         } else {
             part_heads(a, hs, w);
-            const RowTile r = find_tile(a, starts, slot);
+            const RowTile r = find_tile(a, requests, slot);
             w.req = __builtin_amdgcn_readfirstlane(r.req);
             w.row0 = __builtin_amdgcn_readfirstlane(r.row0);
             w.rows = __builtin_amdgcn_readfirstlane(r.rows);

@@ -405,11 +405,12 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
     __shared__ int32_t before[kMaxSlots + 1];      // pieces of the slots before
     __shared__ int32_t cut_before[kMaxSlots + 1];  // pieces of cut tiles in the slots before
     __shared__ int32_t steps_of[kMaxSlots + 1];    // steps of the slot; first its largest visible count
-    __shared__ int32_t starts[kMaxSlots + 1], wave_sums[kTileWaves], sums[2];
+    __shared__ int32_t wave_sums[kTileWaves], sums[2];
+    __shared__ Requests requests;
     const int t = threadIdx.x, slots = a.slots;
     constexpr int kPer = kMaxSlots / kTileThreads;
     if (t < 2) sums[t] = 0;
-    slot_counts<kTileThreads>(a, starts, steps_of);
+    slot_counts<kTileThreads>(a, requests, steps_of);
     int u[kPer], steps = 0, tiles = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -446,7 +447,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
         const int hk = i / slots, slot = i - hk * slots;
         TileSpan s = {hk * cut_per_head + cut_before[slot], cut_before[slot + 1] - cut_before[slot], 0, 0};
         if (s.pieces > 0) {
-            const RowTile w = find_tile(a, starts, slot);
+            const RowTile w = find_tile(a, requests, slot);
             s.row0 = w.row0;
             s.rows = w.rows;
         }
@@ -462,7 +463,7 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
     }
     slot = __builtin_amdgcn_readfirstlane(slot);
     const int n = before[slot + 1] - before[slot], j = at - before[slot], all = steps_of[slot];
-    RowTile w = find_tile(a, starts, slot);
+    RowTile w = find_tile(a, requests, slot);
     w.req = __builtin_amdgcn_readfirstlane(w.req);
     w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
     w.rows = __builtin_amdgcn_readfirstlane(w.rows);
