@@ -167,6 +167,8 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     // tiles with rows: as many as requests or as full tiles, or some more
     const int64_t least = n < R ? n : R, full = (R + T - 1) / T, tiles = (full > least ? full : least) * tile_heads;
     if (p.slots > qsa::kMaxSlots || n > qsa::kMaxSlots || R > kCutRows || tiles > kCutTiles) return p;
+    // the workgroups add up the slots' steps of 64 keys in 32 bits
+    if (p.slots * (keys / 64 + 1) > 0x7FFFFFFF) return p;
     if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.slots * heads);
     if (!p.stream && (n > 1 || fills_badly(tiles)))
         p.bytes = qsa::attn_tile_workspace_bytes(s->head_dim, p.slots * s->num_kv_heads);

@@ -402,9 +402,10 @@ struct TileSpan {
 template <int DT, int D, bool WHOLE>
 __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs a) {
     __shared__ TileShared<D> sh;
-    __shared__ int32_t before[kMaxSlots + 1];      // pieces of the slots before
-    __shared__ int32_t cut_before[kMaxSlots + 1];  // pieces of cut tiles in the slots before
-    __shared__ int32_t steps_of[kMaxSlots + 1];    // steps of the slot; first its largest visible count
+    // pieces of the slots before (at most 1,280), and, shifted by 16, those of cut tiles
+    // among them (at most 512)
+    __shared__ int32_t before[kMaxSlots + 1];
+    __shared__ int32_t steps_of[kMaxSlots + 1];  // steps of the slot; first its largest visible count
     __shared__ int32_t wave_sums[kTileWaves], sums[2];
     __shared__ Requests requests;
     const int t = threadIdx.x, slots = a.slots;
@@ -426,26 +427,29 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
         atomicAdd(&sums[1], tiles);
     }
     __syncthreads();
-    // pieces are total / piece and about half a piece more per tile
-    const int64_t total = (int64_t)sums[0] * a.num_kv_heads, half = (int64_t)sums[1] * a.num_kv_heads / 2;
-    const int room = (int)max((int64_t)kStreamGroups - half, (int64_t)kStreamGroups / 4);
-    const int piece = (int)max((total + room - 1) / room, (int64_t)kLeastSteps);
-    int c[kPer], cut[kPer];
+    // pieces are total / piece and about half a piece more per tile; rounded up, so
+    // that total / piece is below `room` also where the quotient is off by a rounding
+    const float total = (float)sums[0] * (float)a.num_kv_heads;
+    const int half = (int)min((int64_t)sums[1] * a.num_kv_heads / 2, (int64_t)kStreamGroups);
+    const int room = max(kStreamGroups - half, kStreamGroups / 4);
+    const int piece = max((int)(total / (float)room * 1.000001f) + 1, kLeastSteps);
+    int c[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int slot = t * kPer + i;
         if (slot < slots) steps_of[slot] = u[i];
         c[i] = (u[i] + piece - 1) / piece;
-        cut[i] = c[i] > 1 ? c[i] : 0;
+        c[i] |= c[i] > 1 ? c[i] << 16 : 0;
     }
     slot_sums<kTileThreads>(before, slots, c, wave_sums);
-    slot_sums<kTileThreads>(cut_before, slots, cut, wave_sums);
-    const int per_head = before[slots], cut_per_head = cut_before[slots];
+    const auto pieces_before = [&](int slot) { return before[slot] & 0xFFFF; };
+    const auto cut_before = [&](int slot) { return before[slot] >> 16; };
+    const int per_head = pieces_before(slots), cut_per_head = cut_before(slots);
 
     TileSpan *spans = reinterpret_cast<TileSpan *>(a.part + (int64_t)2 * kStreamGroups * kTilePart<D>);
     for (int i = (int)blockIdx.x * kTileThreads + t; i < slots * a.num_kv_heads; i += (int)gridDim.x * kTileThreads) {
         const int hk = i / slots, slot = i - hk * slots;
-        TileSpan s = {hk * cut_per_head + cut_before[slot], cut_before[slot + 1] - cut_before[slot], 0, 0};
+        TileSpan s = {hk * cut_per_head + cut_before(slot), cut_before(slot + 1) - cut_before(slot), 0, 0};
         if (s.pieces > 0) {
             const RowTile w = find_tile(a, requests, slot);
             s.row0 = w.row0;
@@ -455,19 +459,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
     }
     int hk, at;
     if (per_head == 0 || !place_of(a, per_head, blockIdx.x, hk, at)) return;
-    int slot = 0, hi = slots;  // the slot with before[slot] <= at < before[slot + 1]
+    int slot = 0, hi = slots;  // the last slot with at most `at` pieces before it
     while (hi - slot > 1) {
         const int mid = (slot + hi) >> 1;
-        if (before[mid] <= at) slot = mid;
+        if (pieces_before(mid) <= at) slot = mid;
         else hi = mid;
     }
     slot = __builtin_amdgcn_readfirstlane(slot);
-    const int n = before[slot + 1] - before[slot], j = at - before[slot], all = steps_of[slot];
+    const int n = pieces_before(slot + 1) - pieces_before(slot), j = at - pieces_before(slot), all = steps_of[slot];
     RowTile w = find_tile(a, requests, slot);
     w.req = __builtin_amdgcn_readfirstlane(w.req);
     w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
     w.rows = __builtin_amdgcn_readfirstlane(w.rows);
-    float *dest = n > 1 ? a.part + (int64_t)(hk * cut_per_head + cut_before[slot] + j) * kTilePart<D> : nullptr;
+    float *dest = n > 1 ? a.part + (int64_t)(hk * cut_per_head + cut_before(slot) + j) * kTilePart<D> : nullptr;
     run_steps<DT, D, WHOLE>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)((int64_t)all * j / n)),
                             __builtin_amdgcn_readfirstlane((int)((int64_t)all * (j + 1) / n)), dest);
 }

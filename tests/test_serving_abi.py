@@ -129,6 +129,10 @@ def test_attention_workspace():
     assert m.sparse_attention_workspace_bytes(s, 2048, 4) > 0
     assert m.sparse_attention_workspace_bytes(attn_shape(num_rows=4096), 2048, 4) == 0
     assert m.sparse_attention_workspace_bytes(s, 0, 4) == 0
+    # tables whose steps do not add up in 32 bits are not cut
+    big = dict(num_rows=500, num_reqs=500, block_size=1024)
+    assert m.paged_attention_workspace_bytes(attn_shape(max_blocks=1 << 17, **big)) > 0
+    assert m.paged_attention_workspace_bytes(attn_shape(max_blocks=1 << 19, **big)) == 0
     # shapes that the calls refuse need none, and the queries do not fail on them
     for kw in (dict(num_heads=4096), dict(num_heads=2, num_kv_heads=4), dict(num_kv_heads=0), dict(head_dim=0),
                dict(num_rows=-5), dict(num_rows=2 ** 31 - 1), dict(num_reqs=2 ** 31 - 1), dict(block_size=2 ** 31 - 1)):
