@@ -130,7 +130,7 @@ def test_attention_workspace():
     assert m.sparse_attention_workspace_bytes(attn_shape(num_rows=4096), 2048, 4) == 0
     assert m.sparse_attention_workspace_bytes(s, 0, 4) == 0
     # tables whose steps do not add up in 32 bits are not cut
-    big = dict(num_rows=500, num_reqs=500, block_size=1024)
+    big = dict(num_rows=500, num_reqs=500, block_size=1024, num_heads=8, num_kv_heads=1)
     assert m.paged_attention_workspace_bytes(attn_shape(max_blocks=1 << 17, **big)) > 0
     assert m.paged_attention_workspace_bytes(attn_shape(max_blocks=1 << 19, **big)) == 0
     # shapes that the calls refuse need none, and the queries do not fail on them
