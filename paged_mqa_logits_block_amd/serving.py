@@ -4,7 +4,8 @@ Marshalling only, like the rest of the binding (``include/qsaidx.h`` has the
 contracts).  Each call comes as a function and as a ``Prepared`` class: a call
 checked once on fixed tensors, which then only crosses the C ABI.  All tensors of
 a call lie on one device; the call is queued on that device's current stream
-unless ``stream`` is given, whatever the calling thread's current device.
+unless ``stream`` is given, whatever the calling thread's current device (a
+prepared call: on the stream that was current when it was made).
 """
 from __future__ import annotations
 
@@ -361,7 +362,8 @@ class PreparedPagedAttention(_Prepared):
         shape = ctypes.byref(self.shape)
         args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(ctx_lens), _ptr(q_starts), _ptr(out))
         _raise_on(lib.qsa_paged_attention_check(*args, shape, None, 0))
-        ws = self.workspace = _scratch(workspace, int(lib.qsa_paged_attention_workspace_bytes(shape)), dev)
+        with _on(stream, dev):
+            ws = self.workspace = _scratch(workspace, int(lib.qsa_paged_attention_workspace_bytes(shape)), dev)
         _raise_on(lib.qsa_paged_attention_check(*args, shape, _ptr(ws), _nbytes(ws)))
         self.out, self.lse = out, lse
         self._ready(lib.qsa_paged_attention, (*args, _ptr(lse), shape, _ptr(ws), _nbytes(ws)), dev, stream,
@@ -393,7 +395,9 @@ class PreparedSparseAttention(_Prepared):
         shape = ctypes.byref(self.shape)
         args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(row_to_req), _ptr(idx), k, ratio)
         _raise_on(lib.qsa_sparse_attention_check(*args, _ptr(out), shape, None, 0))
-        ws = self.workspace = _scratch(workspace, int(lib.qsa_sparse_attention_workspace_bytes(shape, k, ratio)), dev)
+        with _on(stream, dev):
+            ws = self.workspace = _scratch(workspace,
+                                           int(lib.qsa_sparse_attention_workspace_bytes(shape, k, ratio)), dev)
         _raise_on(lib.qsa_sparse_attention_check(*args, _ptr(out), shape, _ptr(ws), _nbytes(ws)))
         self.out, self.lse = out, lse
         self._ready(lib.qsa_sparse_attention,
