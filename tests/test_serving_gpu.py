@@ -312,6 +312,9 @@ PAGED = [
     # requests without rows between others, one row each, more tiles than workgroups
     ([0, 5, 9, 100] * 20, [0, 1, 0, 2] * 20, dict(group=8, hk=8)),
     ([300] * 40, [1, 20] * 20, dict(group=8, hk=4, dim=64)),
+    # all rows of a batch of few rows per request in one request
+    ([500] * 20, [0] * 19 + [70], dict(group=8, hk=2)),
+    ([500] * 20, [0] * 3 + [65] + [0] * 16, dict(group=33, hk=1, dim=64)),
 ]
 
 
@@ -327,6 +330,26 @@ def test_paged_attention(i):
     out, lse = run_paged(b, workspace=None)
     b.check(out, lse, lambda r: range(b.ctx[r]))
     assert torch.all(out[b.rows:] == 3.0) and torch.all(lse[b.rows:] == 7.0)
+
+
+@pytest.mark.parametrize("rows,group", [(1, 4), (5, 16)])
+def test_paged_attention_many_requests(rows, group):
+    """More requests than a cut launch takes, in both kernels."""
+    n = 1100
+    rng = np.random.default_rng(rows)
+    b = Batch(14, [int(x) for x in rng.integers(0, 40, n)], [rows] * n, hk=1, group=group, dim=64)
+    assert m.paged_attention_workspace_bytes(m.make_attn_shape(b.q.cuda(), b.kc, b.table)) == 0
+    out, lse = run_paged(b)
+    b.check(out, lse, lambda r: range(b.ctx[r]), rows=range(0, b.rows, 7))
+    assert not torch.any(torch.isnan(out))
+
+
+def test_paged_attention_many_rows():
+    """More rows than a cut launch takes: every tile whole."""
+    b = Batch(15, [10, 5], [8000, 300], hk=1, group=1, dim=64)
+    out, lse = run_paged(b)
+    b.check(out, lse, lambda r: range(b.ctx[r]), rows=[*range(0, b.rows, 211), 7999, 8000, b.rows - 1])
+    assert not torch.any(torch.isnan(out))
 
 
 @pytest.mark.parametrize("new", [[6, 5], [100, 90]], ids=["few", "chunk"])
@@ -696,6 +719,49 @@ def test_serving_steps_captured():
         torch.cuda.synchronize()
         server.commit(new)
         server.check(new)
+
+
+def test_attention_graphs_side_by_side():
+    """Calls with workspaces of their own, captured in graphs of their own and
+    replayed on streams of their own, several times, with other work between."""
+    batches = [Batch(60, [4000, 900], [3, 2], group=8), Batch(61, [4000, 900], [40, 33], group=8),
+               Batch(62, [5000], [1], group=4, dim=64)]
+    idx = [sparse_idx(b, 256, 4) for b in batches]
+    runs = []
+    for b, ix in zip(batches, idx):
+        q, ctx, starts, req, sel = b.q.cuda(), dev(b.ctx), dev(b.starts), dev(b.req.astype(np.int32)), dev(ix)
+        outs = [torch.zeros_like(q) for _ in range(2)]
+        lses = [torch.zeros(q.shape[:2], device="cuda") for _ in range(2)]
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            calls = [m.PreparedPagedAttention(q, b.kc, b.vc, b.table, ctx, starts, outs[0], lse=lses[0]),
+                     m.PreparedSparseAttention(q, b.kc, b.vc, b.table, req, sel, outs[1], ratio=4, token_lens=ctx,
+                                               lse=lses[1])]
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph, stream=s):
+                for call in calls:
+                    call()
+        runs.append((b, ix, s, graph, calls, outs, lses, (q, ctx, starts, req, sel)))
+    torch.cuda.synchronize()
+    want = None
+    for _ in range(4):
+        for r in runs:
+            for t in (*r[5], *r[6]):
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        for _, _, s, graph, *_ in runs:
+            with torch.cuda.stream(s):
+                graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for r in runs for t in (*r[5], *r[6])]
+        if want is None:
+            for b, ix, _, _, _, outs, lses, _ in runs:
+                b.check(outs[0], lses[0], lambda r: range(b.ctx[r]))
+                b.check(outs[1], lses[1], lambda r: tokens_of(ix[r], 4, b.ctx[r]))
+            want = got
+        assert all(torch.equal(x, y) for x, y in zip(want, got))
+        torch.randn(1000, 1000, device="cuda") @ torch.randn(1000, 1000, device="cuda")
 
 
 def test_sparse_attention_of_everything_is_dense():
