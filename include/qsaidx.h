@@ -439,7 +439,7 @@ typedef struct qsa_attn_shape {
     int32_t num_reqs;          /* rows of block_table                              */
     int32_t max_blocks;        /* columns of block_table                           */
     int32_t dtype;             /* QSA_BF16 or QSA_FP16: q, caches and out          */
-    float scale;               /* of the scores, positive                          */
+    float scale;               /* of the scores, in (0, 1e38]                      */
     int32_t reserved;
     int64_t num_blocks;
     /* strides in elements (the last dimension is contiguous)                    */

@@ -2,8 +2,6 @@
 // attention over the paged cache (all visible tokens, or the selected ones).
 // As in api.hip, validation reads host scalars only and every call can be
 // captured.
-#include <math.h>
-
 #include "api_common.h"
 #include "attn_internal.h"
 #include "qsa_internal.h"
@@ -213,7 +211,8 @@ qsa_status check_attn(const void *q, const void *kcache, const void *vcache, con
                       const qsa_attn_shape *s, bool sparse, int32_t k, int32_t ratio) {
     qsa_status st = check_attn_sizes(s, sparse, k, ratio);
     if (st != QSA_OK) return st;
-    if (!(s->scale > 0.0f) || isinf(s->scale)) return fail(QSA_E_INVALID, "scale must be positive and finite");
+    // the kernels work with scale * log2(e)
+    if (!(s->scale > 0.0f) || s->scale > 1e38f) return fail(QSA_E_INVALID, "scale must be in (0, 1e38]");
     if (s->q_row_stride < 0 || s->q_head_stride < 0 || s->out_row_stride < 0 || s->out_head_stride < 0 ||
         s->kv_block_stride < 0 || s->kv_slot_stride < 0 || s->kv_head_stride < 0)
         return fail(QSA_E_INVALID, "strides must be >= 0");

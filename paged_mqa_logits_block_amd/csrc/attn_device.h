@@ -76,6 +76,12 @@ __device__ __forceinline__ float xor32_max(float v) {
     return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
+// max(v, v of lane l ^ 16)
+__device__ __forceinline__ float xor16_max(float v) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
 // 16 bytes per lane from global memory to LDS at lds_wave + 16 * lane (lds_wave
 // wave-uniform); outstanding on the vector memory counter until wait_copies().
 __device__ __forceinline__ void copy16(const void *src, uint32_t lds_wave) {
@@ -206,6 +212,72 @@ __device__ __forceinline__ void output_tile(const uint8_t *vbase, const f32x16 &
 // the key (0..31) that register i of a score tile holds in this lane
 __device__ __forceinline__ int score_key(int i, int lane) { return 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3); }
 
+// What one MFMA leaves in a lane: 16 values of a 32x32 tile, or 4 of a 16x16 one.
+template <bool NARROW>
+struct Tile {
+    typedef f32x16 V;
+};
+template <>
+struct Tile<true> {
+    typedef f32x4 V;
+};
+
+template <int DT>
+__device__ __forceinline__ f32x4 mfma16(i32x4 a, i32x4 b, f32x4 c) {
+    typedef typename Half<DT>::V8 V8;
+    if constexpr (DT == kBF16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(V8, a), __builtin_bit_cast(V8, b), c, 0, 0, 0);
+}
+
+// The same as score_tile and output_tile with the 16x16x32 MFMA, for up to 16 pairs:
+// with g = l >> 4, lane l holds elements 8 g .. + 7 of each 32 as an operand, and of
+// the result pair l & 15 and rows 4 g + i.  Score tile u is keys 16 u .. 16 u + 15; the
+// inner elements 8 g + j of the second product stand for keys 4 g + j (j < 4) and
+// 16 + 4 g + j - 4, the lane's own scores.  Output tile m is elements 16 m .. + 15.
+template <int DT, int D>
+__device__ __forceinline__ void score_narrow(const uint8_t *kbase, const i32x4 (&q)[D / 32], f32x4 (&z)[2], int lane) {
+    const int g = lane >> 4;
+    i32x4 k[2][D / 32];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+            const int row = 16 * u + (lane & 15);
+            k[u][c] = *reinterpret_cast<const i32x4 *>(kbase + row * 2 * D + (((4 * c + g) ^ swz_k<D>(row)) << 4));
+        }
+    __builtin_amdgcn_sched_barrier(0);
+    z[0] = z[1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) z[u] = mfma16<DT>(k[u][c], q[c], z[u]);
+}
+
+template <int DT, int D>
+__device__ __forceinline__ void output_narrow(const uint8_t *vbase, const f32x4 (&p)[2], f32x4 (&o)[D / 16], int lane) {
+    const int g = lane >> 4, i = lane & 15;
+    i32x4 v[D / 16];
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int row = 16 * u + 4 * g + (i >> 2), chunk = 2 * m + ((i & 3) >> 1);
+            const auto x = __builtin_bit_cast(
+                i32x2, read_tr(vbase + row * 2 * D + ((chunk ^ swz_v<D>(row)) << 4) + 8 * (i & 1)));
+            v[m][2 * u] = x[0];
+            v[m][2 * u + 1] = x[1];
+        }
+    typename Half<DT>::V8 w;  // rounded as in pack8
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = (typename Half<DT>::T)p[j >> 2][j & 3];
+    const i32x4 b = __builtin_bit_cast(i32x4, w);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int m = 0; m < D / 16; ++m) o[m] = mfma16<DT>(v[m], b, o[m]);
+}
+
 // One step of a pair's softmax over U score tiles: the weights
 // 2^(c z - ref) in place of the scores z (c = scale log2 e), their sum added to
 // `total`.  `ref` (in log2 units, -inf before the first key) is a value near the
@@ -213,13 +285,15 @@ __device__ __forceinline__ int score_key(int i, int lane) { return 8 * (i >> 2) 
 // 8, for then every weight is still below 2^8 and the outputs need no rescaling
 // in most steps (with the exact maximum some of a wave's 32 pairs rises in nearly
 // every step).  Sums and outputs are relative to ref throughout, so it cancels.
-template <int U, int N>
-__device__ __forceinline__ void softmax_step(f32x16 (&z)[U], float c, float &ref, float &total, f32x16 (&o)[N]) {
+template <int U, int N, class V>
+__device__ __forceinline__ void softmax_step(V (&z)[U], float c, float &ref, float &total, V (&o)[N]) {
+    constexpr int kRegs = sizeof(V) / 4;
     float top = z[0][0];
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, z[u][i]);
+        for (int i = 0; i < kRegs; ++i) top = fmaxf(top, z[u][i]);
+    if (kRegs == 4) top = xor16_max(top);
     top = xor32_max(top) * c;
     if (ballot(top > ref + 8.0f)) {
         const float next = fmaxf(ref, top);
@@ -234,7 +308,7 @@ __device__ __forceinline__ void softmax_step(f32x16 (&z)[U], float c, float &ref
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < kRegs; ++i) {
             z[u][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[u][i], c, use));
             sum[i & 1] += z[u][i];
         }

@@ -30,9 +30,9 @@
 // us with one wave per 32 keys' split and arguments in scratch, 198 + 10 without the
 // scratch.  One row over 4,000 tokens: 9 + 4 us, latency: about six dependent loads,
 // of which the launch, the join and the table make half.  Selected tokens of 36 rows
-// (8,192 each, 605 MB): 105 + 5 us, 5.5 TB/s.  Of 1,000 rows (2,048 each): 331 us for
-// 4.2 GB through the L2s (12.7 TB/s; 78% of the requests hit), where halving the
-// products saves 11%: what bounds it is the gather.
+// (8,192 each, 605 MB): 105 + 5 us, 5.5 TB/s.  Of 1,000 rows (2,048 each): 265 us
+// for 4.2 GB through the L2s (15.8 TB/s; 78% of the requests hit), 299 with 32-pair
+// tiles of which these heads fill 8 (NARROW below): what bounds it is the gather.
 #include "attn_device.h"
 
 namespace qsa {
@@ -115,8 +115,11 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int group, int tile
     return a.part + (int64_t)(group + tile) * (kAttnTile * (D + 2));
 }
 
-template <int DT, int D, bool SPARSE>
+// NARROW (selected tokens of up to 16 heads): the 16x16x32 MFMA on 16 pairs instead of
+// the 32x32x16 one on 32, with half the products and half the weights per key.
+template <int DT, int D, bool SPARSE, bool NARROW>
 struct Stream {
+    static_assert(SPARSE || !NARROW, "dense tiles fill 32 pairs where they can");
     static constexpr int kTileBytes = kStreamKeys * D * 2;  // one buffer of keys or values
     static constexpr int kCopies = kTileBytes / (16 * kWave);
     static constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
@@ -140,7 +143,7 @@ struct Stream {
         int t = threadIdx.x;
         asm volatile("" : "+v"(t));  // addresses are made anew for each range, not kept live across them
         const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
-        const Pair pair = pair_of(a, w, lane & 31);
+        const Pair pair = pair_of(a, w, NARROW ? lane & 15 : lane & 31);
         const int ctx = SPARSE ? 0 : (pair.live ? visible(a, pair.row) : 0);
         int least = 0, limit = 0;
         if (SPARSE) {
@@ -149,12 +152,14 @@ struct Stream {
             least = keys;  // the smallest visible count: steps below it need no mask
             for (int r = 0; r < w.rows; ++r) least = min(least, visible(a, w.row0 + r));
         }
-        i32x4 q[D / 16];
+        constexpr int kQ = NARROW ? D / 32 : D / 16;
+        i32x4 q[kQ];
         const uint16_t *qrow = static_cast<const uint16_t *>(a.q) + pair.row * a.q_row + pair.head * a.q_head;
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
+        for (int c = 0; c < kQ; ++c) {
             q[c] = i32x4{0, 0, 0, 0};
-            if (pair.live) q[c] = *reinterpret_cast<const i32x4 *>(qrow + 16 * c + 8 * (lane >> 5));
+            if (pair.live)
+                q[c] = *reinterpret_cast<const i32x4 *>(qrow + (NARROW ? 32 * c + 8 * (lane >> 4) : 16 * c + 8 * (lane >> 5)));
         }
 
         uint8_t *mine = sh.ring[wave];
@@ -233,8 +238,11 @@ struct Stream {
             }
         };
 
-        f32x16 o[D / 32] = {};
-        float m = kNegInf, l = 0.0f;  // l: this lane's half of the sum
+        typedef typename Tile<NARROW>::V V;  // scores and outputs of one MFMA: 4 or 16 per lane
+        constexpr int kScores = NARROW ? 2 : 1, kOut = NARROW ? D / 16 : D / 32, kRegs = NARROW ? 4 : 16;
+        V o[kOut] = {};
+        float m = kNegInf, l = 0.0f;  // l: this lane's part of the sum
+        const auto key_of = [&](int u, int i) { return NARROW ? 16 * u + 4 * (lane >> 4) + i : score_key(i, lane); };
         if (have(0)) {
             if constexpr (SPARSE) {
                 copy_column(0);
@@ -247,7 +255,7 @@ struct Stream {
             // q is waited for here: the compiler would wait for it, and with it for
             // every copy, in the loop
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) asm volatile("" : "+v"(q[c]));
+            for (int c = 0; c < kQ; ++c) asm volatile("" : "+v"(q[c]));
             Step cur = locate(0, k0), ahead = cur;
             copy_rows(a.kcache, cur, false);
             copy_entry(1, next);
@@ -257,7 +265,9 @@ struct Stream {
                 const bool more = have(j + 1);
                 const int s = t0 + wave + j * kStreamWaves;
                 wait_all_but<kCopies>();
-                f32x16 z[1] = {score_tile<DT, D>(mine, q, lane)};
+                V z[kScores];
+                if constexpr (NARROW) score_narrow<DT, D>(mine, q, z, lane);
+                else z[0] = score_tile<DT, D>(mine, q, lane);
                 if (more) {
                     ahead = locate(j + 1, next);
                     wait_reads();
@@ -265,23 +275,31 @@ struct Stream {
                 }
                 if (cur.bad) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        z[0][i] = (cur.bad >> score_key(i, lane)) & 1 ? __builtin_nanf("") : z[0][i];
+                    for (int u = 0; u < kScores; ++u)
+#pragma unroll
+                        for (int i = 0; i < kRegs; ++i)
+                            z[u][i] = (cur.bad >> key_of(u, i)) & 1 ? __builtin_nanf("") : z[u][i];
                 }
                 if (SPARSE) {
                     if (cur.seen != 0xFFFFFFFFu) {
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) z[0][i] = (cur.seen >> score_key(i, lane)) & 1 ? z[0][i] : kNegInf;
+                        for (int u = 0; u < kScores; ++u)
+#pragma unroll
+                            for (int i = 0; i < kRegs; ++i)
+                                z[u][i] = (cur.seen >> key_of(u, i)) & 1 ? z[u][i] : kNegInf;
                     }
                 } else if ((s + 1) * kStreamKeys > least) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) z[0][i] = s * kStreamKeys + score_key(i, lane) < ctx ? z[0][i] : kNegInf;
+                    for (int i = 0; i < kRegs; ++i) z[0][i] = s * kStreamKeys + key_of(0, i) < ctx ? z[0][i] : kNegInf;
                 }
                 softmax_step(z, a.scale_log2, m, l, o);
                 if (more) wait_all_but<kCopies>();
                 else wait_copies();
                 // a step without tokens holds the values of block 0, whatever they are
-                if (!SPARSE || cur.seen != 0) output_tile<DT, D>(mine + kTileBytes, z[0], o, lane);
+                if (!SPARSE || cur.seen != 0) {
+                    if constexpr (NARROW) output_narrow<DT, D>(mine + kTileBytes, z, o, lane);
+                    else output_tile<DT, D>(mine + kTileBytes, z[0], o, lane);
+                }
                 if (more) {
                     next = token(j + 2);
                     wait_reads();
@@ -294,17 +312,20 @@ struct Stream {
             wait_copies();
         }
         l = xor32_sum(l);
+        if (NARROW) l = xor16_sum(l);
 
         // join the waves' states: each leaves its output in its own buffers
         float *left = reinterpret_cast<float *>(mine);
+        const int pair_at = NARROW ? lane & 15 : lane & 31;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+        for (int c = 0; c < kOut; ++c)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
+            for (int g = 0; g < kRegs / 4; ++g) {
                 const f32x4 v = {o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
-                *reinterpret_cast<f32x4 *>(left + left_at(lane & 31, out_element<D>(c, 4 * g, lane) / 4)) = v;
+                const int d = NARROW ? 16 * c + 4 * (lane >> 4) : out_element<D>(c, 4 * g, lane);
+                *reinterpret_cast<f32x4 *>(left + left_at(pair_at, d / 4)) = v;
             }
-        if (lane < kAttnTile) {
+        if (lane == pair_at) {
             sh.top_of[wave][lane] = m;
             sh.sum_of[wave][lane] = l;
         }
@@ -387,9 +408,9 @@ struct Stream {
 };
 
 // one workgroup per tile
-template <int DT, int D, bool SPARSE>
+template <int DT, int D, bool SPARSE, bool NARROW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_stream_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE> S;
+    typedef Stream<DT, D, SPARSE, NARROW> S;
     __shared__ typename S::Shared sh;
     TileWork w;
     if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
@@ -417,9 +438,9 @@ struct TileSpan {
 
 // Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
 // units of a slot are the same for every hs.
-template <int DT, int D, bool SPARSE>
+template <int DT, int D, bool SPARSE, bool NARROW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE> S;
+    typedef Stream<DT, D, SPARSE, NARROW> S;
     __shared__ typename S::Shared sh;
     __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
     __shared__ int32_t wave_sums[kStreamWaves];
@@ -520,15 +541,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
         a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }
 
-template <int DT, int D, bool SPARSE>
+template <int DT, int D, bool SPARSE, bool NARROW>
 hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     const unsigned heads = (unsigned)(a.num_kv_heads * a.num_subs);
     if (!a.part) {
-        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
+        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE, NARROW>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
                            0, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
+    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE, NARROW>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>),
@@ -536,10 +557,15 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+template <int DT, int D>
+hipError_t run_kind(const AttnArgs &a, bool sparse, hipStream_t s) {
+    if (!sparse) return run_stream<DT, D, false, false>(a, s);
+    return a.sub_heads <= 16 ? run_stream<DT, D, true, true>(a, s) : run_stream<DT, D, true, false>(a, s);
+}
+
 template <int DT>
 hipError_t run_dim(const AttnArgs &a, bool sparse, hipStream_t s) {
-    if (a.head_dim == 128) return sparse ? run_stream<DT, 128, true>(a, s) : run_stream<DT, 128, false>(a, s);
-    return sparse ? run_stream<DT, 64, true>(a, s) : run_stream<DT, 64, false>(a, s);
+    return a.head_dim == 128 ? run_kind<DT, 128>(a, sparse, s) : run_kind<DT, 64>(a, sparse, s);
 }
 
 }  // namespace

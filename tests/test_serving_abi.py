@@ -85,7 +85,7 @@ ATTN = [
     (dict(num_heads=512, q_row_stride=65536, out_row_stride=65536), "OK"), (dict(q_row_stride=0), "OK"),
     (dict(num_rows=0), "OK"), (dict(block_size=1), "OK"),
     (dict(num_heads=30), "E_INVALID"), (dict(scale=0.0), "E_INVALID"), (dict(scale=-1.0), "E_INVALID"),
-    (dict(scale=float("nan")), "E_INVALID"), (dict(scale=float("inf")), "E_INVALID"), (dict(num_rows=-1), "E_INVALID"),
+    (dict(scale=float("nan")), "E_INVALID"), (dict(scale=float("inf")), "E_INVALID"), (dict(scale=3e38), "E_INVALID"), (dict(num_rows=-1), "E_INVALID"),
     (dict(out_row_stride=0), "E_INVALID"), (dict(out_head_stride=64), "E_INVALID"), (dict(kv_slot_stride=-8), "E_INVALID"),
     (dict(num_reqs=0), "E_INVALID"), (dict(dtype=m.FP8_E4M3FN), "E_DTYPE"), (dict(head_dim=96), "E_UNSUPPORTED"),
     (dict(num_heads=516), "E_UNSUPPORTED"), (dict(block_size=2048), "E_UNSUPPORTED"),
