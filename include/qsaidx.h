@@ -465,9 +465,10 @@ typedef struct qsa_attn_shape {
  *             [q_starts[i], q_starts[i + 1]) (values are clamped to [0, R]).
  *             Rows outside all requests are left as they were in out and lse.
  *   lse       [R][Hq] f32 contiguous, or NULL.
- *   workspace qsa_paged_attention_workspace_bytes(shape) bytes, 16-byte aligned,
- *             or NULL: then few rows over long contexts are not spread over the
- *             chip.  No initialisation; calls that share it must be ordered.
+ *   workspace qsa_paged_attention_workspace_bytes(shape) bytes (0 also for shapes
+ *             that the call refuses), 16-byte aligned, or NULL: then few rows over
+ *             long contexts are not spread over the chip.  No initialisation; calls
+ *             that share it must be ordered.
  *
  * Keys and values of columns that no row of the request sees are not used, and
  * what only other rows see does not change a row, infinities and NaN included.

@@ -335,12 +335,12 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
 
     // The wave's pairs are done again, each over its own keys, where the tile met a
     // table entry outside the pool, or where a NaN can come from a value that only
-    // other rows of the wave see (zero weight times a value that is not finite; a pair
+    // other rows of the tile see (zero weight times a value that is not finite; a pair
     // whose own scores are NaN has a NaN sum).
     if (ballot(met_bad) && lane == 0) sh.any_bad = 1;
     __syncthreads();
     bool again = sh.any_bad != 0;
-    if (wave_least < wave_most) {
+    if (wave_least < keys) {
         bool nan = false;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)

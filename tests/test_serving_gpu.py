@@ -388,6 +388,21 @@ def test_paged_attention_values_others_see(new, value):
         assert torch.all(torch.isnan(out[r])), r
 
 
+@pytest.mark.parametrize("rows,reqs", [(64, 1), (64, 2), (8, 2)])
+def test_paged_attention_values_other_waves_see(rows, reqs):
+    """The same where whole waves of a tile see one count: the first half of the rows
+    sees 100 tokens, the second half 200, and token 150's value is not finite."""
+    ctx = np.concatenate([np.where(np.arange(rows) < rows // 2, 100, 200) for _ in range(reqs)])
+    b = Batch(13, [200] * reqs, [rows] * reqs, group=4, ctx=ctx)
+    for i in range(reqs):
+        b.vc[int(b.table[i, 150 // b.block]), 150 % b.block] = float("inf")
+    for workspace in ("auto", None):
+        out, lse = run_paged(b, workspace=workspace)
+        clean = [r for r in range(b.rows) if b.ctx[r] == 100]
+        b.check(out, lse, lambda r: range(b.ctx[r]), rows=clean)
+        assert torch.all(torch.isinf(out[[r for r in range(b.rows) if b.ctx[r] == 200]]))
+
+
 @pytest.mark.parametrize("new", [[4, 2], [70, 60]], ids=["few", "chunk"])
 def test_paged_attention_bad_entries(new):
     """Table entries outside the pool: rows that see their columns are NaN, others
