@@ -18,7 +18,7 @@
 //
 // Measured: 2,048 rows at the end of 16,384 tokens, 32 over 4 heads, D = 128, bf16:
 // 460 us, 1,120 TFLOP/s, 92% of the rate of a library product of 8192^3 on the same
-// card (1,214).  On the way there: 931 us with the arguments in scratch, 731 without,
+// card (1,214); up to 516 us on other cards.  On the way there: 931 us with the arguments in scratch, 731 without,
 // 674 with a lagging softmax reference, 569 with the turns and scalar table entries,
 // 552 with heads dealt to the XCDs.  The clock drops from 2.3 to 1.9 GHz while the
 // matrix cores work, so the card's power is part of the bound.
@@ -76,12 +76,12 @@ __device__ __forceinline__ void turn() {
 
 // The products of a turn: PV adds the values (LDS rows at vb) times the packed
 // weights p to o, QK makes the scores z of the keys at kb.  They run in groups of
-// four MFMAs; operands are read kAhead groups before their products, as four
-// waves read at once and a read takes longer than one group's products.
+// four MFMAs; operands are read kAhead groups before their products (1 and 2 take the
+// same time).
 template <int DT, int D, bool PV, bool QK>
 __device__ __forceinline__ void multiply(const uint8_t *vb, const uint8_t *kb, const i32x4 (&p)[4],
                                          const i32x4 (&q)[D / 16], f32x16 (&o)[D / 32], f32x16 (&z)[2], int lane) {
-    constexpr int kAhead = 2, kM = D / 32, kV = PV ? kM : 0, kK = QK ? D / 32 : 0;
+    constexpr int kAhead = 1, kM = D / 32, kV = PV ? kM : 0, kK = QK ? D / 32 : 0;
     i32x4 f[kAhead + 1][4];
     const int row = lane & 31, h = lane >> 5;
     const auto read = [&](int g) {
