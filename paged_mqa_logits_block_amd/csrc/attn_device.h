@@ -54,9 +54,10 @@ __device__ __forceinline__ f32x16 mfma32(i32x4 a, i32x4 b, f32x16 c) {
 }
 
 // 8 values rounded to nearest into 16 bits.  The weights are rounded here to
-// the caches' type: each is off by at most half a step of that type relative to
-// itself, as the output is, and the MFMA then runs at its 16-bit rate.  The sum
-// of the weights is taken before the rounding.
+// the caches' type, and the MFMA then runs at its 16-bit rate: each is off by at most
+// half a step of that type relative to itself, as the output is, but for fp16's
+// subnormal ones, which are off by up to 2^-25 (kLift keeps that to 2^-38 of the
+// largest weight).  The sum of the weights is taken before the rounding.
 template <int DT>
 __device__ __forceinline__ i32x4 pack8(const f32x16 &p, int at) {
     typename Half<DT>::V8 v;
@@ -280,12 +281,23 @@ __device__ __forceinline__ void output_narrow(const uint8_t *vbase, const f32x4 
 
 // One step of a pair's softmax over U score tiles: the weights
 // 2^(c z - ref) in place of the scores z (c = scale log2 e), their sum added to
-// `total`.  `ref` (in log2 units, -inf before the first key) is a value near the
-// running maximum: it follows the maximum only where that has risen by more than
-// 8, for then every weight is still below 2^8 and the outputs need no rescaling
-// in most steps (with the exact maximum some of a wave's 32 pairs rises in nearly
-// every step).  Sums and outputs are relative to ref throughout, so it cancels.
-template <int U, int N, class V>
+// `total`.  `ref` (in log2 units, -inf before the first key) is put kLift below the
+// running maximum, and follows the maximum only where that has risen by more than
+// kLag since, for then every weight is still below 2^(kLift + kLag) and the outputs
+// need no rescaling in most steps (with the exact maximum some of a wave's 32 pairs
+// rises in nearly every step).  Sums and outputs are relative to ref throughout, so
+// it cancels.
+//
+// fp16 holds weights up to 2^15.9, and from 2^-14 down with fewer and fewer bits.
+// With the largest weight between 2^13 and 2^15, keys down to 2^-27 of the largest
+// have all theirs.  (Not lifted, 40,000 keys 16 below one whose value is 0 came out 6%
+// off.  A lag of 8 with a lift of 7, down to 2^-21, takes 519 us for 2,048 rows at
+// 16,384 tokens in fp16, these 525.)
+template <int DT>
+constexpr float kLag = DT == kFP16 ? 2.0f : 8.0f;
+template <int DT>
+constexpr float kLift = DT == kFP16 ? 13.0f : 0.0f;
+template <int DT, int U, int N, class V>
 __device__ __forceinline__ void softmax_step(V (&z)[U], float c, float &ref, float &total, V (&o)[N]) {
     constexpr int kRegs = sizeof(V) / 4;
     float top = z[0][0];
@@ -295,8 +307,8 @@ __device__ __forceinline__ void softmax_step(V (&z)[U], float c, float &ref, flo
         for (int i = 0; i < kRegs; ++i) top = fmaxf(top, z[u][i]);
     if (kRegs == 4) top = xor16_max(top);
     top = xor32_max(top) * c;
-    if (ballot(top > ref + 8.0f)) {
-        const float next = fmaxf(ref, top);
+    if (ballot(top > ref + (kLift<DT> + kLag<DT>))) {
+        const float next = fmaxf(ref, top - kLift<DT>);
         const float keep = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
         ref = next;
         total *= keep;

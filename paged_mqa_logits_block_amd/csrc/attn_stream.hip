@@ -292,7 +292,7 @@ struct Stream {
 #pragma unroll
                     for (int i = 0; i < kRegs; ++i) z[0][i] = s * kStreamKeys + key_of(0, i) < ctx ? z[0][i] : kNegInf;
                 }
-                softmax_step(z, a.scale_log2, m, l, o);
+                softmax_step<DT>(z, a.scale_log2, m, l, o);
                 if (more) wait_all_but<kCopies>();
                 else wait_copies();
                 // a step without tokens holds the values of block 0, whatever they are

@@ -309,7 +309,7 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
                         for (int i = 0; i < 16; ++i)
                             z[u][i] = s * kTileKeys + 32 * u + score_key(i, lane) < ctx ? z[u][i] : kNegInf;
                 }
-                softmax_step(z, a.scale_log2, ref, total, o);
+                softmax_step<DT>(z, a.scale_log2, ref, total, o);
 #pragma unroll
                 for (int g = 0; g < 4; ++g) p[g] = pack8<DT>(z[g >> 1], 8 * (g & 1));
             }

@@ -70,3 +70,14 @@ def bounds(out, lse, spread, size, n, d, half_step):
     tol_o = half_step * np.abs(out) + (1 + half_step) * rel[:, None] * spread * 1.01 + 1e-30
     tol_l = (w + s) * 1.01 + 2.0 ** -22 * np.abs(lse)
     return tol_o, tol_l
+
+
+def fp16_tail(v):
+    """What fp16 weights add to a row's allowed error over values v [n, D].
+
+    `bounds` takes each weight as rounded by half a step relative to itself, which
+    fp16 does down to 2^-14 only; below, it is off by up to 2^-25.  The weights are
+    taken relative to a reference that lies at least 13 (in log2) below the row's
+    largest score, so that the largest weight is 2^13 or more: a probability is off by
+    2^-38 at most.  An output below 2^-14 is itself off by up to 2^-25."""
+    return 2.0 ** -38 * np.abs(v).sum(axis=0) + 2.0 ** -25

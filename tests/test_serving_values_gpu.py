@@ -1,0 +1,81 @@
+"""Paged and selected attention on the GPU at values where a softmax can go wrong:
+scores far apart, very large scores, infinities among a row's own values."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+m = pytest.importorskip("paged_mqa_logits_block_amd")
+
+import serving_ref as ref  # noqa: E402
+from test_serving_gpu import DT, dev  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+def device_cache(k, v, dtype, block=64):
+    """Caches of one request with keys and values [n, hk, d] in scattered blocks, and
+    its table; places behind the last token are NaN."""
+    n, hk, d = k.shape
+    blocks = -(-n // block)
+    ids = np.random.default_rng(n).permutation(blocks + 2)[:blocks]
+    kv = torch.full((2, blocks + 2, block, hk, d), float("nan"), dtype=DT[dtype])
+    pos = np.arange(n)
+    for c, x in zip(kv, (k, v)):
+        c[torch.from_numpy(ids[pos // block]), torch.from_numpy(pos % block)] = x.to(DT[dtype])
+    kv = kv.cuda()
+    return kv[0], kv[1], dev(ids[None].astype(np.int32))
+
+
+def attend_all(kernel, q, kc, vc, table, counts, scale=None):
+    """(out, lse) of rows q [R, H, d] over the first counts[r] tokens by one of the
+    ways through the kernels."""
+    R = q.shape[0]
+    lse = torch.empty(q.shape[:2], device="cuda")
+    counts = np.asarray(counts, np.int32)
+    if kernel.startswith("sparse"):
+        width = table.shape[1] * kc.shape[1]  # padded to the whole table, not packed
+        idx = np.where(np.arange(width)[None, :] < counts[:, None], np.arange(width), -1).astype(np.int32)
+        out = m.sparse_attention(q, kc, vc, table, dev(np.zeros(R, np.int32)), dev(idx), lse=lse, scale=scale,
+                                 workspace="auto" if kernel.endswith("cut") else None)
+    else:
+        out = m.paged_attention(q, kc, vc, table, dev(counts), dev(np.array([0, R], np.int32)), lse=lse, scale=scale,
+                                workspace="auto" if kernel.endswith("cut") else None)
+    return out.double().cpu().numpy(), lse.double().cpu().numpy()
+
+
+# kernel: rows, heads per kv head that take it (few rows stream, many take the tile kernel)
+KERNELS = {"stream": (1, 8), "stream_cut": (1, 8), "tile": (65, 8), "tile_cut": (65, 8), "sparse": (2, 8),
+           "sparse_cut": (2, 8), "sparse_wide": (2, 24), "sparse_wide_cut": (2, 24)}
+
+
+# ---------------------------------------------------------------------------
+# scores far apart
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("gap", [10.0, 14.0, 16.0, 17.5, 19.0, 24.0])
+def test_one_dominant_key(kernel, dtype, gap):
+    """One early key `gap` above n others of one score, its value 0: what the others
+    hold together is the output, though each one's weight is small."""
+    rows, group = KERNELS[kernel]
+    n, d = 40_000, 64
+    g = torch.Generator().manual_seed(int(gap))
+    k, v = torch.zeros(n, 1, d), torch.randn(n, 1, d, generator=g) + 1.0
+    k[0, 0, 0], v[0] = gap, 0.0
+    q = torch.zeros(rows, group, d)
+    q[..., 0] = d ** 0.5
+    q = q.to(DT[dtype])
+    kc, vc, table = device_cache(k, v, dtype)
+    out, lse = attend_all(kernel, q.cuda(), kc, vc, table, [n] * rows)
+    kk, vv = (x.to(DT[dtype]).double().numpy()[:, 0] for x in (k, v))
+    # sums: a product's 16 keys, then one addition per 16 keys of the longest range
+    o, l, spread, size = ref.attend(q[0].double().numpy(), kk, vv, d ** -0.5)
+    to, tl = ref.bounds(o, l, spread, size, n // 16 + 64, d, torch.finfo(DT[dtype]).eps / 2)
+    if dtype == "fp16":
+        to = to + ref.fp16_tail(vv)
+    for r in range(rows):
+        assert np.all(np.abs(out[r] - o) <= to), (r, float((np.abs(out[r] - o) / to).max()))
+        assert np.all(np.abs(lse[r] - l) <= tl), r
