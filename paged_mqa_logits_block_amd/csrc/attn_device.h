@@ -288,6 +288,11 @@ __device__ __forceinline__ void output_narrow(const uint8_t *vbase, const f32x4 
 // rises in nearly every step).  Sums and outputs are relative to ref throughout, so
 // it cancels.
 //
+// c z - ref is one fma, c z itself unrounded, where ref is a rounded c z: they are
+// apart by up to half a step of c z, which passes any exponent once scores are large
+// (from about 2^30 on a row's only key had weight 0 or infinity).  Past 2^20 the
+// products are rounded as ref is, and ref is not lifted (kLift may be less than a step).
+//
 // fp16 holds weights up to 2^15.9, and from 2^-14 down with fewer and fewer bits.
 // With the largest weight between 2^13 and 2^15, keys down to 2^-27 of the largest
 // have all theirs.  (Not lifted, 40,000 keys 16 below one whose value is 0 came out 6%
@@ -307,8 +312,17 @@ __device__ __forceinline__ void softmax_step(V (&z)[U], float c, float &ref, flo
         for (int i = 0; i < kRegs; ++i) top = fmaxf(top, z[u][i]);
     if (kRegs == 4) top = xor16_max(top);
     top = xor32_max(top) * c;
-    if (ballot(top > ref + (kLift<DT> + kLag<DT>))) {
-        const float next = fmaxf(ref, top - kLift<DT>);
+    const bool large = fabsf(top) > 0x1p20f;
+    if (ballot(large && top != kNegInf)) {
+#pragma clang fp contract(off)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < kRegs; ++i) z[u][i] *= c;
+        c = 1.0f;
+    }
+    if (ballot(top - ref > kLift<DT> + kLag<DT>)) {
+        const float next = fmaxf(ref, large ? top : top - kLift<DT>);
         const float keep = next == kNegInf ? 1.0f : __builtin_amdgcn_exp2f(ref - next);
         ref = next;
         total *= keep;

@@ -79,3 +79,36 @@ def test_one_dominant_key(kernel, dtype, gap):
     for r in range(rows):
         assert np.all(np.abs(out[r] - o) <= to), (r, float((np.abs(out[r] - o) / to).max()))
         assert np.all(np.abs(lse[r] - l) <= tl), r
+
+
+# ---------------------------------------------------------------------------
+# large scores
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype,size", [("fp16", 2.0 ** 12), ("fp16", 1.375 * 2.0 ** 14), ("fp16", 1.75 * 2.0 ** 14),
+                                        ("bf16", 1.25 * 2.0 ** 14), ("bf16", 1.375 * 2.0 ** 50)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_large_scores(kernel, dtype, size, sign):
+    """Scores of +-size^2 d / 8, and 0 for the keys of the other sign: the softmax is
+    the mean of the values of the keys with the largest score, the log-sum-exp that
+    score and the log of their number.  Rows see 1, 2 or all keys."""
+    rows, group = KERNELS[kernel]
+    n, d = 700, 64
+    g = torch.Generator().manual_seed(3)
+    v = torch.randn(n, 1, d, generator=g).to(DT[dtype])
+    k = torch.zeros(n, 1, d)
+    top = [0, 1, 600] if sign > 0 else list(range(n))  # keys of the largest score
+    k[top] = sign * size
+    q = torch.full((rows, group, d), size).to(DT[dtype])
+    kc, vc, table = device_cache(k, v, dtype)
+    score = sign * size * size * d ** 0.5  # exact in 32 bits
+    u = torch.finfo(DT[dtype]).eps / 2
+    for count in (1, 2, n):
+        out, lse = attend_all(kernel, q.cuda(), kc, vc, table, [count] * rows)
+        mine = [t for t in top if t < count]
+        want = v[mine, 0].double().numpy().mean(axis=0)
+        # equal weights, a sum of len(mine) products, a division, two roundings to the type
+        tol = (2 * u + (len(mine) + 8) * 2.0 ** -24) * np.abs(v[mine, 0].double().numpy()).mean(axis=0)
+        assert np.all(np.abs(out - want) <= tol), count
+        assert np.all(np.abs(lse - (score + np.log(len(mine)))) <= 2.0 ** -21 * abs(score) + 1e-6), count
