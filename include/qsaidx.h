@@ -471,7 +471,8 @@ typedef struct qsa_attn_shape {
  *             that share it must be ordered.
  *
  * Keys and values of columns that no row of the request sees are not used, and
- * what only other rows see does not change a row, infinities and NaN included.
+ * what only other rows see does not change a row, infinities and NaN included; an
+ * infinite value that a row sees is infinite in its output.
  * A table entry outside [0, num_blocks) is not dereferenced: rows that see its
  * columns are NaN.  Weights are rounded to dtype before the second product (fp16:
  * those below 2^-27 of a row's largest to multiples of 2^-37 of it, or finer); sums,

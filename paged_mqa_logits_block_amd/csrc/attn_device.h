@@ -495,22 +495,32 @@ __device__ __forceinline__ const AttnArgs &launch_args() {
     return *(const AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-// One pair's softmax state over keys [k0, k1), by one wave with plain loads: the
-// key range of every pair is its own, where the tile kernels multiply a zero
-// weight with the value of a key that another row of the tile sees.  Taken only
-// when such a value is not finite (see the caller).
-template <int DT, int D>
-__device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, int k0,
-                                                    int k1, float &m, float &l, float (&o)[D / 64]) {
+// One pair's softmax state over its own keys of places [k0, k1), by one wave with
+// plain loads and 32-bit weights.  The tile kernels multiply a zero weight with the
+// values of keys that only other rows of the tile see and of the keys that fill up a
+// step (the last one once more), and weights below what the caches' type holds are
+// zero too: where such a value is infinite or NaN, the pair is done again here, with
+// no other key's value touched.  Taken only then (see the callers).  A place's token:
+// the place itself, or with `idx` that of the selected column, if it is below `limit`.
+template <int DT, int D, bool SPARSE>
+__device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk,
+                                                    const int32_t *idx, int limit, int k0, int k1, float &m, float &l,
+                                                    float (&o)[D / 64]) {
     const int lane = lane_id();
     m = kNegInf;
     l = 0.0f;
     for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
     for (int base = k0; base < k1; base += kWave) {
-        const int key = base + lane;
+        int64_t key = base + lane;
+        bool seen = key < k1;
+        if (SPARSE && seen) {
+            const int column = idx[(int)key / a.ratio];
+            key = (int64_t)column * a.ratio + (int)key % a.ratio;
+            seen = column >= 0 && key < limit;
+        }
         float s = kNegInf;
         int64_t off = 0;
-        if (key < k1) {
+        if (seen) {
             const uint32_t at = block_index(a, (uint32_t)key);
             const int e = a.block_table[(int64_t)req * a.max_blocks + at];
             const bool bad = e < 0 || e >= a.num_blocks;
@@ -520,13 +530,15 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
             for (int d = 0; d < D; ++d) dot += to_f32<DT>(q[d]) * to_f32<DT>(k[d]);
             s = bad ? __builtin_nanf("") : dot * a.scale_log2;
         }
+        const uint64_t mine = ballot(seen);
         const float top = fmaxf(m, wave_max_f(s));
         const float ref = top == kNegInf ? 0.0f : top;
         const float p = __builtin_amdgcn_exp2f(s - ref), keep = __builtin_amdgcn_exp2f(m - ref);
         l = l * keep + wave_sum_f(p);
         for (int i = 0; i < D / 64; ++i) o[i] *= keep;
         m = top;
-        for (int j = 0; j < min(kWave, k1 - base); ++j) {
+        for (int j = 0; j < kWave; ++j) {
+            if (!(mine >> j & 1)) continue;
             const float pj = readlane_f(p, j);
             const int64_t oj = ((int64_t)readlane((int)(off >> 32), j) << 32) | (uint32_t)readlane((int)off, j);
             const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache + oj);

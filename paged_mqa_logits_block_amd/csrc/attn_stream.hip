@@ -351,33 +351,29 @@ struct Stream {
             }
         }
         const Pair pp = pair_of(a, w, pm);
-        if (!SPARSE && least < keys) {
-            // A NaN can come from a value that only other rows of the tile see (zero
-            // weight times a value that is not finite; a pair whose own scores are NaN
-            // has a NaN sum): then every pair is done again over its own keys.
-            bool nan = false;
+        // A NaN can come from a zero weight times a value that is not finite (a pair
+        // whose own scores are NaN has a NaN sum): then the wave does its pairs again,
+        // each over its own keys.
+        bool nan = false;
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
-            if (__syncthreads_or(nan && pp.live && total == total)) {
-                float *again = reinterpret_cast<float *>(sh.ring[0]);
-                for (int p = wave; p < kAttnTile; p += kStreamWaves) {
-                    const Pair x = pair_of(a, w, p);
-                    if (!x.live) continue;
-                    float pm2, pl2, po[D / 64];
-                    own_range<DT, D>(launch_args(), w.req,
-                                     static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head, w.hk,
-                                     t0 * kStreamKeys, min(t1 * kStreamKeys, visible(a, x.row)), pm2, pl2, po);
-                    for (int i = 0; i < D / 64; ++i) again[p * D + lane * (D / 64) + i] = po[i];
-                    if (lane == 0) {
-                        sh.top_of[0][p] = pm2;
-                        sh.sum_of[0][p] = pl2;
-                    }
+        for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
+        if (ballot(nan && pp.live && total == total)) {
+            constexpr int kMine = kWave / kThreadsPer, kOwn = D / 64;  // pairs of a wave, outputs per lane there
+            for (int p = wave * kMine; p < (wave + 1) * kMine; ++p) {
+                const Pair x = pair_of(a, w, p);
+                if (!x.live) continue;
+                float pm2, pl2, po[kOwn];
+                own_range<DT, D, SPARSE>(launch_args(), max(w.req, 0),
+                                         static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
+                                         w.hk, idx, limit, t0 * kStreamKeys,
+                                         min(t1 * kStreamKeys, SPARSE ? keys : visible(a, x.row)), pm2, pl2, po);
+                top = pm == p ? pm2 : top;
+                total = pm == p ? pl2 : total;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) {  // d0 is a multiple of kOwn
+                    const float y = __int_as_float(shfl_i(__float_as_int(po[i % kOwn]), (d0 + i) / kOwn));
+                    r[i] = pm == p ? y : r[i];
                 }
-                __syncthreads();
-                top = sh.top_of[0][pm];
-                total = sh.sum_of[0][pm];
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) r[i] = again[pm * D + d0 + i];
             }
         }
         if (pp.live && dest) {

@@ -49,8 +49,8 @@ __device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, 
         if (r >= rows) break;
         const int row = row0 + r, head = hk * a.group + (m - r * a.group);
         float top, total, o[D / 64];
-        own_range<DT, D>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk, k0,
-                         min(k1, min(max(a.ctx_lens[row], 0), a.cap)), top, total, o);
+        own_range<DT, D, false>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk,
+                                nullptr, 0, k0, min(k1, min(max(a.ctx_lens[row], 0), a.cap)), top, total, o);
         if (dest) {
             for (int i = 0; i < D / 64; ++i) dest[m * D + lane * (D / 64) + i] = o[i];
             if (lane == 0) {
@@ -334,21 +334,16 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     total = xor32_sum(total);
 
     // The wave's pairs are done again, each over its own keys, where the tile met a
-    // table entry outside the pool, or where a NaN can come from a value that only
-    // other rows of the tile see (zero weight times a value that is not finite; a pair
-    // whose own scores are NaN has a NaN sum).
+    // table entry outside the pool, or where a NaN can come from a zero weight times a
+    // value that is not finite (a pair whose own scores are NaN has a NaN sum).
     if (ballot(met_bad) && lane == 0) sh.any_bad = 1;
     __syncthreads();
-    bool again = sh.any_bad != 0;
-    if (wave_least < keys) {
-        bool nan = false;
+    bool nan = false;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+    for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-            for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
-        again |= ballot(nan && live && total == total) != 0;
-    }
-    if (again) {
+        for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
+    if (sh.any_bad != 0 || ballot(nan && live && total == total)) {
         own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, dest);
         return;
     }

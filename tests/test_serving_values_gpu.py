@@ -112,3 +112,57 @@ def test_large_scores(kernel, dtype, size, sign):
         tol = (2 * u + (len(mine) + 8) * 2.0 ** -24) * np.abs(v[mine, 0].double().numpy()).mean(axis=0)
         assert np.all(np.abs(out - want) <= tol), count
         assert np.all(np.abs(lse - (score + np.log(len(mine)))) <= 2.0 ** -21 * abs(score) + 1e-6), count
+
+
+# ---------------------------------------------------------------------------
+# infinities that a row sees itself
+# ---------------------------------------------------------------------------
+
+def check_values(out, lse, q, k, v, counts, dtype):
+    """Against the 64-bit result where that is finite; infinities and NaN are equal."""
+    k, v = (x.to(DT[dtype]).double().numpy() for x in (k, v))
+    for r, c in enumerate(counts):
+        o, l, spread, size = ref.attend(q[r].double().numpy(), k[:c, 0], v[:c, 0], q.shape[2] ** -0.5)
+        finite = np.isfinite(o)
+        to, tl = ref.bounds(np.where(finite, o, 0), l, np.where(finite, spread, 0), size, c, q.shape[2],
+                            torch.finfo(DT[dtype]).eps / 2)
+        assert np.array_equal(out[r][~finite], o[~finite], equal_nan=True), r
+        assert np.all(np.abs(out[r][finite] - o[finite]) <= to[finite]), r
+        assert np.all(np.abs(lse[r] - l) <= tl), r
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("count", [1, 31, 33, 100, 128, 2000])
+def test_own_infinities(kernel, count):
+    """Infinite values at the first and the last token, and at the last multiple of 32,
+    of rows that all see the same tokens, whatever the count is a multiple of; and of
+    both signs in one element."""
+    rows, group = KERNELS[kernel]
+    d = 64
+    g = torch.Generator().manual_seed(count)
+    k, v = torch.randn(count, 1, d, generator=g), torch.randn(count, 1, d, generator=g)
+    v[0, 0, 3], v[-1, 0, 5], v[-1, 0, 40] = float("inf"), float("inf"), -float("inf")
+    v[0, 0, 60], v[-1, 0, 60], v[(count - 1) // 32 * 32, 0, 20] = float("inf"), -float("inf"), float("inf")
+    q = torch.randn(rows, group, d, generator=g).to(torch.bfloat16)
+    kc, vc, table = device_cache(k, v, "bf16")
+    with np.errstate(invalid="ignore"):
+        check_values(*attend_all(kernel, q.cuda(), kc, vc, table, [count] * rows), q, k, v, [count] * rows, "bf16")
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_infinity_of_a_small_weight(kernel, dtype):
+    """An infinite value whose weight (e^-31) the type holds or not is infinite in the
+    output."""
+    rows, group = KERNELS[kernel]
+    n, d = 300, 64
+    g = torch.Generator().manual_seed(7)
+    k, v = torch.zeros(n, 1, d), torch.randn(n, 1, d, generator=g)
+    k[5, 0, 0], v[250, 0, 9] = 31.0, float("inf")
+    q = torch.zeros(rows, group, d)
+    q[..., 0] = d ** 0.5
+    q = q.to(DT[dtype])
+    kc, vc, table = device_cache(k, v, dtype)
+    out, lse = attend_all(kernel, q.cuda(), kc, vc, table, [n] * rows)
+    assert np.all(out[:, :, 9] == np.inf)
+    check_values(out, lse, q, k, v, [n] * rows, dtype)
