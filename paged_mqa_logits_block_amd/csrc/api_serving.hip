@@ -134,6 +134,7 @@ struct AttnPlan {
     int sub_heads, num_subs;   // streaming: heads per workgroup, workgroups per kv head
     int tile_rows;             // query rows per tile
     int64_t slots;             // row tiles
+    int64_t tiles;             // a cut launch of the streaming kernel: the most tiles with rows
     int64_t bytes;             // workspace of a cut launch, 0: not cut
 };
 
@@ -150,8 +151,9 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
         p.stream = true;
         p.tile_rows = 1;
         p.slots = R;
+        p.tiles = R * heads;
         if (R <= qsa::kMaxSlots && R * heads <= kCutTiles && fills_badly(R * heads) && long_keys)
-            p.bytes = qsa::attn_workspace_bytes(s->head_dim, R * heads);
+            p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.tiles);
         return p;
     }
     // With at most four rows per request on average (a verify step), what one long
@@ -167,7 +169,8 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     if (p.slots > qsa::kMaxSlots || n > qsa::kMaxSlots || R > kCutRows || tiles > kCutTiles) return p;
     // the workgroups add up the slots' steps of 64 keys in 32 bits
     if (p.slots * (keys / 64 + 1) > 0x7FFFFFFF) return p;
-    if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.slots * heads);
+    p.tiles = (R / T + least) * heads;
+    if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.tiles);
     if (!p.stream && (n > 1 || fills_badly(tiles)))
         p.bytes = qsa::attn_tile_workspace_bytes(s->head_dim, p.slots * s->num_kv_heads);
     return p;
@@ -282,6 +285,7 @@ void launch_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.num_subs = p.num_subs;
     a.tile_rows = p.tile_rows;
     a.slots = (int32_t)p.slots;
+    a.tiles = (int32_t)p.tiles;
     a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
 }
 

@@ -53,6 +53,7 @@ struct AttnArgs {
     int32_t div_shift;
     // launch shape
     int32_t slots;              // row tiles of the grid
+    int32_t tiles;              // the most tiles with rows, of all head parts (a cut launch)
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile

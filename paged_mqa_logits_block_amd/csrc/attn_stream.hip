@@ -21,8 +21,8 @@
 // requests of mixed lengths keep the whole chip busy to the end.  A tile that is
 // cut leaves its parts' states (32-bit maximum, sum, unnormalised output) in the
 // workspace and a second kernel joins them; part (workgroup, tile) has place
-// workgroup + tile, as both only grow along the line.  With many tiles each gets
-// a workgroup.
+// workgroup + tile, as both only grow along the line (tiles are numbered without the
+// slots that have no rows).  With many tiles each gets a workgroup.
 //
 // Measured (kernel traces): a verify step of 9 requests with 4 rows, 16,000 to 65,600
 // tokens, 539 MB of cache at D = 128, 32 over 4 heads, bf16: 107 us and 6 for the
@@ -427,9 +427,34 @@ __device__ __forceinline__ int group_of(int64_t u, int64_t total) {
     return (int)(((u + 1) * groups_of(total) + total - 1) / total) - 1;
 }
 
-// the workgroups with parts of a tile, and its rows
+// the workgroups with parts of a tile, its head part and its rows
 struct TileSpan {
-    int first, last, row0, rows;
+    int16_t first, last;
+    int hs, row0, rows;
+};
+
+// Which slots have rows: a thread's kPer consecutive slots as kPer masks of its wave.
+struct LiveSlots {
+    static constexpr int kPer = kMaxSlots / kStreamThreads;
+    uint64_t mask[kStreamWaves][kPer];
+
+    __device__ __forceinline__ int all() const {
+        int n = 0;
+        for (int w = 0; w < kStreamWaves; ++w)
+            for (int i = 0; i < kPer; ++i) n += __builtin_popcountll(mask[w][i]);
+        return n;
+    }
+    // how many of them lie before `slot`
+    __device__ __forceinline__ int before(int slot) const {
+        const int thread = slot / kPer, wave = thread / kWave, lane = thread % kWave;
+        int n = 0;
+        for (int w = 0; w <= wave; ++w)
+            for (int i = 0; i < kPer; ++i) {
+                const uint64_t below = ((uint64_t)1 << lane) - 1 + ((uint64_t)(i < slot % kPer) << lane);
+                n += __builtin_popcountll(w < wave ? mask[w][i] : mask[w][i] & below);
+            }
+        return n;
+    }
 };
 
 // Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
@@ -442,42 +467,45 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
     __shared__ int32_t wave_sums[kStreamWaves];
     const int t = threadIdx.x, g = blockIdx.x;
     const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
-    __shared__ Requests requests;  // dense only
+    __shared__ Requests requests;  // dense only, as is `live`
+    __shared__ LiveSlots live;
     if constexpr (SPARSE) {
         const int u = units_of(a.k * a.ratio);
         for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
         __syncthreads();
     } else {
         slot_counts<kStreamThreads>(a, requests, before);
-        constexpr int kPer = kMaxSlots / kStreamThreads;
+        constexpr int kPer = LiveSlots::kPer;
         int u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
             u[i] = keys < 0 ? 0 : units_of(keys);
+            const uint64_t with_rows = ballot(keys >= 0);
+            if ((t & 63) == 0) live.mask[t >> 6][i] = with_rows;
         }
         __syncthreads();
         slot_sums<kStreamThreads>(before, slots, u, wave_sums);
     }
-    const int per_head = before[slots];
+    const int per_head = before[slots], tiles = SPARSE ? slots : live.all();  // of a head part
+    const auto tile_of = [&](int hs, int slot) { return hs * tiles + (SPARSE ? slot : live.before(slot)); };
     const int64_t total = (int64_t)per_head * hss;
     if (g > 0 && g >= groups_of(total)) return;
     if (g == 0) {  // which workgroups have parts of each tile
-        TileSpan *spans = reinterpret_cast<TileSpan *>(part_of<D>(a, kStreamGroups, slots * hss));
+        TileSpan *spans = reinterpret_cast<TileSpan *>(part_of<D>(a, kStreamGroups, a.tiles));
+        for (int i = tiles * hss + t; i < a.tiles; i += kStreamThreads) spans[i] = {};
         for (int i = t; i < slots * hss; i += kStreamThreads) {
             const int hs = i / slots, slot = i - hs * slots;
             const int64_t u0 = (int64_t)hs * per_head + before[slot], u1 = (int64_t)hs * per_head + before[slot + 1];
-            TileSpan s = {0, 0, slot, 1};
-            if (u1 > u0) {
-                s.first = group_of(u0, total);
-                s.last = group_of(u1 - 1, total);
-                if constexpr (!SPARSE) {
-                    const RowTile w = find_tile(a, requests, slot);
-                    s.row0 = w.row0;
-                    s.rows = w.rows;
-                }
+            if (u1 == u0) continue;
+            TileSpan s = {(int16_t)group_of(u0, total), (int16_t)group_of(u1 - 1, total), hs, slot, 1};
+            if constexpr (!SPARSE) {
+                const RowTile w = find_tile(a, requests, slot);
+                s.row0 = w.row0;
+                s.rows = w.rows;
             }
-            spans[i] = s;
+            const int tile = tile_of(hs, slot);
+            if (tile < a.tiles) spans[tile] = s;
         }
     }
     if (total == 0) return;
@@ -509,7 +537,12 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
         const int steps = (keys + kStreamKeys - 1) / kStreamKeys;
         const int t0 = __builtin_amdgcn_readfirstlane((int)(u - tile0) * kStreamWaves);
         const int t1 = __builtin_amdgcn_readfirstlane(min((int)(stop - tile0) * kStreamWaves, steps));
-        float *dest = u == tile0 && stop == tile1 ? nullptr : part_of<D>(a, g, hs * slots + slot);
+        float *dest = nullptr;
+        if (u > tile0 || stop < tile1) {
+            // q_starts that decrease could make more tiles than there are places for
+            const int tile = tile_of(hs, slot);
+            if (tile < a.tiles) dest = part_of<D>(a, g, tile);
+        }
         S::run(a, sh, w, keys, t0, t1, dest);
         u = stop;
         __syncthreads();  // the joined states have been read before the next copies land
@@ -518,13 +551,13 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
 
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
-    const int hss = a.num_kv_heads * a.num_subs, tile = blockIdx.x, hs = tile / a.slots;
-    const TileSpan s = reinterpret_cast<const TileSpan *>(part_of<D>(a, kStreamGroups, a.slots * hss))[tile];
+    const int tile = blockIdx.x;
+    const TileSpan s = reinterpret_cast<const TileSpan *>(part_of<D>(a, kStreamGroups, a.tiles))[tile];
     if (s.last <= s.first) return;
     constexpr int kPairs = kJoinThreads / (D / 4);
     const int m = blockIdx.y * kPairs + threadIdx.x / (D / 4);
     TileWork w;
-    part_heads(a, hs, w);
+    part_heads(a, s.hs, w);
     w.row0 = s.row0;
     w.rows = s.rows;
     const Pair pp = pair_of(a, w, m);
@@ -549,7 +582,7 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>),
-                       dim3((unsigned)a.slots * heads, kAttnTile * (D / 4) / kJoinThreads), dim3(kJoinThreads), 0, s, a);
+                       dim3((unsigned)a.tiles, kAttnTile * (D / 4) / kJoinThreads), dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }
 

@@ -142,6 +142,21 @@ def test_attention_workspace():
                  0) == m.E_RANGE
 
 
+@pytest.mark.parametrize("rows,reqs,kv_heads", [(20, 20, 32), (20, 1000, 32), (1, 1000, 1024), (1, 1023, 1), (600, 600, 1),
+                                                (4, 500, 250)])
+def test_attention_workspace_is_bounded(rows, reqs, kv_heads):
+    """Requests without rows cost no workspace: a state of 32 pairs (and a note) for
+    each of 256 workgroups and for each of at most 2 x 1,024 tiles with rows is all
+    that a cut launch of the streaming kernel leaves."""
+    def need(n):
+        s = attn_shape(num_rows=rows, num_reqs=n, num_heads=8 * kv_heads, num_kv_heads=kv_heads,
+                       q_row_stride=1024 * kv_heads, out_row_stride=1024 * kv_heads)
+        return m.paged_attention_workspace_bytes(s)
+    state = 32 * 130 * 4 + 16
+    assert 0 < need(reqs) <= (256 + 2 * 1024) * state
+    assert need(reqs) == need(min(rows, reqs))
+
+
 def test_host_tensors_are_refused():
     import torch
     q = torch.zeros(4, 8, 64, dtype=torch.bfloat16)

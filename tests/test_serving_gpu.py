@@ -344,6 +344,22 @@ def test_paged_attention_many_requests(rows, group):
     assert not torch.any(torch.isnan(out))
 
 
+@pytest.mark.parametrize("kw", [dict(group=8, hk=4), dict(group=40, hk=2, dim=64, dtype="fp16")])
+def test_paged_attention_few_of_many_requests(kw):
+    """A table of 1,000 requests of which five have rows, some over long contexts whose
+    tiles are cut, some that see nothing."""
+    past, new = [0] * 1000, [0] * 1000
+    for i, p, a in ((0, 3000, 1), (17, 9, 3), (500, 12_000, 2), (501, 0, 1), (999, 700, 4)):
+        past[i], new[i] = p, a
+    b = Batch(16, past, new, pad=2, **kw)
+    b.ctx[4] = 0
+    assert m.paged_attention_workspace_bytes(m.make_attn_shape(b.q.cuda(), b.kc, b.table)) > 0
+    for workspace in ("auto", None):
+        out, lse = run_paged(b, workspace=workspace)
+        b.check(out, lse, lambda r: range(b.ctx[r]))
+        assert torch.all(out[b.rows:] == 3.0) and torch.all(lse[b.rows:] == 7.0)
+
+
 def test_paged_attention_many_rows():
     """More rows than a cut launch takes: every tile whole."""
     b = Batch(15, [10, 5], [8000, 300], hk=1, group=1, dim=64)
