@@ -148,8 +148,9 @@ class PreparedPlanBatch(_Prepared):
     def __init__(self, past_lens, new_lens, free_blocks, block_table, *, block_size: int, num_blocks: int,
                  out: BatchPlan, ratio: int = 1, stream=None):
         import torch
+        buffers = {f.name: getattr(out, f.name) for f in dataclasses.fields(out)}
         dev = _one_device(past_lens=past_lens, new_lens=new_lens, free_blocks=free_blocks, block_table=block_table,
-                          **{f.name: getattr(out, f.name) for f in dataclasses.fields(out)})
+                          **buffers)
         _require(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous(),
                  "block_table must be contiguous int32 [n, max_blocks]")
         n = int(block_table.shape[0])
@@ -173,7 +174,8 @@ class PreparedPlanBatch(_Prepared):
         self.out = out
         self._ready(lib.qsa_plan_batch,
                     (*ins, *outs, _ptr(out.col_lens), _ptr(out.col_slots), _ptr(out.blocks_used),
-                     ctypes.byref(shape)), dev, stream, (past_lens, new_lens, free_blocks, block_table, out, shape))
+                     ctypes.byref(shape)), dev, stream,
+                    (past_lens, new_lens, free_blocks, block_table, buffers, shape))
 
     def __call__(self) -> BatchPlan:
         self._launch()

@@ -102,6 +102,25 @@ def test_plan_optional_outputs_and_bad_entries():
     assert out.slots.cpu().tolist() == [-1, -1, 20, 21, 22, 23]
 
 
+def test_prepared_plan_keeps_its_buffers():
+    """The buffers of a prepared call live as long as it does, whatever becomes of the
+    BatchPlan's fields."""
+    import gc
+    import weakref
+    out = m.BatchPlan.empty(2, 6, "cuda")
+    fields = ("q_starts", "row_to_req", "ctx_lens", "slots", "col_lens", "col_slots", "blocks_used")
+    alive = [weakref.ref(getattr(out, f)) for f in fields]
+    call = m.PreparedPlanBatch(dev(np.zeros(2, np.int32)), dev(np.ones(2, np.int32)), dev(np.arange(4, dtype=np.int32)),
+                               dev(np.full((2, 3), -1, np.int32)), block_size=4, num_blocks=10, out=out)
+    for f in fields:
+        setattr(out, f, None)
+    gc.collect()
+    assert all(r() is not None for r in alive)
+    del call
+    gc.collect()
+    assert all(r() is None for r in alive)
+
+
 # ---------------------------------------------------------------------------
 # cache writes
 # ---------------------------------------------------------------------------
