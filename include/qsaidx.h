@@ -500,6 +500,11 @@ QSA_API int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *shape)
  * The order of a row's indices does not matter; an index given twice counts
  * twice.  A row without tokens has out 0 and lse -inf.
  *
+ * qsa_topk over qsa_plan_batch's col_lens selects whole columns.  A row's newest
+ * ctx_lens % ratio tokens, its own among them, are in none of those: a caller that
+ * wants them gives column ctx_lens / ratio as one index more per row, which
+ * token_lens = ctx_lens cuts behind the row's own token.
+ *
  *   row_to_req [R] int32; a value outside [0, num_reqs) makes the row's outputs
  *              NaN (if it selects anything).
  *   idx        [R][k] int32, negative entries are padding, anywhere.

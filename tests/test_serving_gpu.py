@@ -743,6 +743,37 @@ def test_serving_steps():
         server.check(new)
 
 
+def test_selection_with_the_newest_tokens():
+    """Selected columns are whole ones; with the column that a row stands in as one
+    index more, each row sees its own token, and all tokens while they fit."""
+    step = Step()
+    server = Server(step, 3)
+    for new in STEPS:
+        server.load(new)
+        step.run()
+        ratio, plan = step.RATIO, step.plan
+        tail = torch.where(plan.ctx_lens % ratio > 0, plan.col_lens, -1)
+        idx = torch.cat([step.idx, tail[:, None]], dim=1)
+        out = m.sparse_attention(step.q, step.kc, step.vc, step.table, plan.row_to_req, idx, ratio=ratio,
+                                 token_lens=plan.ctx_lens)
+        server.commit(new)
+        at = 0
+        for i, a in enumerate(new):
+            for r in range(at, at + a):
+                ctx = server.lens[i] - a + r - at + 1
+                toks = tokens_of(idx[r], ratio, ctx)
+                assert ctx - 1 in toks and len(set(toks)) == len(toks)
+                if ctx <= step.TOPK * ratio:
+                    assert sorted(toks) == list(range(ctx))
+                for h in range(step.HK):
+                    hs = slice(h * step.GROUP, (h + 1) * step.GROUP)
+                    o, l, spread, size = ref.attend(step.q[r, hs].double().cpu().numpy(), server.k[i][toks, h].numpy(),
+                                                    server.v[i][toks, h].numpy(), step.D ** -0.5)
+                    tol, _ = ref.bounds(o, l, spread, size, len(toks), step.D, torch.finfo(torch.bfloat16).eps / 2)
+                    assert np.all(np.abs(out[r, hs].double().cpu().numpy() - o) <= tol), (i, r, h)
+            at += a
+
+
 def test_serving_steps_captured():
     """The same from one captured graph, replayed with the program's own work
     between the replays."""
