@@ -114,6 +114,17 @@ def test_attention_pointers_and_sizes():
         assert m.lib.qsa_sparse_attention_check(A, A, A, A, A, A, k, ratio, A, s, None, 0) == st
 
 
+@pytest.mark.parametrize("kw,status", [
+    (dict(num_rows=1 << 21), "OK"), (dict(num_rows=(1 << 21) + 1), "E_RANGE"),
+    (dict(num_reqs=1 << 21, num_heads=8, num_kv_heads=1), "OK"), (dict(num_reqs=(1 << 21) + 1, num_heads=8, num_kv_heads=1), "E_RANGE"),
+    (dict(max_blocks=1 << 20, block_size=1024), "OK"), (dict(max_blocks=(1 << 20) + 1, block_size=1024), "E_RANGE"),
+])
+def test_attention_limits(kw, status):
+    s = attn_shape(**kw)
+    assert m.lib.qsa_paged_attention_check(A, A, A, A, A, A, A, s, None, 0) == getattr(m, status), m.last_error()
+    assert m.lib.qsa_sparse_attention_check(A, A, A, A, A, A, 2048, 4, A, s, None, 0) == getattr(m, status)
+
+
 def test_attention_workspace():
     """A workspace is wanted only where few rows meet long tables; one that is
     given must hold it."""

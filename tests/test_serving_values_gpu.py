@@ -9,7 +9,7 @@ torch = pytest.importorskip("torch")
 m = pytest.importorskip("paged_mqa_logits_block_amd")
 
 import serving_ref as ref  # noqa: E402
-from test_serving_gpu import DT, dev  # noqa: E402
+from test_serving_gpu import Batch, DT, dev, run_paged  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,71 @@ def test_infinity_of_a_small_weight(kernel, dtype):
     out, lse = attend_all(kernel, q.cuda(), kc, vc, table, [n] * rows)
     assert np.all(out[:, :, 9] == np.inf)
     check_values(out, lse, q, k, v, [n] * rows, dtype)
+
+
+# ---------------------------------------------------------------------------
+# entries outside the pool, values of others, in launches whose tiles are not cut too
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("workspace", ["auto", None])
+@pytest.mark.parametrize("past,new", [([206], [3]), ([206, 333], [4, 2]), ([206], [80]), ([206, 333], [70, 60])])
+def test_bad_entries_cut_and_whole(past, new, workspace):
+    b = Batch(12, past, new, group=4)
+    b.table = b.table.clone()
+    first = (past[0] + 2) // b.block  # the entry of the request's third new row on
+    b.table[0, first] = b.kc.shape[0]
+    out, lse = run_paged(b, workspace=workspace)
+    clean = [r for r in range(b.rows) if b.req[r] == 1 or b.ctx[r] <= first * b.block]
+    assert 0 < len(clean) < b.rows
+    b.check(out, lse, lambda r: range(b.ctx[r]), rows=clean)
+    for r in set(range(b.rows)) - set(clean):
+        assert torch.all(torch.isnan(out[r])) and torch.all(torch.isnan(lse[r])), r
+
+
+@pytest.mark.parametrize("workspace", ["auto", None])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("past,new", [([200], [4]), ([200, 333], [4, 2]), ([200], [80]), ([200, 333], [70, 60])])
+def test_values_others_see_cut_and_whole(past, new, value, workspace):
+    b = Batch(11, past, new, group=4)
+    bad = past[0] + new[0] // 2  # seen by the later rows of request 0 only
+    b.vc[int(b.table[0, bad // b.block]), bad % b.block] = value
+    out, lse = run_paged(b, workspace=workspace)
+    clean = [r for r in range(b.rows) if b.req[r] == 1 or b.ctx[r] <= bad]
+    b.check(out, lse, lambda r: range(b.ctx[r]), rows=clean)
+    for r in set(range(b.rows)) - set(clean):
+        assert torch.all(torch.isnan(out[r]) if np.isnan(value) else out[r] == value), r
+
+
+# ---------------------------------------------------------------------------
+# the two attentions, and keys that are not finite
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,group", [("bf16", 8), ("fp16", 20)])
+def test_selection_of_everything(dtype, group):
+    """With every token selected both attentions give the 64-bit result, and so are
+    within both bounds of each other."""
+    b = Batch(90, [250, 90], [4, 4], group=group, dtype=dtype)
+    idx = np.where(np.arange(256)[None, :] < b.ctx[:, None], np.arange(256), -1).astype(np.int32)
+    lse = torch.empty(b.q.shape[:2], device="cuda")
+    out = m.sparse_attention(b.q.cuda(), b.kc, b.vc, b.table, dev(b.req.astype(np.int32)), dev(idx), lse=lse)
+    b.check(out, lse, lambda r: range(b.ctx[r]))
+    b.check(*run_paged(b), lambda r: range(b.ctx[r]))
+
+
+@pytest.mark.parametrize("layout", [m.KV_PAGED, m.KV_COPACKED, m.KV_COPACKED_SHUFFLED])
+def test_keys_not_finite_stay_so(layout):
+    """A key with an infinity or a NaN is stored as one that is not finite: the element
+    itself, and with an infinity (whose scale is infinite) all of them."""
+    x = torch.ones(5, 64, dtype=torch.bfloat16)
+    x[1, 3], x[2, 7], x[4, 63] = float("inf"), float("nan"), -float("inf")
+    kc = torch.zeros(1, 16 * (64 if layout == m.KV_PAGED else 68), dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(1, 16, device="cuda") if layout == m.KV_PAGED else None
+    m.write_keys(x.cuda(), torch.arange(5).cuda(), kc, block_size=16, kscale=ks, layout=layout)
+    codes = kc.cpu()[0, :16 * 64].view(torch.float8_e4m3fn).float()
+    codes = codes.view(4, 16, 16).transpose(0, 1).reshape(16, 64) if layout == m.KV_COPACKED_SHUFFLED else codes.view(16, 64)
+    scale = ks.cpu()[0] if ks is not None else kc.cpu()[0, 16 * 64:].view(torch.float32)
+    back = codes * scale[:, None]
+    assert torch.all(~torch.isfinite(back[1])) and torch.all(~torch.isfinite(back[4]))
+    assert torch.isnan(back[2, 7]) and torch.all(torch.isfinite(back[2, :7])) and torch.all(torch.isfinite(back[2, 8:]))
+    for r in (0, 3):
+        assert torch.all(back[r] == 448.0 * (torch.tensor(1.0) / 448.0)), r
