@@ -433,27 +433,30 @@ struct TileSpan {
     int hs, row0, rows;
 };
 
-// Which slots have rows: a thread's kPer consecutive slots as kPer masks of its wave.
+// Which slots have rows: bit l of word kPer w + i is that of slot kPer (64 w + l) + i,
+// the i-th of lane l of wave w.
 struct LiveSlots {
-    static constexpr int kPer = kMaxSlots / kStreamThreads;
-    uint64_t mask[kStreamWaves][kPer];
+    static constexpr int kPer = kMaxSlots / kStreamThreads, kWords = kStreamWaves * kPer;
+    uint64_t words[kWords];
 
-    __device__ __forceinline__ int all() const {
-        int n = 0;
-        for (int w = 0; w < kStreamWaves; ++w)
-            for (int i = 0; i < kPer; ++i) n += __builtin_popcountll(mask[w][i]);
-        return n;
+    // how many slots before `slot` have rows, in word n
+    __device__ __forceinline__ int count(int n, int slot) const {
+        const int thread = slot / kPer - kWave * (n / kPer);  // `slot` is its slot % kPer
+        const int lanes = thread + (n % kPer < slot % kPer);   // lanes whose slot of the word lies before
+        const uint64_t below = lanes <= 0 ? 0 : lanes >= kWave ? ~(uint64_t)0 : ((uint64_t)1 << lanes) - 1;
+        return __builtin_popcountll(words[n] & below);
     }
-    // how many of them lie before `slot`
+    // all words, by one wave
     __device__ __forceinline__ int before(int slot) const {
-        const int thread = slot / kPer, wave = thread / kWave, lane = thread % kWave;
-        int n = 0;
-        for (int w = 0; w <= wave; ++w)
-            for (int i = 0; i < kPer; ++i) {
-                const uint64_t below = ((uint64_t)1 << lane) - 1 + ((uint64_t)(i < slot % kPer) << lane);
-                n += __builtin_popcountll(w < wave ? mask[w][i] : mask[w][i] & below);
-            }
-        return n;
+        static_assert(kWords <= kWave, "a word per lane");
+        const int n = lane_id();
+        return wave_total_sum(n < kWords ? count(n, slot) : 0);
+    }
+    // the same by one thread
+    __device__ __forceinline__ int before_alone(int slot) const {
+        int sum = 0;
+        for (int n = 0; n < kWords; ++n) sum += count(n, slot);
+        return sum;
     }
 };
 
@@ -482,13 +485,13 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
             const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
             u[i] = keys < 0 ? 0 : units_of(keys);
             const uint64_t with_rows = ballot(keys >= 0);
-            if ((t & 63) == 0) live.mask[t >> 6][i] = with_rows;
+            if ((t & 63) == 0) live.words[kPer * (t >> 6) + i] = with_rows;
         }
         __syncthreads();
         slot_sums<kStreamThreads>(before, slots, u, wave_sums);
     }
-    const int per_head = before[slots], tiles = SPARSE ? slots : live.all();  // of a head part
-    const auto tile_of = [&](int hs, int slot) { return hs * tiles + (SPARSE ? slot : live.before(slot)); };
+    const int per_head = before[slots];
+    const int tiles = SPARSE ? slots : live.before(slots);  // of a head part
     const int64_t total = (int64_t)per_head * hss;
     if (g > 0 && g >= groups_of(total)) return;
     if (g == 0) {  // which workgroups have parts of each tile
@@ -504,7 +507,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
                 s.row0 = w.row0;
                 s.rows = w.rows;
             }
-            const int tile = tile_of(hs, slot);
+            const int tile = hs * tiles + (SPARSE ? slot : live.before_alone(slot));
             if (tile < a.tiles) spans[tile] = s;
         }
     }
@@ -540,7 +543,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
         float *dest = nullptr;
         if (u > tile0 || stop < tile1) {
             // q_starts that decrease could make more tiles than there are places for
-            const int tile = tile_of(hs, slot);
+            const int tile = hs * tiles + (SPARSE ? slot : live.before(slot));
             if (tile < a.tiles) dest = part_of<D>(a, g, tile);
         }
         S::run(a, sh, w, keys, t0, t1, dest);
