@@ -495,39 +495,106 @@ __device__ __forceinline__ const AttnArgs &launch_args() {
     return *(const AttnArgs *)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-// One pair's softmax state over its own keys of places [k0, k1), by one wave with
-// plain loads and 32-bit weights.  The tile kernels multiply a zero weight with the
-// values of keys that only other rows of the tile see and of the keys that fill up a
-// step (the last one once more), and weights below what the caches' type holds are
-// zero too: where such a value is infinite or NaN, the pair is done again here, with
-// no other key's value touched.  Taken only then (see the callers).  A place's token:
-// the place itself, or with `idx` that of the selected column, if it is below `limit`.
+// Outputs that are NaN though the pair's sum is a number.  The kernels multiply a zero
+// weight with the values of keys that only other rows of the tile see, of the keys that
+// fill up a step (the last one once more) and of those whose weight is below what the
+// caches' type holds; where such a value is infinite or NaN, so is the product.  What the
+// element is follows from the values that the pair itself sees: NaN, or infinities of
+// both signs, make it NaN, infinities of one sign infinite, and otherwise it is finite
+// and the pair is done again over its own keys.  The first place of each of the three
+// kinds is found once per wave, for all its pairs.  (Doing every such pair again, one NaN
+// that all rows see took 168 ms for 2,048 rows at 16,384 tokens.)
+//
+// Places are tokens, or with SPARSE the entries of `idx` times `ratio`; a lane has the
+// elements lane D / 64 on.  All this is cold.
+
+// the lane's place: false if it has no token, or one behind a table entry outside the pool
+template <bool SPARSE>
+__device__ __forceinline__ bool place_offset(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit, int place,
+                                             int64_t &off, bool &bad) {
+    int64_t key = place;
+    if constexpr (SPARSE) {
+        const int column = idx[place / a.ratio];
+        key = (int64_t)column * a.ratio + place % a.ratio;
+        if (column < 0 || key >= limit) return false;
+    }
+    const uint32_t at = block_index(a, (uint32_t)key);
+    const int e = a.block_table[(int64_t)req * a.max_blocks + at];
+    bad = e < 0 || e >= a.num_blocks;
+    if (!bad) off = kv_offset(a, e, (uint32_t)key - at * (uint32_t)a.block_size, hk);
+    return true;
+}
+
+// The lane's elements of the values at off of lanes j .. j + 7; any lane's off is in the
+// pool (0 where it has no token).
+template <int D>
+__device__ __forceinline__ void value_rows(const AttnArgs &a, int64_t off, int j, uint16_t (&x)[8][D / 64]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t at = ((int64_t)readlane((int)(off >> 32), j + i) << 32) | (uint32_t)readlane((int)off, j + i);
+        const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache + at) + lane_id() * (D / 64);
+        if constexpr (D == 128) *reinterpret_cast<uint32_t *>(x[i]) = *reinterpret_cast<const uint32_t *>(v);
+        else x[i][0] = v[0];
+    }
+}
+
+// first places of values that are NaN, infinite and minus infinite
+template <int D>
+struct FirstPlaces {
+    int nan[D / 64], inf[D / 64], minus[D / 64];
+};
+
 template <int DT, int D, bool SPARSE>
-__device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk,
-                                                    const int32_t *idx, int limit, int k0, int k1, float &m, float &l,
-                                                    float (&o)[D / 64]) {
-    const int lane = lane_id();
+__device__ __forceinline__ FirstPlaces<D> first_places(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit,
+                                                       int k0, int k1) {
+    FirstPlaces<D> f;
+    for (int i = 0; i < D / 64; ++i) f.nan[i] = f.inf[i] = f.minus[i] = 0x7FFFFFFF;
+    for (int base = k0; base < k1; base += kWave) {
+        int64_t off = 0;
+        bool bad = false;
+        const bool seen = base + lane_id() < k1 && place_offset<SPARSE>(a, req, hk, idx, limit, base + lane_id(), off, bad);
+        const uint64_t mine = ballot(seen && !bad);
+        for (int j = 0; j < kWave; j += 8) {
+            uint16_t x[8][D / 64];
+            value_rows<D>(a, off, j, x);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (!(mine >> (j + u) & 1)) continue;
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const float v = to_f32<DT>(x[u][i]);
+                    if (v != v) f.nan[i] = min(f.nan[i], base + j + u);
+                    if (v == -kNegInf) f.inf[i] = min(f.inf[i], base + j + u);
+                    if (v == kNegInf) f.minus[i] = min(f.minus[i], base + j + u);
+                }
+            }
+        }
+    }
+    return f;
+}
+
+// One pair's softmax state over its own places [k0, k1), by one wave with plain loads
+// and 32-bit weights: no other key's value is touched.
+template <int DT, int D, bool SPARSE>
+__device__ __forceinline__ void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, const int32_t *idx,
+                                          int limit, int k0, int k1, float &m, float &l, float (&o)[D / 64]) {
     m = kNegInf;
     l = 0.0f;
     for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
     for (int base = k0; base < k1; base += kWave) {
-        int64_t key = base + lane;
-        bool seen = key < k1;
-        if (SPARSE && seen) {
-            const int column = idx[(int)key / a.ratio];
-            key = (int64_t)column * a.ratio + (int)key % a.ratio;
-            seen = column >= 0 && key < limit;
-        }
-        float s = kNegInf;
         int64_t off = 0;
+        bool bad = false;
+        const bool seen = base + lane_id() < k1 && place_offset<SPARSE>(a, req, hk, idx, limit, base + lane_id(), off, bad);
+        float s = kNegInf;
         if (seen) {
-            const uint32_t at = block_index(a, (uint32_t)key);
-            const int e = a.block_table[(int64_t)req * a.max_blocks + at];
-            const bool bad = e < 0 || e >= a.num_blocks;
-            off = kv_offset(a, bad ? 0 : e, (uint32_t)key - at * (uint32_t)a.block_size, hk);
-            const uint16_t *k = reinterpret_cast<const uint16_t *>(a.kcache + off);
+            const i32x4 *k = reinterpret_cast<const i32x4 *>(a.kcache + off);
             float dot = 0.0f;
-            for (int d = 0; d < D; ++d) dot += to_f32<DT>(q[d]) * to_f32<DT>(k[d]);
+            for (int c = 0; c < D / 8; ++c) {
+                const i32x4 x = k[c];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    dot += to_f32<DT>(q[8 * c + e]) * to_f32<DT>((uint16_t)((uint32_t)x[e >> 1] >> (16 * (e & 1))));
+            }
             s = bad ? __builtin_nanf("") : dot * a.scale_log2;
         }
         const uint64_t mine = ballot(seen);
@@ -537,13 +604,64 @@ __device__ __attribute__((noinline)) void own_range(const AttnArgs &a, int req, 
         l = l * keep + wave_sum_f(p);
         for (int i = 0; i < D / 64; ++i) o[i] *= keep;
         m = top;
-        for (int j = 0; j < kWave; ++j) {
-            if (!(mine >> j & 1)) continue;
-            const float pj = readlane_f(p, j);
-            const int64_t oj = ((int64_t)readlane((int)(off >> 32), j) << 32) | (uint32_t)readlane((int)off, j);
-            const uint16_t *v = reinterpret_cast<const uint16_t *>(a.vcache + oj);
-            for (int i = 0; i < D / 64; ++i) o[i] += pj * to_f32<DT>(v[lane * (D / 64) + i]);
+        for (int j = 0; j < kWave; j += 8) {
+            uint16_t x[8][D / 64];
+            value_rows<D>(a, off, j, x);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (!(mine >> (j + u) & 1)) continue;
+                const float pj = readlane_f(p, j + u);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) o[i] += pj * to_f32<DT>(x[u][i]);
+            }
         }
+    }
+}
+
+// A pair's place in the outputs, or with `state` in a cut tile's part.
+struct PairPlace {
+    const uint16_t *q;
+    void *out;
+    float *lse;                   // or null
+    float *state, *top, *total;   // all null, or the state's outputs, reference and sum
+};
+
+// Mends what the wave has written of one pair, or does the pair anew (`anew`).
+template <int DT, int D, bool SPARSE>
+__device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit, int k0, int k1,
+                                          const FirstPlaces<D> &f, bool anew, const PairPlace &p) {
+    typedef typename Half<DT>::T T;
+    const int at = lane_id() * (D / 64);
+    T *out = static_cast<T *>(p.out) + at;
+    float o[D / 64], top, total, inv = 1.0f;
+    bool finite = anew, write = false;
+    if (!anew) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+            o[i] = p.state ? p.state[at + i] : (float)out[i];
+            if (o[i] == o[i]) continue;
+            const bool inf = f.inf[i] < k1, minus = f.minus[i] < k1;
+            if (f.nan[i] < k1 || (inf && minus)) continue;
+            finite |= !inf && !minus;
+            write = true;
+            o[i] = inf ? -kNegInf : kNegInf;
+        }
+    }
+    if (ballot(finite)) {
+        own_range<DT, D, SPARSE>(a, req, p.q, hk, idx, limit, k0, k1, top, total, o);
+        write = true;
+        if (lane_id() == 0 && p.state) {
+            *p.top = top;
+            *p.total = total;
+        }
+        if (lane_id() == 0 && !p.state && p.lse) *p.lse = (top + __builtin_amdgcn_logf(total)) * kLn2;
+        if (!p.state) inv = total == 0.0f ? 0.0f : 1.0f / total;
+    }
+    if (!write) return;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+        if (p.state) p.state[at + i] = o[i];
+        else out[i] = (T)(o[i] * inv);
     }
 }
 

@@ -351,31 +351,12 @@ struct Stream {
             }
         }
         const Pair pp = pair_of(a, w, pm);
-        // A NaN can come from a zero weight times a value that is not finite (a pair
-        // whose own scores are NaN has a NaN sum): then the wave does its pairs again,
-        // each over its own keys.
+        // a NaN output whose own sum is a number is mended (a pair whose own scores are
+        // NaN has a NaN sum)
         bool nan = false;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) nan |= r[i] != r[i];
-        if (ballot(nan && pp.live && total == total)) {
-            constexpr int kMine = kWave / kThreadsPer, kOwn = D / 64;  // pairs of a wave, outputs per lane there
-            for (int p = wave * kMine; p < (wave + 1) * kMine; ++p) {
-                const Pair x = pair_of(a, w, p);
-                if (!x.live) continue;
-                float pm2, pl2, po[kOwn];
-                own_range<DT, D, SPARSE>(launch_args(), max(w.req, 0),
-                                         static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
-                                         w.hk, idx, limit, t0 * kStreamKeys,
-                                         min(t1 * kStreamKeys, SPARSE ? keys : visible(a, x.row)), pm2, pl2, po);
-                top = pm == p ? pm2 : top;
-                total = pm == p ? pl2 : total;
-#pragma unroll
-                for (int i = 0; i < kPer; ++i) {  // d0 is a multiple of kOwn
-                    const float y = __int_as_float(shfl_i(__float_as_int(po[i % kOwn]), (d0 + i) / kOwn));
-                    r[i] = pm == p ? y : r[i];
-                }
-            }
-        }
+        const bool mend = ballot(nan && pp.live && total == total) != 0;
         if (pp.live && dest) {
 #pragma unroll
             for (int i = 0; i < kPer; i += 4)
@@ -399,6 +380,37 @@ struct Stream {
             if (a.lse && d0 == 0)
                 a.lse[(int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head] =
                     (top + __builtin_amdgcn_logf(total)) * kLn2;
+        }
+        if (mend) {
+            __threadfence_block();  // what this wave wrote is read back
+            mend_pairs(launch_args(), w, wave, keys, t0 * kStreamKeys, t1 * kStreamKeys, total, dest);
+        }
+    }
+
+    // The wave's pairs of the join over places [k0, k1) (see mend_pair); sums: that of
+    // its i-th pair in lanes 16 i on.
+    static __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, TileWork w, int wave, int keys, int k0,
+                                                                int k1, float sums, float *dest) {
+        constexpr int kMine = kAttnTile / kStreamWaves;
+        const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
+        const int limit = !SPARSE || !a.ctx_lens ? a.cap : visible(a, w.row0), req = max(w.req, 0);
+        k1 = min(k1, keys);
+        const FirstPlaces<D> f = first_places<DT, D, SPARSE>(a, req, w.hk, idx, limit, k0, k1);
+        for (int i = 0; i < kMine; ++i) {
+            const int p = wave * kMine + i;
+            const Pair x = pair_of(a, w, p);
+            const float sum = readlane_f(sums, kWave / kMine * i);
+            if (!x.live || sum != sum) continue;
+            PairPlace at = {static_cast<const uint16_t *>(a.q) + x.row * a.q_row + x.head * a.q_head,
+                            static_cast<typename Half<DT>::T *>(a.out) + x.row * a.o_row + x.head * a.o_head,
+                            a.lse ? a.lse + (int64_t)x.row * (a.num_kv_heads * a.group) + x.head : nullptr, nullptr,
+                            nullptr, nullptr};
+            if (dest) {
+                at.state = dest + p * D;
+                at.top = dest + kAttnTile * D + p;
+                at.total = dest + kAttnTile * (D + 1) + p;
+            }
+            mend_pair<DT, D, SPARSE>(a, req, w.hk, idx, limit, k0, SPARSE ? k1 : min(k1, visible(a, x.row)), f, false, at);
         }
     }
 };

@@ -38,32 +38,29 @@ static_assert(kTilePairs == kAttnTile * kTileWaves, "32 pairs to a wave");
 template <int D>
 constexpr int kTilePart = kTilePairs * (D + 2);
 
-// The wave's pairs, each over its own visible keys of [k0, k1) (see own_range).
+// The wave's pairs over keys [k0, k1), mended or done anew (see mend_pair); sums: that
+// of pair p in lane p.
 template <int DT, int D>
-__device__ __attribute__((noinline)) void own_pairs(const AttnArgs &a, int req, int row0, int rows, int wave, int hk,
-                                                    int k0, int k1, float *dest) {
-    typedef typename Half<DT>::T T;
-    const int lane = lane_id();
+__device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, int req, int row0, int rows, int wave, int hk,
+                                                     int k0, int k1, int most, bool anew, float sums, float *dest) {
+    FirstPlaces<D> f;
+    if (!anew) f = first_places<DT, D, false>(a, req, hk, nullptr, 0, k0, min(k1, most));
     for (int p = 0; p < kAttnTile; ++p) {
         const int m = wave * kAttnTile + p, r = m / a.group;
         if (r >= rows) break;
+        const float sum = readlane_f(sums, p);
+        if (!anew && sum != sum) continue;
         const int row = row0 + r, head = hk * a.group + (m - r * a.group);
-        float top, total, o[D / 64];
-        own_range<DT, D, false>(a, req, static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head, hk,
-                                nullptr, 0, k0, min(k1, min(max(a.ctx_lens[row], 0), a.cap)), top, total, o);
+        PairPlace at = {static_cast<const uint16_t *>(a.q) + row * a.q_row + head * a.q_head,
+                        static_cast<typename Half<DT>::T *>(a.out) + row * a.o_row + head * a.o_head,
+                        a.lse ? a.lse + (int64_t)row * (a.num_kv_heads * a.group) + head : nullptr, nullptr, nullptr,
+                        nullptr};
         if (dest) {
-            for (int i = 0; i < D / 64; ++i) dest[m * D + lane * (D / 64) + i] = o[i];
-            if (lane == 0) {
-                dest[kTilePairs * D + m] = top;
-                dest[kTilePairs * (D + 1) + m] = total;
-            }
-            continue;
+            at.state = dest + m * D;
+            at.top = dest + kTilePairs * D + m;
+            at.total = dest + kTilePairs * (D + 1) + m;
         }
-        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-        T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
-        for (int i = 0; i < D / 64; ++i) out[lane * (D / 64) + i] = (T)(o[i] * inv);
-        if (a.lse && lane == 0)
-            a.lse[(int64_t)row * (a.num_kv_heads * a.group) + head] = (top + __builtin_amdgcn_logf(total)) * kLn2;
+        mend_pair<DT, D, false>(a, req, hk, nullptr, 0, k0, min(k1, visible(a, row)), f, anew, at);
     }
 }
 
@@ -333,49 +330,52 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     }
     total = xor32_sum(total);
 
-    // The wave's pairs are done again, each over its own keys, where the tile met a
-    // table entry outside the pool, or where a NaN can come from a zero weight times a
-    // value that is not finite (a pair whose own scores are NaN has a NaN sum).
+    // Where the tile met a table entry outside the pool the wave's pairs are done anew,
+    // each over its own keys; a NaN output whose own sum is a number is mended (a pair
+    // whose own scores are NaN has a NaN sum).
     if (ballot(met_bad) && lane == 0) sh.any_bad = 1;
     __syncthreads();
+    const bool anew = sh.any_bad != 0;
     bool nan = false;
 #pragma unroll
     for (int c = 0; c < D / 32; ++c)
 #pragma unroll
         for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
-    if (sh.any_bad != 0 || ballot(nan && live && total == total)) {
-        own_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, dest);
-        return;
-    }
-    if (!live) return;
-    if (dest) {
+    const bool mend = ballot(nan && live && total == total) != 0;
+    if (live && !anew) {
+        const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+        typedef typename Half<DT>::T T;
+        typedef T V4 __attribute__((ext_vector_type(4)));
+        T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4 *>(dest + m * D + out_element<D>(c, 4 * g, lane)) =
-                    f32x4{o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
+            for (int g = 0; g < 4; ++g) {
+                const int at = out_element<D>(c, 4 * g, lane);
+                const f32x4 v = {o[c][4 * g], o[c][4 * g + 1], o[c][4 * g + 2], o[c][4 * g + 3]};
+                if (dest) {
+                    *reinterpret_cast<f32x4 *>(dest + m * D + at) = v;
+                    continue;
+                }
+                V4 x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = (T)(v[j] * inv);
+                *reinterpret_cast<V4 *>(out + at) = x;
+            }
         if (lane < kAttnTile) {
-            dest[kTilePairs * D + m] = ref;
-            dest[kTilePairs * (D + 1) + m] = total;
+            if (dest) {
+                dest[kTilePairs * D + m] = ref;
+                dest[kTilePairs * (D + 1) + m] = total;
+            } else if (a.lse) {
+                a.lse[(int64_t)row * (a.num_kv_heads * a.group) + head] = (ref + __builtin_amdgcn_logf(total)) * kLn2;
+            }
         }
-        return;
     }
-    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
-    typedef typename Half<DT>::T T;
-    typedef T V4 __attribute__((ext_vector_type(4)));
-    T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
-#pragma unroll
-    for (int c = 0; c < D / 32; ++c)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-            V4 v;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = (T)(o[c][4 * g + j] * inv);
-            *reinterpret_cast<V4 *>(out + out_element<D>(c, 4 * g, lane)) = v;
-        }
-    if (a.lse && lane < kAttnTile)
-        a.lse[(int64_t)row * (a.num_kv_heads * a.group) + head] = (ref + __builtin_amdgcn_logf(total)) * kLn2;
+    if (anew || mend) {
+        __threadfence_block();  // what this wave wrote is read back
+        mend_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, wave_most,
+                          anew, total, dest);
+    }
 }
 
 // one workgroup per tile

@@ -122,6 +122,9 @@ def check_values(out, lse, q, k, v, counts, dtype):
     """Against the 64-bit result where that is finite; infinities and NaN are equal."""
     k, v = (x.to(DT[dtype]).double().numpy() for x in (k, v))
     for r, c in enumerate(counts):
+        if c == 0:
+            assert np.all(out[r] == 0) and np.all(lse[r] == -np.inf), r
+            continue
         o, l, spread, size = ref.attend(q[r].double().numpy(), k[:c, 0], v[:c, 0], q.shape[2] ** -0.5)
         finite = np.isfinite(o)
         to, tl = ref.bounds(np.where(finite, o, 0), l, np.where(finite, spread, 0), size, c, q.shape[2],
@@ -166,6 +169,28 @@ def test_infinity_of_a_small_weight(kernel, dtype):
     out, lse = attend_all(kernel, q.cuda(), kc, vc, table, [n] * rows)
     assert np.all(out[:, :, 9] == np.inf)
     check_values(out, lse, q, k, v, [n] * rows, dtype)
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("dtype,seed", [("bf16", 1), ("fp16", 2), ("bf16", 3)])
+def test_values_not_finite_anywhere(kernel, dtype, seed):
+    """NaN and infinities of both signs at a tenth of the tokens, one element each, and
+    rows of different counts: every element of every row is what its own tokens make
+    it."""
+    rows, group = KERNELS[kernel]
+    rows = max(rows, 3)
+    n, d = 900, 64
+    rng = np.random.default_rng(seed)
+    g = torch.Generator().manual_seed(seed)
+    k, v = torch.randn(n, 1, d, generator=g), torch.randn(n, 1, d, generator=g)
+    at = rng.choice(n, n // 10, replace=False)
+    v[at, 0, rng.integers(0, d, len(at))] = torch.from_numpy(rng.choice([np.nan, np.inf, -np.inf], len(at))).float()
+    q = torch.randn(rows, group, d, generator=g).to(DT[dtype])
+    counts = rng.integers(0, n + 1, rows)
+    counts[:3] = n, 1, 40
+    kc, vc, table = device_cache(k, v, dtype)
+    with np.errstate(invalid="ignore"):
+        check_values(*attend_all(kernel, q.cuda(), kc, vc, table, counts), q, k, v, counts, dtype)
 
 
 # ---------------------------------------------------------------------------
