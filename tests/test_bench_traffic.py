@@ -124,3 +124,14 @@ def test_write_traffic_counts_only_the_fused_call(tmp_path, monkeypatch):
     dirs2 = [str(tmp_path / d) for d in ("f2", "w2", "cf", "cw")]
     bench.write_traffic("fp8_paged", "topk", dirs2, 1024)
     assert json.load(open(tmp_path / "traffic.json"))["fp8_paged:topk"]["fetch_bytes"] == 16 * 1024 * 2
+
+
+def test_committed_counters_belong_to_the_committed_kernels():
+    """Every entry of profiles/traffic.json was taken on the sources as they are: the
+    bench reports its bytes, and not that there are none."""
+    with open(bench.TRAFFIC_FILE) as f:
+        entries = json.load(f)
+    assert entries
+    for key, e in entries.items():
+        kernels = [k for k in bench.KERNEL_FILES if (k == "topk") == key.endswith(":topk")]
+        assert e["source_hash"] in [bench.source_hash(k) for k in kernels], key
