@@ -476,7 +476,8 @@ typedef struct qsa_attn_shape {
  * A table entry outside [0, num_blocks) is not dereferenced: rows that see its
  * columns are NaN.  Weights are rounded to dtype before the second product (fp16:
  * those below 2^-27 of a row's largest to multiples of 2^-37 of it, or finer); sums,
- * maxima and lse are 32-bit.
+ * maxima and lse are 32-bit.  Weighted values are summed before the division: with bf16
+ * the magnitudes of a row's values in one element have to add up to less than 2^119.
  *
  * Compiled set: Hq / Hk <= 128, Hq <= 8192, B <= 1024.  Range: max_blocks * B <=
  * 2^30, R and num_reqs <= 2^21, and (R * Hq / (256 Hk) + num_reqs) * Hk tiles <= 2^22.

@@ -157,8 +157,15 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
         return p;
     }
     // With at most four rows per request on average (a verify step), what one long
-    // request adds to a batch streamed whole stays below the others' part.  (64 requests
-    // of 4 rows, 8,000 to 16,000 tokens: 279 us streamed, 323 by the tile kernel.)
+    // request adds to a batch streamed whole stays below the others' part.  us streamed
+    // / by the tile kernel, 4 kv heads of 8 heads at D = 128: 64 requests of 4 rows,
+    // 8,000 to 16,000 tokens 279 / 323; 63 requests of one row and one of 32, 64, 192,
+    // 8,000 tokens each 209 / 200, 221 / 324, 280 / 313; 199 and one of 100, 300, 600,
+    // 4,000 tokens 315 / 363, 353 / 355, 393 / 356; 7 and one of 8, 24, 8,000 tokens
+    // 34 / 32, 44 / 39.  2 of 16 at D = 64: 63 and one of 32, 192, 8,000 tokens 58 / 121,
+    // 83 / 122; 64 of 4 rows 89 / 72.  1 of 32: 63 and one of 96, 8,000 tokens 78 / 77.
+    // The lengths, which decide it, are on the device: over 130 such batches the choice
+    // costs at most 27% (8 requests of 4 rows, 1 of 32: 21 / 27).
     const int64_t few = group >= kStreamPairs ? 1 : kStreamPairs / group;
     p.stream = R <= few * n && (R <= 4 * n || R * group <= kSmallPairs);
     const int64_t T = p.tile_rows = p.stream ? qsa::kAttnTile / p.sub_heads : qsa::kTilePairs / group;

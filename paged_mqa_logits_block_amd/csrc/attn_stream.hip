@@ -25,14 +25,16 @@
 // slots that have no rows).  With many tiles each gets a workgroup.
 //
 // Measured (kernel traces): a verify step of 9 requests with 4 rows, 16,000 to 65,600
-// tokens, 539 MB of cache at D = 128, 32 over 4 heads, bf16: 107 us and 6 for the
-// join, 4.8 TB/s against the 4.9 TB/s (read and written) of a large copy; 262 + 26
-// us with one wave per 32 keys' split and arguments in scratch, 198 + 10 without the
-// scratch.  One row over 4,000 tokens: 9 + 4 us, latency: about six dependent loads,
-// of which the launch, the join and the table make half.  Selected tokens of 36 rows
-// (8,192 each, 605 MB): 105 + 5 us, 5.5 TB/s.  Of 1,000 rows (2,048 each): 265 us
-// for 4.2 GB through the L2s (15.8 TB/s; 78% of the requests hit), 299 with 32-pair
-// tiles of which these heads fill 8 (NARROW below): what bounds it is the gather.
+// tokens, 539 MB of cache at D = 128, 32 over 4 heads, bf16: 109 us and 5 for the
+// join, 4.8 TB/s of both, where a kernel that only reads as many bytes in order takes
+// 87 (6.2 TB/s); 262 + 26 us with one wave per 32 keys' split and arguments in scratch,
+// 198 + 10 without the scratch.  One row over 4,000 tokens: 10 + 4 us, latency: about
+// six dependent loads, of which the launch, the join and the table make half.  Selected
+// tokens of 36 rows (8,192 each, 605 MB): 106 + 5 us, 5.5 TB/s.  Of 1,000 rows (2,048
+// each): 267 us for 4.2 GB through the L2s (15.7 TB/s; 78% of the requests hit), 299
+// with 32-pair tiles of which these heads fill 8 (NARROW below).  A plain kernel that
+// loads the same rows and multiplies nothing takes 230 us (18.2 TB/s): what bounds it
+// is the gather.
 #include "attn_device.h"
 
 namespace qsa {

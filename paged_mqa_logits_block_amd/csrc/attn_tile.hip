@@ -17,11 +17,12 @@
 // were last read in multiply s - 1, which all waves have left by then.
 //
 // Measured: 2,048 rows at the end of 16,384 tokens, 32 over 4 heads, D = 128, bf16:
-// 460 us, 1,120 TFLOP/s, 92% of the rate of a library product of 8192^3 on the same
-// card (1,214); up to 516 us on other cards.  On the way there: 931 us with the arguments in scratch, 731 without,
-// 674 with a lagging softmax reference, 569 with the turns and scalar table entries,
-// 552 with heads dealt to the XCDs.  The clock drops from 2.3 to 1.9 GHz while the
-// matrix cores work, so the card's power is part of the bound.
+// 471 us, 1,095 TFLOP/s, where a library product of 8192^3 reaches 1,390 on the same
+// card (459 to 516 us by card; fp16 takes 8% more).  On the way there: 931 us with the
+// arguments in scratch, 731 without, 674 with a lagging softmax reference, 569 with the
+// turns and scalar table entries, 552 with heads dealt to the XCDs.  The clock drops
+// from 2.3 to 1.9 GHz while the matrix cores work, so the card's power is part of the
+// bound.
 
 #include "attn_device.h"
 
