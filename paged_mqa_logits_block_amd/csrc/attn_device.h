@@ -501,9 +501,10 @@ __device__ __forceinline__ const AttnArgs &launch_args() {
 // fill up a step (the last one once more) and of those whose weight is below what the
 // caches' type holds; where such a value is infinite or NaN, so is the product.  What the
 // element is follows from the values that the pair itself sees: NaN, or infinities of
-// both signs, make it NaN, infinities of one sign infinite, and otherwise it is finite
-// and the pair is done again over its own keys.  The first place of each of the three
-// kinds is found once per wave, for all its pairs.  (Doing every such pair again, one NaN
+// both signs, make it NaN, infinities of one sign infinite, and otherwise the NaN is
+// another row's and the pair is done again over its own keys (selected tokens: there
+// are no other rows).  The first place of each of the three kinds is found once per
+// wave, for all its pairs.  (Doing every such pair again, one NaN
 // that all rows see took 168 ms for 2,048 rows at 16,384 tokens.)
 //
 // Places are tokens, or with SPARSE the entries of `idx` times `ratio`; a lane has the
@@ -574,18 +575,18 @@ __device__ __forceinline__ FirstPlaces<D> first_places(const AttnArgs &a, int re
     return f;
 }
 
-// One pair's softmax state over its own places [k0, k1), by one wave with plain loads
-// and 32-bit weights: no other key's value is touched.
-template <int DT, int D, bool SPARSE>
-__device__ __forceinline__ void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, const int32_t *idx,
-                                          int limit, int k0, int k1, float &m, float &l, float (&o)[D / 64]) {
+// One pair's softmax state over its own keys [k0, k1), by one wave with plain loads and
+// 32-bit weights: no other key's value is touched.
+template <int DT, int D>
+__device__ __forceinline__ void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, int k0, int k1, float &m,
+                                          float &l, float (&o)[D / 64]) {
     m = kNegInf;
     l = 0.0f;
     for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
     for (int base = k0; base < k1; base += kWave) {
         int64_t off = 0;
         bool bad = false;
-        const bool seen = base + lane_id() < k1 && place_offset<SPARSE>(a, req, hk, idx, limit, base + lane_id(), off, bad);
+        const bool seen = base + lane_id() < k1 && place_offset<false>(a, req, hk, nullptr, 0, base + lane_id(), off, bad);
         float s = kNegInf;
         if (seen) {
             const i32x4 *k = reinterpret_cast<const i32x4 *>(a.kcache + off);
@@ -627,36 +628,47 @@ struct PairPlace {
     float *state, *top, *total;   // all null, or the state's outputs, reference and sum
 };
 
-// Mends what the wave has written of one pair, or does the pair anew (`anew`).
+// Mends what the wave has written of one pair over its places before k1, or does the
+// pair anew (`anew`).
 template <int DT, int D, bool SPARSE>
-__device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit, int k0, int k1,
-                                          const FirstPlaces<D> &f, bool anew, const PairPlace &p) {
+__device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, int k0, int k1, const FirstPlaces<D> &f,
+                                          bool anew, const PairPlace &p) {
     typedef typename Half<DT>::T T;
     const int at = lane_id() * (D / 64);
     T *out = static_cast<T *>(p.out) + at;
-    float o[D / 64], top, total, inv = 1.0f;
-    bool finite = anew, write = false;
-    if (!anew) {
+    float o[D / 64], inv = 1.0f;
+    bool others = anew, write = false;
+    const auto settle = [&]() {  // NaN elements by the values that the pair sees
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            o[i] = p.state ? p.state[at + i] : (float)out[i];
-            if (o[i] == o[i]) continue;
             const bool inf = f.inf[i] < k1, minus = f.minus[i] < k1;
-            if (f.nan[i] < k1 || (inf && minus)) continue;
-            finite |= !inf && !minus;
-            write = true;
-            o[i] = inf ? -kNegInf : kNegInf;
+            if (o[i] == o[i] || f.nan[i] < k1 || (inf && minus)) continue;
+            if (inf || minus) {
+                o[i] = inf ? -kNegInf : kNegInf;
+                write = true;
+            } else {
+                others = true;
+            }
         }
+    };
+    if (!anew) {
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) o[i] = p.state ? p.state[at + i] : (float)out[i];
+        settle();
     }
-    if (ballot(finite)) {
-        own_range<DT, D, SPARSE>(a, req, p.q, hk, idx, limit, k0, k1, top, total, o);
-        write = true;
-        if (lane_id() == 0 && p.state) {
-            *p.top = top;
-            *p.total = total;
+    if constexpr (!SPARSE) {
+        if (ballot(others)) {
+            float top, total;
+            own_range<DT, D>(a, req, p.q, hk, k0, k1, top, total, o);
+            if (!anew) settle();
+            write = true;
+            if (lane_id() == 0 && p.state) {
+                *p.top = top;
+                *p.total = total;
+            }
+            if (lane_id() == 0 && !p.state && p.lse) *p.lse = (top + __builtin_amdgcn_logf(total)) * kLn2;
+            if (!p.state) inv = total == 0.0f ? 0.0f : 1.0f / total;
         }
-        if (lane_id() == 0 && !p.state && p.lse) *p.lse = (top + __builtin_amdgcn_logf(total)) * kLn2;
-        if (!p.state) inv = total == 0.0f ? 0.0f : 1.0f / total;
     }
     if (!write) return;
 #pragma unroll

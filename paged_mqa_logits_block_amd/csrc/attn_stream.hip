@@ -412,7 +412,7 @@ struct Stream {
                 at.top = dest + kAttnTile * D + p;
                 at.total = dest + kAttnTile * (D + 1) + p;
             }
-            mend_pair<DT, D, SPARSE>(a, req, w.hk, idx, limit, k0, SPARSE ? k1 : min(k1, visible(a, x.row)), f, false, at);
+            mend_pair<DT, D, SPARSE>(a, req, w.hk, k0, SPARSE ? k1 : min(k1, visible(a, x.row)), f, false, at);
         }
     }
 };

@@ -61,7 +61,7 @@ __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, int req,
             at.top = dest + kTilePairs * D + m;
             at.total = dest + kTilePairs * (D + 1) + m;
         }
-        mend_pair<DT, D, false>(a, req, hk, nullptr, 0, k0, min(k1, visible(a, row)), f, anew, at);
+        mend_pair<DT, D, false>(a, req, hk, k0, min(k1, visible(a, row)), f, anew, at);
     }
 }
 
