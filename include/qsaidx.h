@@ -312,8 +312,10 @@ QSA_API qsa_status qsa_expand(const int32_t *idx, int32_t num_rows, int32_t k, i
  *   qsa_plan_batch        request lengths -> block table, slot maps, visible counts
  *   qsa_write_kv          new keys and values into the paged caches
  *   qsa_write_keys        new index keys into the scorer's cache
+ *   qsa_norm_rope         head norms and rotary positions, keys and values to the caches
  *   qsa_paged_attention   attention over all visible tokens
  *   qsa_sparse_attention  attention over the tokens of the selected columns
+ *   qsa_verify_drafts     drafted tokens against the target's probabilities
  */
 
 typedef struct qsa_plan_shape {
@@ -430,6 +432,74 @@ QSA_API qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *
 QSA_API qsa_status qsa_write_keys_check(const void *keys, const int64_t *slots, const void *kcache,
                                         const float *kscale, const qsa_keys_shape *shape);
 
+typedef enum qsa_rope_layout {
+    QSA_ROPE_HALF = 0,         /* pair i: elements i and i + rot_dim / 2           */
+    QSA_ROPE_INTERLEAVED = 1   /* pair i: elements 2 i and 2 i + 1                 */
+} qsa_rope_layout;
+
+typedef struct qsa_rope_shape {
+    int32_t num_rows;          /* R rows                                           */
+    int32_t num_heads;         /* Hq query heads, 0: no queries                    */
+    int32_t num_kv_heads;      /* Hk key heads, 0: no keys                         */
+    int32_t head_dim;          /* D: 64 or 128                                     */
+    int32_t rot_dim;           /* rotated elements of a head, a multiple of 16     */
+    int32_t rot_offset;        /* the first of them, a multiple of 8               */
+    int32_t layout;            /* qsa_rope_layout                                  */
+    int32_t dtype;             /* QSA_BF16 or QSA_FP16: all heads and the caches   */
+    int32_t position_offset;   /* added to positions                               */
+    int32_t block_size;        /* B tokens per block (with caches)                 */
+    float eps;                 /* of the norms, >= 0                               */
+    float factor;              /* on cosines and sines, 1 where nothing is scaled  */
+    int64_t num_blocks;        /* (with caches)                                    */
+    /* strides in elements (the last dimension is contiguous)                    */
+    int64_t q_row_stride, q_head_stride, k_row_stride, k_head_stride, v_row_stride, v_head_stride;
+    int64_t q_out_row_stride, q_out_head_stride, k_out_row_stride, k_out_head_stride;
+    int64_t kv_block_stride, kv_slot_stride, kv_head_stride;
+} qsa_rope_shape;
+
+/*
+ * qsa_norm_rope -- query and key heads normed and rotated by their positions, keys and
+ * values into the paged caches, in one pass:
+ *
+ *     y = x w / sqrt(mean(x^2) + eps)          over a head's D elements, where it has a weight
+ *     (a, b) -> factor (a cos t - b sin t, b cos t + a sin t),   t = position inv_freq[i]
+ *
+ * for the pairs i of elements [rot_offset, rot_offset + rot_dim), the others unchanged.
+ * position = positions[r] + position_offset: qsa_plan_batch's ctx_lens with an offset of
+ * -1 are the rows' positions.  A row whose position is negative (one behind the last
+ * request's) writes nothing.
+ *
+ *   q, q_out   [R][Hq][D]; both NULL with Hq = 0.  q_out may be q.
+ *   k, k_out   [R][Hk][D]; both NULL with Hk = 0.  k_out may be k, or NULL where kcache
+ *              takes the keys.
+ *   v          [R][Hk][D], stored as they are; with vcache.
+ *   q_weight, k_weight [D] f32, or NULL: no norm.
+ *   positions  [R] int32.
+ *   inv_freq   [rot_dim / 2] f64, radians per position (any scaling for long contexts is in
+ *              them and in factor); NULL with rot_dim = 0.
+ *   slots      [R] int64 with the caches, as qsa_write_kv's (rows outside
+ *              [0, num_blocks * B) write q_out and k_out only).
+ *   kcache, vcache  NULL, or k's and v's; vcache only with kcache.  Both have the same
+ *              strides.
+ *
+ * Norms, angles' reduction and products are 32-bit or more with one rounding at the end;
+ * the angle itself is a 64-bit product.  A head's sum of squares has to stay below 2^127 (heads
+ * of larger values come out 0 or NaN).  An infinity or a NaN spoils its own head only.
+ *
+ * Device precondition: the slots written are distinct.  Outputs must not overlap inputs
+ * but for q_out = q and k_out = k with their strides.  Compiled set: D in {64, 128};
+ * Hq <= 8192, Hk <= 1024.  Range: R <= 2^27.  Alignment: q, k, v, their outputs and the
+ * caches 16 bytes, strides multiples of 8 elements.
+ */
+QSA_API qsa_status qsa_norm_rope(const void *q, const void *k, const void *v, const float *q_weight,
+                                 const float *k_weight, const int32_t *positions, const double *inv_freq,
+                                 const int64_t *slots, void *q_out, void *k_out, void *kcache, void *vcache,
+                                 const qsa_rope_shape *shape, void *stream);
+QSA_API qsa_status qsa_norm_rope_check(const void *q, const void *k, const void *v, const int32_t *positions,
+                                       const double *inv_freq, const int64_t *slots, const void *q_out,
+                                       const void *k_out, const void *kcache, const void *vcache,
+                                       const qsa_rope_shape *shape);
+
 typedef struct qsa_attn_shape {
     int32_t num_rows;          /* R query rows of q and out                        */
     int32_t num_heads;         /* Hq query heads                                   */
@@ -526,6 +596,61 @@ QSA_API qsa_status qsa_sparse_attention_check(const void *q, const void *kcache,
                                               const qsa_attn_shape *shape, const void *workspace,
                                               int64_t workspace_bytes);
 QSA_API int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *shape, int32_t k, int32_t ratio);
+
+typedef struct qsa_verify_shape {
+    int32_t num_rows;          /* R rows of probs                                  */
+    int32_t num_reqs;          /* n requests                                       */
+    int32_t vocab;             /* V                                                */
+    int32_t max_tokens;        /* columns of out_tokens, >= 1                      */
+    int64_t prob_stride;       /* floats between rows of probs, >= V               */
+    int64_t draft_stride;      /* the same of draft_probs                          */
+} qsa_verify_shape;
+
+/*
+ * qsa_verify_drafts -- the end of a verify step: which drafted tokens are kept, and the
+ * token after them, so that the tokens are distributed as the target's.
+ *
+ * Request i's rows are [q_starts[i], q_starts[i + 1]) (values are clamped to [0, R]); of
+ * more than max_tokens rows only the first max_tokens count.  Row s + j's input is
+ * tokens[s + j]: the last token so far at j = 0, then the drafts, so that draft j is
+ * x = tokens[s + j + 1] and p = probs[s + j] is the target's distribution for its place.
+ *
+ *     draft j is kept      iff all before it are and uniforms[s + j] * q(x) < p(x)
+ *     the token after them ~ max(p - q, 0) of the first row whose draft is not kept, or
+ *                            p of the last row where all are
+ *
+ * with q = draft_probs[s + j], or the certainty of x without draft_probs.  The token is
+ * the lowest index whose cumulative weight passes sample_uniforms[i] times the weights'
+ * sum (the last index with weight where none does): sums and products in 64 bits, a row's
+ * own sum need not be 1.  Entries that are not positive numbers have no weight.  Where
+ * p is nowhere above q the token is taken from p, and it is -1 where p has no weight either.
+ * A draft outside [0, V) is not kept.
+ *
+ *   probs, draft_probs [R][V] f32 (draft_probs or NULL; a request's last row of it is not
+ *                   read).  Rows that do not decide anything are not read.
+ *   tokens          [R] int32.
+ *   uniforms        [R] f32 in [0, 1), one per draft (a request's last is not used).
+ *   sample_uniforms [n] f32 in [0, 1).
+ *   out_tokens      [n][max_tokens] int32: the drafts kept, the token after them, then -1.
+ *   num_tokens      [n] int32: drafts kept + 1, what qsa_plan_batch's past_lens grow by; 0 for
+ *                   a request without rows.
+ *   workspace       qsa_verify_drafts_workspace_bytes(shape) bytes (0: none is used), 16-byte
+ *                   aligned, or NULL: then few requests are not spread over the chip (the
+ *                   tokens do not change).  No initialisation; calls that share it must be
+ *                   ordered.
+ *
+ * Compiled set: V <= 2^20.  Range: R and n <= 2^24, n * max_tokens <= 2^30.
+ */
+QSA_API qsa_status qsa_verify_drafts(const float *probs, const float *draft_probs, const int32_t *tokens,
+                                     const int32_t *q_starts, const float *uniforms, const float *sample_uniforms,
+                                     int32_t *out_tokens, int32_t *num_tokens, const qsa_verify_shape *shape,
+                                     void *workspace, int64_t workspace_bytes, void *stream);
+QSA_API qsa_status qsa_verify_drafts_check(const float *probs, const float *draft_probs, const int32_t *tokens,
+                                           const int32_t *q_starts, const float *uniforms,
+                                           const float *sample_uniforms, const int32_t *out_tokens,
+                                           const int32_t *num_tokens, const qsa_verify_shape *shape,
+                                           const void *workspace, int64_t workspace_bytes);
+QSA_API int64_t qsa_verify_drafts_workspace_bytes(const qsa_verify_shape *shape);
 
 /* Message for the calling thread's last non-OK status ("" if none). Owned by the
  * library; valid until the thread's next call. */

@@ -1,6 +1,7 @@
 """Python binding of libqsaidx: paged MQA-logits scoring and per-row top-k on
 MI355X (gfx950), and the calls around them in a serving step (batch plan, cache
-writes, attention; in ``serving.py``).
+writes, head norms with rotary positions, attention, verification of drafts; in
+``serving.py``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 kernels behind the C ABI declared in ``include/qsaidx.h``.  Tensors are torch
@@ -31,7 +32,8 @@ EXPORTED = ("qsa_paged_logits", "qsa_paged_logits_timed", "qsa_paged_logits_chec
             "qsa_expand", "qsa_plan_batch", "qsa_plan_batch_check", "qsa_write_kv", "qsa_write_kv_check",
             "qsa_write_keys", "qsa_write_keys_check", "qsa_paged_attention", "qsa_paged_attention_check",
             "qsa_paged_attention_workspace_bytes", "qsa_sparse_attention", "qsa_sparse_attention_check",
-            "qsa_sparse_attention_workspace_bytes", "qsa_last_error", "qsa_version")
+            "qsa_sparse_attention_workspace_bytes", "qsa_norm_rope", "qsa_norm_rope_check", "qsa_verify_drafts",
+            "qsa_verify_drafts_check", "qsa_verify_drafts_workspace_bytes", "qsa_last_error", "qsa_version")
 
 
 class QsaError(RuntimeError):
@@ -448,7 +450,9 @@ def paged_logits_topk(q, kcache, block_table, ctx_lens, row_to_req, *, k: int, w
     return call()
 
 
-from .serving import (AttnShape, BatchPlan, KeysShape, KvShape, PlanShape, PreparedPagedAttention,  # noqa: E402
-                      PreparedPlanBatch, PreparedSparseAttention, PreparedWriteKeys, PreparedWriteKv,
-                      make_attn_shape, paged_attention, paged_attention_workspace_bytes, plan_batch,
-                      sparse_attention, sparse_attention_workspace_bytes, write_keys, write_kv)
+from .serving import (ROPE_HALF, ROPE_INTERLEAVED, AttnShape, BatchPlan, KeysShape, KvShape, PlanShape,  # noqa: E402
+                      PreparedNormRope, PreparedPagedAttention, PreparedPlanBatch, PreparedSparseAttention,
+                      PreparedVerifyDrafts, PreparedWriteKeys, PreparedWriteKv, RopeShape, VerifyShape, make_attn_shape,
+                      norm_rope, paged_attention, paged_attention_workspace_bytes, plan_batch, rope_frequencies,
+                      sparse_attention, sparse_attention_workspace_bytes, verify_drafts, verify_drafts_workspace_bytes,
+                      write_keys, write_kv)

@@ -12,7 +12,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libqsaidx.so")
 SOURCES = ["api.hip", "logits.hip", "logits_decode.hip", "logits_looped.hip", "logits_mtp.hip",
            "logits_prefill.hip", "topk.hip", "expand.hip", "api_serving.hip", "plan.hip", "write.hip",
-           "attn_stream.hip", "attn_tile.hip"]
+           "attn_stream.hip", "attn_tile.hip", "rope.hip", "verify.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

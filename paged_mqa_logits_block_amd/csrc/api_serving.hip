@@ -1,11 +1,15 @@
-// C-ABI entry points around the scorer: the batch plan, the cache writes, and
-// attention over the paged cache (all visible tokens, or the selected ones).
+// C-ABI entry points around the scorer: the batch plan, the cache writes, head norms
+// with rotary positions, attention over the paged cache (all visible tokens, or the
+// selected ones), and the verification of drafted tokens.
 // As in api.hip, validation reads host scalars only and every call can be
 // captured.
 #include "api_common.h"
 #include "attn_internal.h"
 #include "qsa_internal.h"
 #include "qsaidx.h"
+#include "step_internal.h"
+
+#include <initializer_list>
 
 namespace {
 
@@ -104,6 +108,113 @@ qsa_status check_write_keys(const void *keys, const int64_t *slots, const void *
         return fail(QSA_E_ALIGN, "keys and kcache must be 16-byte aligned");
     if (s->num_rows > 1 && s->src_stride % 8 != 0)
         return fail(QSA_E_ALIGN, "src_stride must be a multiple of 8 elements");
+    return ok();
+}
+
+bool negative(std::initializer_list<int64_t> strides) {
+    for (const int64_t x : strides)
+        if (x < 0) return true;
+    return false;
+}
+
+qsa_status check_rope(const void *q, const void *k, const void *v, const int32_t *positions, const double *inv_freq,
+                      const int64_t *slots, const void *q_out, const void *k_out, const void *kcache,
+                      const void *vcache, const qsa_rope_shape *s) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0 || s->num_heads < 0 || s->num_kv_heads < 0)
+        return fail(QSA_E_INVALID, "num_rows, num_heads and num_kv_heads must be >= 0");
+    if (s->num_heads == 0 && s->num_kv_heads == 0) return fail(QSA_E_INVALID, "no query and no key heads");
+    if (s->layout != QSA_ROPE_HALF && s->layout != QSA_ROPE_INTERLEAVED)
+        return fail(QSA_E_INVALID, "layout = %d", s->layout);
+    if (!(s->eps >= 0.0f) || s->eps > 1e30f) return fail(QSA_E_INVALID, "eps must be in [0, 1e30]");
+    if (!(s->factor >= -1e30f && s->factor <= 1e30f)) return fail(QSA_E_INVALID, "factor must be in [-1e30, 1e30]");
+    if (s->dtype != QSA_BF16 && s->dtype != QSA_FP16) return fail(QSA_E_DTYPE, "dtype = %d (built: bf16, fp16)", s->dtype);
+    if (s->head_dim != 64 && s->head_dim != 128)
+        return fail(QSA_E_UNSUPPORTED, "head_dim = %d (built: 64, 128)", s->head_dim);
+    if (s->rot_dim < 0 || s->rot_offset < 0 || s->rot_offset > s->head_dim || s->rot_dim > s->head_dim - s->rot_offset)
+        return fail(QSA_E_INVALID, "rot_offset = %d and rot_dim = %d do not lie in head_dim = %d", s->rot_offset,
+                    s->rot_dim, s->head_dim);
+    if (s->rot_dim % 16 != 0 || s->rot_offset % 8 != 0)
+        return fail(QSA_E_UNSUPPORTED, "rot_dim = %d and rot_offset = %d (built: multiples of 16 and of 8)", s->rot_dim,
+                    s->rot_offset);
+    if (s->num_heads > 8192 || s->num_kv_heads > 1024)
+        return fail(QSA_E_UNSUPPORTED, "num_heads = %d, num_kv_heads = %d (built: up to 8192 and 1024)", s->num_heads,
+                    s->num_kv_heads);
+    if (s->num_rows > (1 << 27)) return fail(QSA_E_RANGE, "num_rows = %d > 2^27", s->num_rows);
+    if (negative({s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride, s->v_row_stride,
+                  s->v_head_stride, s->q_out_row_stride, s->q_out_head_stride, s->k_out_row_stride,
+                  s->k_out_head_stride, s->kv_block_stride, s->kv_slot_stride, s->kv_head_stride}))
+        return fail(QSA_E_INVALID, "strides must be >= 0");
+    // what the flags of the call ask for, also where there are no rows
+    if ((s->num_kv_heads == 0 && (kcache || vcache || v || k_out)) || (s->num_heads == 0 && q_out))
+        return fail(QSA_E_INVALID, "outputs of heads that the shape does not have");
+    if (vcache && !kcache) return fail(QSA_E_INVALID, "vcache without kcache");
+    if (!v != !vcache) return fail(QSA_E_INVALID, "v and vcache belong together");
+    if (s->num_rows > 0) {
+        if (!positions || (s->rot_dim > 0 && !inv_freq)) return fail(QSA_E_INVALID, "positions and inv_freq must be non-NULL");
+        if (s->num_heads > 0 && (!q || !q_out)) return fail(QSA_E_INVALID, "q and q_out must be non-NULL");
+        if (s->num_kv_heads > 0 && (!k || (!k_out && !kcache)))
+            return fail(QSA_E_INVALID, "k and one of k_out and kcache must be non-NULL");
+        if (kcache && !slots) return fail(QSA_E_INVALID, "slots must be non-NULL with kcache");
+    }
+    const bool many = s->num_rows > 1;
+    if ((q_out && ((many && s->q_out_row_stride < s->head_dim) || (s->num_heads > 1 && s->q_out_head_stride < s->head_dim))) ||
+        (k_out && ((many && s->k_out_row_stride < s->head_dim) || (s->num_kv_heads > 1 && s->k_out_head_stride < s->head_dim))))
+        return fail(QSA_E_INVALID, "output strides must be at least head_dim");
+    if (kcache) {
+        if (s->block_size < 1 || s->num_blocks < 1) return fail(QSA_E_INVALID, "block_size and num_blocks must be >= 1");
+        if (s->block_size > 1024) return fail(QSA_E_UNSUPPORTED, "block_size = %d (built: 1 to 1024)", s->block_size);
+        if (s->kv_head_stride < (s->num_kv_heads > 1 ? s->head_dim : 0) ||
+            s->kv_slot_stride < (s->block_size > 1 ? s->head_dim : 0) ||
+            s->kv_block_stride < (s->num_blocks > 1 ? s->head_dim : 0))
+            return fail(QSA_E_INVALID, "cache strides must be at least head_dim");
+        if (s->num_blocks > ((int64_t)1 << 50) || s->kv_block_stride > ((int64_t)1 << 50) / s->num_blocks ||
+            s->kv_slot_stride > ((int64_t)1 << 40) || s->kv_head_stride > ((int64_t)1 << 40))
+            return fail(QSA_E_RANGE, "cache too large");
+    }
+    const int64_t most = (int64_t)1 << 30;
+    if (s->q_row_stride > most || s->q_head_stride > most || s->k_row_stride > most || s->k_head_stride > most ||
+        s->v_row_stride > most || s->v_head_stride > most || s->q_out_row_stride > most ||
+        s->q_out_head_stride > most || s->k_out_row_stride > most || s->k_out_head_stride > most)
+        return fail(QSA_E_RANGE, "a stride is too large");
+    if (s->num_rows > 0 && (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) || !aligned16(k_out) ||
+                            !aligned16(kcache) || !aligned16(vcache)))
+        return fail(QSA_E_ALIGN, "q, k, v, q_out, k_out, kcache and vcache must be 16-byte aligned");
+    if (s->num_rows > 0 && ((s->q_row_stride | s->q_head_stride | s->k_row_stride | s->k_head_stride | s->v_row_stride |
+                             s->v_head_stride | s->q_out_row_stride | s->q_out_head_stride | s->k_out_row_stride |
+                             s->k_out_head_stride | s->kv_block_stride | s->kv_slot_stride | s->kv_head_stride) & 7) != 0)
+        return fail(QSA_E_ALIGN, "strides must be multiples of 8 elements");
+    return ok();
+}
+
+qsa_status check_verify_sizes(const qsa_verify_shape *s) {
+    if (!s) return fail(QSA_E_INVALID, "shape is NULL");
+    if (s->num_rows < 0 || s->num_reqs < 0)
+        return fail(QSA_E_INVALID, "num_rows = %d and num_reqs = %d must be >= 0", s->num_rows, s->num_reqs);
+    if (s->vocab < 1 || s->max_tokens < 1) return fail(QSA_E_INVALID, "vocab and max_tokens must be >= 1");
+    if (s->vocab > qsa::kVerifyMaxVocab)
+        return fail(QSA_E_UNSUPPORTED, "vocab = %d (built: up to %d)", s->vocab, qsa::kVerifyMaxVocab);
+    if (s->num_rows > (1 << 24) || s->num_reqs > (1 << 24) || (int64_t)s->num_reqs * s->max_tokens > (1 << 30))
+        return fail(QSA_E_RANGE, "num_rows, num_reqs or num_reqs * max_tokens too large");
+    return ok();
+}
+
+qsa_status check_verify(const float *probs, const float *draft_probs, const int32_t *tokens, const int32_t *q_starts,
+                        const float *uniforms, const float *sample_uniforms, const int32_t *out_tokens,
+                        const int32_t *num_tokens, const qsa_verify_shape *s) {
+    const qsa_status st = check_verify_sizes(s);
+    if (st != QSA_OK) return st;
+    if (s->num_reqs > 0 && (!q_starts || !sample_uniforms || !out_tokens || !num_tokens))
+        return fail(QSA_E_INVALID, "q_starts, sample_uniforms, out_tokens and num_tokens must be non-NULL");
+    if (s->num_reqs > 0 && s->num_rows > 0 && (!probs || !tokens || !uniforms))
+        return fail(QSA_E_INVALID, "probs, tokens and uniforms must be non-NULL");
+    if (s->num_rows > 1 && (s->prob_stride < s->vocab || (draft_probs && s->draft_stride < s->vocab)))
+        return fail(QSA_E_INVALID, "row strides must be at least vocab = %d", s->vocab);
+    if (s->prob_stride > ((int64_t)1 << 36) || s->draft_stride > ((int64_t)1 << 36) || s->prob_stride < 0 ||
+        s->draft_stride < 0)
+        return fail(QSA_E_RANGE, "row strides must be in [0, 2^36]");
+    if (((uintptr_t)probs & 3) != 0 || ((uintptr_t)draft_probs & 3) != 0)
+        return fail(QSA_E_ALIGN, "probs and draft_probs must be 4-byte aligned");
     return ok();
 }
 
@@ -351,6 +462,91 @@ qsa_status qsa_write_keys(const void *keys, const int64_t *slots, void *kcache, 
                             s->num_rows, s->head_dim, s->block_size, s->src_dtype, s->k_dtype, s->kv_layout,
                             s->num_blocks, s->src_stride, block};
     return launched(qsa::launch_write_keys(a, static_cast<hipStream_t>(stream)));
+}
+
+qsa_status qsa_norm_rope_check(const void *q, const void *k, const void *v, const int32_t *positions,
+                               const double *inv_freq, const int64_t *slots, const void *q_out, const void *k_out,
+                               const void *kcache, const void *vcache, const qsa_rope_shape *shape) {
+    return check_rope(q, k, v, positions, inv_freq, slots, q_out, k_out, kcache, vcache, shape);
+}
+
+qsa_status qsa_norm_rope(const void *q, const void *k, const void *v, const float *q_weight, const float *k_weight,
+                         const int32_t *positions, const double *inv_freq, const int64_t *slots, void *q_out,
+                         void *k_out, void *kcache, void *vcache, const qsa_rope_shape *s, void *stream) {
+    qsa_status st = check_rope(q, k, v, positions, inv_freq, slots, q_out, k_out, kcache, vcache, s);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    qsa::NormRopeArgs a = {};
+    a.q = static_cast<const uint16_t *>(q);
+    a.k = static_cast<const uint16_t *>(k);
+    a.v = static_cast<const uint16_t *>(v);
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.positions = positions;
+    a.inv_freq = inv_freq;
+    a.slots = slots;
+    a.q_out = static_cast<uint16_t *>(q_out);
+    a.k_out = static_cast<uint16_t *>(k_out);
+    a.kcache = static_cast<uint16_t *>(kcache);
+    a.vcache = static_cast<uint16_t *>(vcache);
+    a.num_rows = s->num_rows;
+    a.num_heads = s->num_heads;
+    a.num_kv_heads = s->num_kv_heads;
+    a.head_dim = s->head_dim;
+    a.rot_dim = s->rot_dim;
+    a.rot_offset = s->rot_offset;
+    a.layout = s->layout;
+    a.dtype = s->dtype;
+    a.position_offset = s->position_offset;
+    a.block_size = s->block_size;
+    a.eps = s->eps;
+    a.factor = s->factor;
+    a.num_blocks = s->num_blocks;
+    a.q_row = s->q_row_stride;
+    a.q_head = s->q_head_stride;
+    a.k_row = s->k_row_stride;
+    a.k_head = s->k_head_stride;
+    a.v_row = s->v_row_stride;
+    a.v_head = s->v_head_stride;
+    a.qo_row = s->q_out_row_stride;
+    a.qo_head = s->q_out_head_stride;
+    a.ko_row = s->k_out_row_stride;
+    a.ko_head = s->k_out_head_stride;
+    a.kv_block = s->kv_block_stride;
+    a.kv_slot = s->kv_slot_stride;
+    a.kv_head = s->kv_head_stride;
+    a.heads = s->num_heads + s->num_kv_heads * (v ? 2 : 1);
+    return launched(qsa::launch_norm_rope(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qsa_verify_drafts_workspace_bytes(const qsa_verify_shape *s) {
+    if (check_verify_sizes(s) != QSA_OK || s->num_reqs == 0) return 0;
+    return 0;
+}
+
+qsa_status qsa_verify_drafts_check(const float *probs, const float *draft_probs, const int32_t *tokens,
+                                   const int32_t *q_starts, const float *uniforms, const float *sample_uniforms,
+                                   const int32_t *out_tokens, const int32_t *num_tokens, const qsa_verify_shape *s,
+                                   const void *workspace, int64_t workspace_bytes) {
+    qsa_status st = check_verify(probs, draft_probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens, s);
+    if (st != QSA_OK) return st;
+    return check_workspace(workspace, workspace_bytes, qsa_verify_drafts_workspace_bytes(s));
+}
+
+qsa_status qsa_verify_drafts(const float *probs, const float *draft_probs, const int32_t *tokens,
+                             const int32_t *q_starts, const float *uniforms, const float *sample_uniforms,
+                             int32_t *out_tokens, int32_t *num_tokens, const qsa_verify_shape *s, void *workspace,
+                             int64_t workspace_bytes, void *stream) {
+    qsa_status st = qsa_verify_drafts_check(probs, draft_probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens,
+                                            num_tokens, s, workspace, workspace_bytes);
+    if (st != QSA_OK) return st;
+    if (s->num_reqs == 0) return ok();
+    const int64_t need = qsa_verify_drafts_workspace_bytes(s);
+    qsa::VerifyArgs a = {probs, draft_probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens,
+                         need > 0 ? static_cast<double *>(workspace) : nullptr, s->num_rows, s->num_reqs, s->vocab,
+                         s->max_tokens, (s->vocab + qsa::kVerifySpan - 1) / qsa::kVerifySpan, s->prob_stride,
+                         s->draft_stride};
+    return launched(qsa::launch_verify(a, static_cast<hipStream_t>(stream)));
 }
 
 int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *s) {

@@ -1,4 +1,5 @@
-"""The calls around the scorer: batch plan, cache writes and attention.
+"""The calls around the scorer: batch plan, cache writes, head norms with rotary
+positions, attention, and the verification of drafted tokens.
 
 Marshalling only, like the rest of the binding (``include/qsaidx.h`` has the
 contracts).  Each call comes as a function and as a ``Prepared`` class: a call
@@ -11,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import math
 from typing import Any, Optional
 
 from . import (BF16, E_DTYPE, FP8_E4M3FN, FP16, KV_PAGED, OK, QsaError, _check_rows_i32, _ptr, _raise_on, _require,
@@ -35,6 +37,21 @@ class KeysShape(ctypes.Structure):
                [("num_blocks", ctypes.c_int64), ("src_stride", ctypes.c_int64)]
 
 
+class RopeShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_rows", "num_heads", "num_kv_heads", "head_dim", "rot_dim",
+                                              "rot_offset", "layout", "dtype", "position_offset", "block_size")] + \
+               [("eps", ctypes.c_float), ("factor", ctypes.c_float)] + \
+               [(n, ctypes.c_int64) for n in ("num_blocks", "q_row_stride", "q_head_stride", "k_row_stride",
+                                              "k_head_stride", "v_row_stride", "v_head_stride", "q_out_row_stride",
+                                              "q_out_head_stride", "k_out_row_stride", "k_out_head_stride",
+                                              "kv_block_stride", "kv_slot_stride", "kv_head_stride")]
+
+
+class VerifyShape(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_rows", "num_reqs", "vocab", "max_tokens")] + \
+               [("prob_stride", ctypes.c_int64), ("draft_stride", ctypes.c_int64)]
+
+
 class AttnShape(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in ("num_rows", "num_heads", "num_kv_heads", "head_dim", "block_size",
                                               "num_reqs", "max_blocks", "dtype")] + \
@@ -54,6 +71,11 @@ def _declare():
             ("qsa_write_kv_check", [vp] * 5 + [p(KvShape)], ctypes.c_int),
             ("qsa_write_keys", [vp] * 4 + [p(KeysShape), vp], ctypes.c_int),
             ("qsa_write_keys_check", [vp] * 4 + [p(KeysShape)], ctypes.c_int),
+            ("qsa_norm_rope", [vp] * 12 + [p(RopeShape), vp], ctypes.c_int),
+            ("qsa_norm_rope_check", [vp] * 10 + [p(RopeShape)], ctypes.c_int),
+            ("qsa_verify_drafts", [vp] * 8 + [p(VerifyShape), vp, i64, vp], ctypes.c_int),
+            ("qsa_verify_drafts_check", [vp] * 8 + [p(VerifyShape), vp, i64], ctypes.c_int),
+            ("qsa_verify_drafts_workspace_bytes", [p(VerifyShape)], i64),
             ("qsa_paged_attention", [vp] * 8 + [p(AttnShape), vp, i64, vp], ctypes.c_int),
             ("qsa_paged_attention_check", [vp] * 7 + [p(AttnShape), vp, i64], ctypes.c_int),
             ("qsa_paged_attention_workspace_bytes", [p(AttnShape)], i64),
@@ -291,6 +313,146 @@ def write_keys(keys, slots, kcache, *, block_size: int, kscale=None, layout: int
 
 
 # ---------------------------------------------------------------------------
+# head norms and rotary positions
+# ---------------------------------------------------------------------------
+
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "none", factor: float = 1.0,
+                     original_len: Optional[int] = None, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                     device=None):
+    """(inv_freq, rope_scale) for ``norm_rope``: f64 [rot_dim / 2] radians per position,
+    base ** (-2 i / rot_dim), and the factor on cosines and sines.  For contexts
+    ``factor`` times longer:
+
+    - ``"linear"``: all positions stretched by the factor.
+    - ``"ntk"``: the base raised so that the slowest pair is stretched by the factor
+      and the fastest is not.
+    - ``"yarn"``: pairs that turn less than ``beta_slow`` times in ``original_len``
+      positions stretched, those that turn more than ``beta_fast`` times kept, a ramp over the pairs
+      between; rope_scale = 0.1 ln(factor) + 1."""
+    import torch
+    _require(rot_dim >= 0 and rot_dim % 2 == 0, f"rot_dim = {rot_dim} must be even and >= 0")
+    _require(base > 1.0 and factor >= 1.0, "base must be > 1 and factor >= 1")
+    _require(scaling in ("none", "linear", "ntk", "yarn"), f"unknown scaling {scaling!r}")
+    i = torch.arange(0, rot_dim, 2, dtype=torch.float64)
+    if scaling == "ntk":
+        _require(rot_dim > 2, "ntk needs rot_dim > 2")
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    freq = float(base) ** (-i / max(rot_dim, 1))
+    scale = 1.0
+    if scaling == "linear":
+        freq = freq / factor
+    elif scaling == "yarn":
+        _require(original_len is not None and original_len > 0 and beta_fast > beta_slow > 0,
+                 "yarn needs original_len and beta_fast > beta_slow > 0")
+
+        def pair(turns):  # the pair that turns so often in original_len positions
+            return rot_dim * math.log(original_len / (turns * 2 * math.pi)) / (2 * math.log(base))
+
+        low = max(math.floor(pair(beta_fast)), 0)
+        high = min(math.ceil(pair(beta_slow)), rot_dim - 1)
+        ramp = ((i / 2 - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+        freq = freq / factor * ramp + freq * (1.0 - ramp)
+        scale = 0.1 * math.log(factor) + 1.0
+    return freq.to(device), scale
+
+
+def _heads(name, t, rows, dim, dtype):
+    """(row stride, head stride) of a [R, heads, head_dim] tensor."""
+    _require(t.dtype == dtype, f"{name} must have the heads' type {dtype}")
+    _require(t.dim() == 3 and int(t.shape[0]) == rows and int(t.shape[2]) == dim and (t.stride(2) == 1 or dim == 1),
+             f"{name} must be [R, heads, head_dim] with a contiguous last dimension")
+    # the stride of a dimension of one element has no meaning: any allowed value does
+    return int(t.stride(0)) if rows > 1 else dim, int(t.stride(1)) if int(t.shape[1]) > 1 else dim
+
+
+class PreparedNormRope(_Prepared):
+    """A validated ``qsa_norm_rope`` call on fixed tensors."""
+
+    def __init__(self, q, k, positions, inv_freq, q_out=None, *, k_out=None, v=None, slots=None, kcache=None,
+                 vcache=None, q_weight=None, k_weight=None, eps: float = 1e-6, rot_offset: int = 0,
+                 layout: int = ROPE_HALF, rope_scale: float = 1.0, position_offset: int = 0, stream=None):
+        import torch
+        dev = _one_device(positions=positions, inv_freq=inv_freq, q=q, k=k, v=v, slots=slots, q_out=q_out, k_out=k_out,
+                          kcache=kcache, vcache=vcache, q_weight=q_weight, k_weight=k_weight)
+        some = q if q is not None else k
+        _require(some is not None and some.dim() == 3, "q and k must be [R, heads, head_dim]; one of them may be None")
+        code = _half_code("q" if q is not None else "k", some)
+        R, d, dt = int(some.shape[0]), int(some.shape[2]), some.dtype
+        _require((q is None) == (q_out is None), "q and q_out belong together")
+        _require((v is None) == (vcache is None), "v and vcache belong together")
+        _require(k is not None or (k_out is None and kcache is None and v is None), "outputs of keys without k")
+        strides = {}
+        for name, t, like in (("q", q, q), ("k", k, k), ("v", v, k), ("q_out", q_out, q), ("k_out", k_out, k)):
+            strides[name] = (0, 0)
+            if t is not None:
+                strides[name] = _heads(name, t, R, d, dt)
+                _require(t.shape == like.shape, f"{name} must have the shape of its heads")
+        cache = dict(block_size=0, num_blocks=0, kv_block_stride=0, kv_slot_stride=0, kv_head_stride=0)
+        if kcache is not None:
+            kv = _kv_strides("kcache", kcache)
+            _require(kcache.dtype == dt and (int(kcache.shape[2]), int(kcache.shape[3])) == (int(k.shape[1]), d),
+                     "kcache must have k's type and heads")
+            if vcache is not None:
+                _require(vcache.dtype == dt and vcache.shape == kcache.shape and _kv_strides("vcache", vcache) == kv,
+                         "kcache and vcache must have equal types, shapes and strides")
+            _require(slots is not None, "kcache needs slots")
+            _rows("slots", slots, R, torch.int64)
+            cache = dict(block_size=int(kcache.shape[1]), num_blocks=int(kcache.shape[0]), kv_block_stride=kv[0],
+                         kv_slot_stride=kv[1], kv_head_stride=kv[2])
+        else:
+            _require(slots is None and vcache is None, "slots and vcache go with kcache")
+        _rows("positions", positions, R, torch.int32)
+        _rows("inv_freq", inv_freq, int(inv_freq.numel()), torch.float64)
+        for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+            if w is not None:
+                _rows(name, w, d, torch.float32)
+        _require(q_weight is None or q is not None, "q_weight without q")
+        _require(k_weight is None or k is not None, "k_weight without k")
+        self.shape = RopeShape(
+            num_rows=R, num_heads=0 if q is None else int(q.shape[1]), num_kv_heads=0 if k is None else int(k.shape[1]),
+            head_dim=d, rot_dim=2 * int(inv_freq.numel()), rot_offset=int(rot_offset), layout=int(layout), dtype=code,
+            position_offset=int(position_offset), eps=float(eps), factor=float(rope_scale),
+            **{f"{n}_{w}_stride": strides[n][i] for n in strides for i, w in enumerate(("row", "head"))}, **cache)
+        shape = ctypes.byref(self.shape)
+        ins = (_ptr(q), _ptr(k), _ptr(v))
+        at = (_ptr(positions), _ptr(inv_freq), _ptr(slots))
+        outs = (_ptr(q_out), _ptr(k_out), _ptr(kcache), _ptr(vcache))
+        _raise_on(lib.qsa_norm_rope_check(*ins, *at, *outs, shape))
+        self.q_out, self.k_out = q_out, k_out
+        self._ready(lib.qsa_norm_rope, (*ins, _ptr(q_weight), _ptr(k_weight), *at, *outs, shape), dev, stream,
+                    (q, k, v, q_weight, k_weight, positions, inv_freq, slots, q_out, k_out, kcache, vcache))
+
+    def __call__(self):
+        self._launch()
+        return self.q_out, self.k_out
+
+
+def norm_rope(q, k, positions, inv_freq, *, q_out=None, k_out=None, v=None, slots=None, kcache=None, vcache=None,
+              q_weight=None, k_weight=None, eps: float = 1e-6, rot_offset: int = 0, layout: int = ROPE_HALF,
+              rope_scale: float = 1.0, position_offset: int = 0, stream=None):
+    """``qsa_norm_rope``: heads of q and k [R, heads, head_dim] (either may be None) normed
+    where they have a weight (f32 [head_dim]) and rotated by ``positions`` (int32 [R], plus
+    ``position_offset``: -1 with a plan's ``ctx_lens``) in elements [rot_offset,
+    rot_offset + 2 len(inv_freq)); ``rope_frequencies`` makes inv_freq and rope_scale.
+    With ``kcache`` and ``slots`` the keys go to the paged cache, and v to ``vcache``.
+    Returns (q_out, k_out); k_out is None where only the cache takes the keys.  Rows with a
+    negative position are not written (0 in outputs made here)."""
+    import torch
+    _one_device(positions=positions)
+    with _on(stream, positions.device):
+        if q is not None and q_out is None:
+            q_out = torch.zeros(tuple(q.shape), dtype=q.dtype, device=q.device)
+        if k is not None and k_out is None and kcache is None:
+            k_out = torch.zeros(tuple(k.shape), dtype=k.dtype, device=k.device)
+        return PreparedNormRope(q, k, positions, inv_freq, q_out, k_out=k_out, v=v, slots=slots, kcache=kcache,
+                                vcache=vcache, q_weight=q_weight, k_weight=k_weight, eps=eps, rot_offset=rot_offset,
+                                layout=layout, rope_scale=rope_scale, position_offset=position_offset)()
+
+
+# ---------------------------------------------------------------------------
 # attention
 # ---------------------------------------------------------------------------
 
@@ -448,3 +610,79 @@ def paged_attention_workspace_bytes(shape: AttnShape) -> int:
 def sparse_attention_workspace_bytes(shape: AttnShape, k: int, ratio: int = 1) -> int:
     """``qsa_sparse_attention_workspace_bytes`` (see ``make_attn_shape``)."""
     return int(lib.qsa_sparse_attention_workspace_bytes(ctypes.byref(shape), int(k), int(ratio)))
+
+
+# ---------------------------------------------------------------------------
+# verification of drafted tokens
+# ---------------------------------------------------------------------------
+
+class PreparedVerifyDrafts(_Prepared):
+    """A validated ``qsa_verify_drafts`` call on fixed tensors (workspace as in
+    PreparedPagedAttention)."""
+
+    def __init__(self, probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens, *, draft_probs=None,
+                 workspace="auto", stream=None):
+        import torch
+        dev = _one_device(probs=probs, draft_probs=draft_probs, tokens=tokens, q_starts=q_starts, uniforms=uniforms,
+                          sample_uniforms=sample_uniforms, out_tokens=out_tokens, num_tokens=num_tokens)
+        for name, t in (("probs", probs), ("draft_probs", draft_probs)):
+            if t is not None:
+                _require(t.dtype == torch.float32 and t.dim() == 2 and t.shape == probs.shape and
+                         (t.stride(1) == 1 or int(t.shape[1]) == 1), f"{name} must be f32 [R, V], its rows contiguous")
+        R, v = (int(x) for x in probs.shape)
+        _require(out_tokens.dtype == torch.int32 and out_tokens.dim() == 2 and out_tokens.is_contiguous(),
+                 "out_tokens must be contiguous int32 [n, max_tokens]")
+        n, most = (int(x) for x in out_tokens.shape)
+        _rows("tokens", tokens, R, torch.int32)
+        _rows("uniforms", uniforms, R, torch.float32)
+        _rows("q_starts", q_starts, n + 1, torch.int32)
+        _rows("sample_uniforms", sample_uniforms, n, torch.float32)
+        _rows("num_tokens", num_tokens, n, torch.int32)
+
+        def stride(t):
+            return v if t is None or R <= 1 else int(t.stride(0))
+
+        self.shape = VerifyShape(num_rows=R, num_reqs=n, vocab=v, max_tokens=most, prob_stride=stride(probs),
+                                 draft_stride=stride(draft_probs))
+        shape = ctypes.byref(self.shape)
+        args = (_ptr(probs), _ptr(draft_probs), _ptr(tokens), _ptr(q_starts), _ptr(uniforms), _ptr(sample_uniforms),
+                _ptr(out_tokens), _ptr(num_tokens))
+        _raise_on(lib.qsa_verify_drafts_check(*args, shape, None, 0))
+        with _on(stream, dev):
+            ws = self.workspace = _scratch(workspace, int(lib.qsa_verify_drafts_workspace_bytes(shape)), dev)
+        _raise_on(lib.qsa_verify_drafts_check(*args, shape, _ptr(ws), _nbytes(ws)))
+        self.out_tokens, self.num_tokens = out_tokens, num_tokens
+        self._ready(lib.qsa_verify_drafts, (*args, shape, _ptr(ws), _nbytes(ws)), dev, stream,
+                    (probs, draft_probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens, ws))
+
+    def __call__(self):
+        self._launch()
+        return self.out_tokens, self.num_tokens
+
+
+def verify_drafts(probs, tokens, q_starts, uniforms, sample_uniforms, *, max_tokens: int, draft_probs=None,
+                  out_tokens=None, num_tokens=None, workspace="auto", stream=None):
+    """``qsa_verify_drafts``: which drafts of a verify step's requests are kept, and the token
+    after them.  ``probs`` f32 [R, V] are the target's distributions of the step's rows,
+    ``tokens`` int32 [R] the rows' inputs (a request's last token, then its drafts),
+    ``draft_probs`` the distributions the drafts came from, row by row with ``probs`` (None:
+    each was certain); ``uniforms`` f32 [R] and ``sample_uniforms`` f32 [n] in [0, 1).
+    Returns (int32 [n, max_tokens] tokens, -1 behind the last, int32 [n] their number)."""
+    import torch
+    _one_device(probs=probs, q_starts=q_starts)
+    n = int(q_starts.numel()) - 1
+    _require(n >= 0, "q_starts must have an entry more than there are requests")
+    with _on(stream, probs.device):
+        if out_tokens is None:
+            out_tokens = torch.empty((n, int(max_tokens)), dtype=torch.int32, device=probs.device)
+        if num_tokens is None:
+            num_tokens = torch.empty(n, dtype=torch.int32, device=probs.device)
+        _require(out_tokens.dim() == 2 and int(out_tokens.shape[1]) == int(max_tokens),
+                 "out_tokens must be [n, max_tokens]")
+        return PreparedVerifyDrafts(probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens,
+                                    draft_probs=draft_probs, workspace=workspace)()
+
+
+def verify_drafts_workspace_bytes(shape: VerifyShape) -> int:
+    """``qsa_verify_drafts_workspace_bytes``."""
+    return int(lib.qsa_verify_drafts_workspace_bytes(ctypes.byref(shape)))
