@@ -314,6 +314,7 @@ QSA_API qsa_status qsa_expand(const int32_t *idx, int32_t num_rows, int32_t k, i
  *   qsa_write_keys        new index keys into the scorer's cache
  *   qsa_norm_rope         head norms and rotary positions, keys and values to the caches
  *   qsa_paged_attention   attention over all visible tokens
+ *   qsa_window_attention  attention over the newest tokens and the first ones
  *   qsa_sparse_attention  attention over the tokens of the selected columns
  *   qsa_verify_drafts     drafted tokens against the target's probabilities
  */
@@ -565,7 +566,35 @@ QSA_API qsa_status qsa_paged_attention_check(const void *q, const void *kcache, 
 QSA_API int64_t qsa_paged_attention_workspace_bytes(const qsa_attn_shape *shape);
 
 /*
- * qsa_sparse_attention -- the same over selected tokens: row r attends to tokens
+ * qsa_window_attention -- qsa_paged_attention over a sliding window and the first tokens:
+ * row r sees the newest `window` of its ctx_lens[r] tokens and the first `sinks`, that is
+ * the columns c < ctx_lens[r] with c >= ctx_lens[r] - window or c < sinks, each once.
+ *
+ * Table entries and tokens that no row of a request sees are not used when its rows'
+ * visible counts are neighbours (qsa_plan_batch's are): the blocks between the first
+ * tokens and the oldest row's window may have been freed, their entries be anything.  (With
+ * other counts, rows far apart in one request, entries between their windows are read
+ * too: those outside [0, num_blocks) cost time, nothing else.)
+ *
+ *   window    >= 1.  sinks >= 0.
+ *   workspace as above, qsa_window_attention_workspace_bytes(shape, window, sinks).
+ *
+ * The other arguments, errors and limits are qsa_paged_attention's.
+ */
+QSA_API qsa_status qsa_window_attention(const void *q, const void *kcache, const void *vcache,
+                                        const int32_t *block_table, const int32_t *ctx_lens,
+                                        const int32_t *q_starts, int32_t window, int32_t sinks, void *out, float *lse,
+                                        const qsa_attn_shape *shape, void *workspace, int64_t workspace_bytes,
+                                        void *stream);
+QSA_API qsa_status qsa_window_attention_check(const void *q, const void *kcache, const void *vcache,
+                                              const int32_t *block_table, const int32_t *ctx_lens,
+                                              const int32_t *q_starts, int32_t window, int32_t sinks, const void *out,
+                                              const qsa_attn_shape *shape, const void *workspace,
+                                              int64_t workspace_bytes);
+QSA_API int64_t qsa_window_attention_workspace_bytes(const qsa_attn_shape *shape, int32_t window, int32_t sinks);
+
+/*
+ * qsa_sparse_attention -- qsa_paged_attention over selected tokens: row r attends to tokens
  * idx[r][p] * ratio + j, j < ratio, for its non-negative idx (qsa_topk's output,
  * or with ratio 1 qsa_expand's); tokens at or behind token_lens[r] are left out.
  * The order of a row's indices does not matter; an index given twice counts

@@ -33,7 +33,8 @@ EXPORTED = ("qsa_paged_logits", "qsa_paged_logits_timed", "qsa_paged_logits_chec
             "qsa_write_keys", "qsa_write_keys_check", "qsa_paged_attention", "qsa_paged_attention_check",
             "qsa_paged_attention_workspace_bytes", "qsa_sparse_attention", "qsa_sparse_attention_check",
             "qsa_sparse_attention_workspace_bytes", "qsa_norm_rope", "qsa_norm_rope_check", "qsa_verify_drafts",
-            "qsa_verify_drafts_check", "qsa_verify_drafts_workspace_bytes", "qsa_last_error", "qsa_version")
+            "qsa_verify_drafts_check", "qsa_verify_drafts_workspace_bytes", "qsa_window_attention",
+            "qsa_window_attention_check", "qsa_window_attention_workspace_bytes", "qsa_last_error", "qsa_version")
 
 
 class QsaError(RuntimeError):
@@ -452,7 +453,8 @@ def paged_logits_topk(q, kcache, block_table, ctx_lens, row_to_req, *, k: int, w
 
 from .serving import (ROPE_HALF, ROPE_INTERLEAVED, AttnShape, BatchPlan, KeysShape, KvShape, PlanShape,  # noqa: E402
                       PreparedNormRope, PreparedPagedAttention, PreparedPlanBatch, PreparedSparseAttention,
-                      PreparedVerifyDrafts, PreparedWriteKeys, PreparedWriteKv, RopeShape, VerifyShape, make_attn_shape,
-                      norm_rope, paged_attention, paged_attention_workspace_bytes, plan_batch, rope_frequencies,
-                      sparse_attention, sparse_attention_workspace_bytes, verify_drafts, verify_drafts_workspace_bytes,
-                      write_keys, write_kv)
+                      PreparedVerifyDrafts, PreparedWindowAttention, PreparedWriteKeys, PreparedWriteKv, RopeShape,
+                      VerifyShape, make_attn_shape, norm_rope, paged_attention, paged_attention_workspace_bytes,
+                      plan_batch, rope_frequencies, sparse_attention, sparse_attention_workspace_bytes, verify_drafts,
+                      verify_drafts_workspace_bytes, window_attention, window_attention_workspace_bytes, write_keys,
+                      write_kv)

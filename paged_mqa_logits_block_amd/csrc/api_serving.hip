@@ -1,6 +1,6 @@
 // C-ABI entry points around the scorer: the batch plan, the cache writes, head norms
-// with rotary positions, attention over the paged cache (all visible tokens, or the
-// selected ones), and the verification of drafted tokens.
+// with rotary positions, attention over the paged cache (all visible tokens, the newest
+// and first ones, or the selected ones), and the verification of drafted tokens.
 // As in api.hip, validation reads host scalars only and every call can be
 // captured.
 #include "api_common.h"
@@ -249,6 +249,7 @@ struct AttnPlan {
     int64_t bytes;             // workspace of a cut launch, 0: not cut
 };
 
+// keys: the most that a tile works through, or with a window about that many
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     AttnPlan p = {};
     const int group = s->num_heads / s->num_kv_heads;
@@ -286,7 +287,8 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     const int64_t least = n < R ? n : R, full = (R + T - 1) / T, tiles = (full > least ? full : least) * tile_heads;
     if (p.slots > qsa::kMaxSlots || n > qsa::kMaxSlots || R > kCutRows || tiles > kCutTiles) return p;
     // the workgroups add up the slots' steps of 64 keys in 32 bits
-    if (p.slots * (keys / 64 + 1) > 0x7FFFFFFF) return p;
+    const int64_t cap = (int64_t)s->max_blocks * s->block_size;
+    if (p.slots * (cap / 64 + 1) > 0x7FFFFFFF) return p;
     p.tiles = (R / T + least) * heads;
     if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.tiles);
     if (!p.stream && (n > 1 || fills_badly(tiles)))
@@ -354,6 +356,18 @@ qsa_status check_attn(const void *q, const void *kcache, const void *vcache, con
                              s->kv_block_stride | s->kv_slot_stride | s->kv_head_stride) & 7) != 0)
         return fail(QSA_E_ALIGN, "strides must be multiples of 8 elements");
     return ok();
+}
+
+qsa_status check_window(int32_t window, int32_t sinks) {
+    if (window < 1) return fail(QSA_E_INVALID, "window = %d < 1", window);
+    if (sinks < 0) return fail(QSA_E_INVALID, "sinks = %d < 0", sinks);
+    return ok();
+}
+
+// what the keys of a windowed call come to
+int64_t window_keys(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
+    const int64_t cap = (int64_t)s->max_blocks * s->block_size, seen = (int64_t)window + sinks;
+    return seen < cap ? seen : cap;
 }
 
 qsa_status check_workspace(const void *workspace, int64_t bytes, int64_t need) {
@@ -577,6 +591,40 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
     launch_shape(a, p, workspace);
     return launched(p.stream ? qsa::launch_attn_stream(a, false, static_cast<hipStream_t>(stream))
                              : qsa::launch_attn_tile(a, static_cast<hipStream_t>(stream)));
+}
+
+int64_t qsa_window_attention_workspace_bytes(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
+    if (check_attn_sizes(s, false, 0, 0) != QSA_OK || check_window(window, sinks) != QSA_OK || s->num_rows == 0) return 0;
+    return plan_attn(s, false, window_keys(s, window, sinks)).bytes;
+}
+
+qsa_status qsa_window_attention_check(const void *q, const void *kcache, const void *vcache,
+                                      const int32_t *block_table, const int32_t *ctx_lens, const int32_t *q_starts,
+                                      int32_t window, int32_t sinks, const void *out, const qsa_attn_shape *s,
+                                      const void *workspace, int64_t workspace_bytes) {
+    qsa_status st = check_attn(q, kcache, vcache, block_table, ctx_lens, q_starts, out, s, false, 0, 0);
+    if (st == QSA_OK) st = check_window(window, sinks);
+    if (st != QSA_OK) return st;
+    return check_workspace(workspace, workspace_bytes, qsa_window_attention_workspace_bytes(s, window, sinks));
+}
+
+qsa_status qsa_window_attention(const void *q, const void *kcache, const void *vcache, const int32_t *block_table,
+                                const int32_t *ctx_lens, const int32_t *q_starts, int32_t window, int32_t sinks,
+                                void *out, float *lse, const qsa_attn_shape *s, void *workspace,
+                                int64_t workspace_bytes, void *stream) {
+    qsa_status st = qsa_window_attention_check(q, kcache, vcache, block_table, ctx_lens, q_starts, window, sinks, out, s,
+                                               workspace, workspace_bytes);
+    if (st != QSA_OK) return st;
+    if (s->num_rows == 0) return ok();
+    const AttnPlan p = plan_attn(s, false, window_keys(s, window, sinks));
+    qsa::AttnArgs a = attn_args(q, kcache, vcache, block_table, out, lse, s);
+    a.ctx_lens = ctx_lens;
+    a.q_starts = q_starts;
+    a.window = window;
+    a.sinks = sinks;
+    launch_shape(a, p, workspace);
+    return launched(p.stream ? qsa::launch_window_stream(a, static_cast<hipStream_t>(stream))
+                             : qsa::launch_window_tile(a, static_cast<hipStream_t>(stream)));
 }
 
 int64_t qsa_sparse_attention_workspace_bytes(const qsa_attn_shape *s, int32_t k, int32_t ratio) {

@@ -347,6 +347,54 @@ __device__ __forceinline__ uint32_t block_index(const AttnArgs &a, uint32_t tok)
     return __umulhi(2 * tok, a.div_mul) >> a.div_shift;
 }
 
+// The tokens that a tile of rows works through, in steps of KEYS.  Without a window
+// these are the first `keys`.  With one they are the first tokens and those from the
+// oldest row's window on: `head` steps of the former, then `gap` steps left out, in
+// whole steps, so that a step's tokens are neighbours.  Tokens of a step that no row
+// sees may lie in blocks that have been freed: copies take a token that is seen in
+// their place.
+struct KeySpan {
+    int keys;        // behind the last token that a row sees
+    int first, old;  // tokens of [first, old) are not seen by any row
+    int head, gap;
+};
+
+// hi: the rows' largest visible count, lo: the smallest one above 0
+template <bool WINDOW, int KEYS>
+__device__ __forceinline__ KeySpan key_span(const AttnArgs &a, int hi, int lo) {
+    KeySpan s = {hi, 0, 0, 0, 0};
+    if constexpr (WINDOW) {
+        if (hi <= 0) return s;
+        s.first = min(a.sinks, hi);
+        s.old = max(lo - a.window, 0);
+        s.head = (s.first + KEYS - 1) / KEYS;
+        s.gap = max(s.old / KEYS - s.head, 0);
+    }
+    return s;
+}
+template <int KEYS>
+__device__ __forceinline__ int span_steps(const KeySpan &s) { return (s.keys + KEYS - 1) / KEYS - s.gap; }
+// the step of a request's tokens that is step s of the span
+template <bool WINDOW>
+__device__ __forceinline__ int token_step(const KeySpan &k, int s) { return WINDOW && s >= k.head ? s + k.gap : s; }
+// the token that is copied for `tok`
+template <bool WINDOW>
+__device__ __forceinline__ int copied_token(const KeySpan &k, int tok) {
+    if (tok >= k.keys) return k.keys - 1;
+    return WINDOW && tok >= k.first && tok < k.old ? k.old : tok;
+}
+// whether a row with ctx visible tokens sees token tok
+template <bool WINDOW>
+__device__ __forceinline__ bool sees(const AttnArgs &a, int ctx, int tok) {
+    return tok < ctx && (!WINDOW || tok < a.sinks || tok >= ctx - a.window);
+}
+// whether the tokens [tok, tok + KEYS) are not seen by all rows, whose visible counts are
+// from `least` to `most`
+template <bool WINDOW, int KEYS>
+__device__ __forceinline__ bool partly_seen(const AttnArgs &a, int tok, int least, int most) {
+    return tok + KEYS > least || (WINDOW && tok < most - a.window && tok + KEYS > a.sinks);
+}
+
 // byte offset of place `in` of pool block `block`, kv head hk
 __device__ __forceinline__ int64_t kv_offset(const AttnArgs &a, uint32_t block, uint32_t in, int hk) {
     return (int64_t)(((uint64_t)block * a.kv_block + (uint64_t)in * a.kv_slot + (uint64_t)(uint32_t)hk * a.kv_head) << 4);
@@ -409,8 +457,9 @@ __device__ __forceinline__ RowTile find_tile(const AttnArgs &a, const Requests &
 // count, or -1 for a slot without rows.  A thread takes consecutive rows, 8 counts on
 // their way at once (one at a time, and with a division per row, this took 10 us for
 // 3,163 rows).
-template <int THREADS>
-__device__ __forceinline__ void slot_counts(const AttnArgs &a, Requests &q, int32_t *counts) {
+// `lows`, with WINDOW: each slot's smallest visible count above 0.
+template <int THREADS, bool WINDOW>
+__device__ __forceinline__ void slot_counts(const AttnArgs &a, Requests &q, int32_t *counts, int32_t *lows) {
     constexpr int kBatch = 8;
     const int t = threadIdx.x, n = a.num_reqs, T = a.tile_rows;
     for (int i = t; i <= n; i += THREADS) {
@@ -418,7 +467,10 @@ __device__ __forceinline__ void slot_counts(const AttnArgs &a, Requests &q, int3
         q.row[i] = s;
         q.slot[i] = s / T + i;
     }
-    for (int i = t; i <= a.slots; i += THREADS) counts[i] = -1;
+    for (int i = t; i <= a.slots; i += THREADS) {
+        counts[i] = -1;
+        if constexpr (WINDOW) lows[i] = 0x7FFFFFFF;
+    }
     __syncthreads();
     const int per = (a.num_rows + THREADS - 1) / THREADS, r0 = t * per, r1 = min(r0 + per, a.num_rows);
     int req = 0;
@@ -448,7 +500,10 @@ __device__ __forceinline__ void slot_counts(const AttnArgs &a, Requests &q, int3
                 in = 0;
             }
             if (r < s || r >= e) continue;
-            if (at < a.slots) atomicMax(&counts[at], v[j]);
+            if (at < a.slots) {
+                atomicMax(&counts[at], v[j]);
+                if (WINDOW && v[j] > 0) atomicMin(&lows[at], v[j]);
+            }
             if (++in == T) {
                 in = 0;
                 ++at;
@@ -546,11 +601,10 @@ struct FirstPlaces {
     int nan[D / 64], inf[D / 64], minus[D / 64];
 };
 
+// adds the places [k0, k1)
 template <int DT, int D, bool SPARSE>
-__device__ __forceinline__ FirstPlaces<D> first_places(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit,
-                                                       int k0, int k1) {
-    FirstPlaces<D> f;
-    for (int i = 0; i < D / 64; ++i) f.nan[i] = f.inf[i] = f.minus[i] = 0x7FFFFFFF;
+__device__ __forceinline__ void find_places(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit, int k0,
+                                            int k1, FirstPlaces<D> &f) {
     for (int base = k0; base < k1; base += kWave) {
         int64_t off = 0;
         bool bad = false;
@@ -572,17 +626,28 @@ __device__ __forceinline__ FirstPlaces<D> first_places(const AttnArgs &a, int re
             }
         }
     }
+}
+
+template <int D>
+__device__ __forceinline__ FirstPlaces<D> no_places() {
+    FirstPlaces<D> f;
+    for (int i = 0; i < D / 64; ++i) f.nan[i] = f.inf[i] = f.minus[i] = 0x7FFFFFFF;
     return f;
 }
 
-// One pair's softmax state over its own keys [k0, k1), by one wave with plain loads and
+template <int DT, int D, bool SPARSE>
+__device__ __forceinline__ FirstPlaces<D> first_places(const AttnArgs &a, int req, int hk, const int32_t *idx, int limit,
+                                                       int k0, int k1) {
+    FirstPlaces<D> f = no_places<D>();
+    find_places<DT, D, SPARSE>(a, req, hk, idx, limit, k0, k1, f);
+    return f;
+}
+
+// Adds a pair's own keys [k0, k1) to its softmax state, by one wave with plain loads and
 // 32-bit weights: no other key's value is touched.
 template <int DT, int D>
 __device__ __forceinline__ void own_range(const AttnArgs &a, int req, const uint16_t *q, int hk, int k0, int k1, float &m,
                                           float &l, float (&o)[D / 64]) {
-    m = kNegInf;
-    l = 0.0f;
-    for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
     for (int base = k0; base < k1; base += kWave) {
         int64_t off = 0;
         bool bad = false;
@@ -628,11 +693,36 @@ struct PairPlace {
     float *state, *top, *total;   // all null, or the state's outputs, reference and sum
 };
 
-// Mends what the wave has written of one pair over its places before k1, or does the
-// pair anew (`anew`).
+// The places that a pair sees: [k0, k1), and with a window [k2, k3) before them.
+struct OwnPlaces {
+    int k0, k1, k2, k3;
+};
+
+// What a row with ctx visible tokens sees of steps [s0, s1) of KEYS keys of its tile's span.
+template <int KEYS>
+__device__ __forceinline__ OwnPlaces window_places(const AttnArgs &a, const KeySpan &span, int ctx, int s0, int s1) {
+    const int first = min(a.sinks, ctx), old = max(ctx - a.window, first);
+    // the window's steps are behind the gap, the first tokens' before it
+    const int gap = span.gap * KEYS;
+    return {max(s0 * KEYS + gap, old), min(s1 * KEYS + gap, ctx), s0 * KEYS, min(s1 * KEYS, first)};
+}
+
+// first places over all that a pair sees
+template <int DT, int D>
+__device__ __forceinline__ FirstPlaces<D> own_first_places(const AttnArgs &a, int req, int hk, const OwnPlaces &k) {
+    FirstPlaces<D> f = no_places<D>();
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i)
+        find_places<DT, D, false>(a, req, hk, nullptr, 0, i ? k.k0 : k.k2, i ? k.k1 : k.k3, f);
+    return f;
+}
+
+// Mends what the wave has written of one pair over its places `k`, of which k1 is the
+// end, or does the pair anew (`anew`).
 template <int DT, int D, bool SPARSE>
-__device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, int k0, int k1, const FirstPlaces<D> &f,
+__device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, const OwnPlaces &k, const FirstPlaces<D> &f,
                                           bool anew, const PairPlace &p) {
+    const int k1 = k.k1;
     typedef typename Half<DT>::T T;
     const int at = lane_id() * (D / 64);
     T *out = static_cast<T *>(p.out) + at;
@@ -658,8 +748,11 @@ __device__ __forceinline__ void mend_pair(const AttnArgs &a, int req, int hk, in
     }
     if constexpr (!SPARSE) {
         if (ballot(others)) {
-            float top, total;
-            own_range<DT, D>(a, req, p.q, hk, k0, k1, top, total, o);
+            float top = kNegInf, total = 0.0f;
+            for (int i = 0; i < D / 64; ++i) o[i] = 0.0f;
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i)
+                own_range<DT, D>(a, req, p.q, hk, i ? k.k0 : k.k2, i ? k1 : k.k3, top, total, o);
             if (!anew) settle();
             write = true;
             if (lane_id() == 0 && p.state) {

@@ -57,9 +57,13 @@ struct AttnArgs {
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile
+    // window: a row sees its newest `window` tokens and the first `sinks`
+    int32_t window, sinks;
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
+hipError_t launch_window_stream(const AttnArgs &a, hipStream_t s);
+hipError_t launch_window_tile(const AttnArgs &a, hipStream_t s);
 // bytes of a cut launch's workspace, of the streaming and of the tile kernel
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles);
 int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles);

@@ -41,7 +41,6 @@ namespace qsa {
 namespace {
 
 constexpr int kStreamThreads = 64 * kStreamWaves;
-constexpr int kUnitKeys = kStreamKeys * kStreamWaves;  // one step of every wave
 
 struct TileWork {
     int req, row0, rows;  // dense: a request's tile; sparse: one row
@@ -89,14 +88,20 @@ __device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, T
     return true;
 }
 
-// keys the tile works through: the largest visible count of its rows, or the
+// keys the tile works through: up to the largest visible count of its rows, or the
 // selected tokens
-template <bool SPARSE>
-__device__ __forceinline__ int tile_keys(const AttnArgs &a, int row0, int rows) {
-    if (SPARSE) return a.k * a.ratio;
-    int most = 0;
-    for (int r = 0; r < rows; ++r) most = max(most, visible(a, row0 + r));
-    return most;
+template <bool SPARSE, bool WINDOW>
+__device__ __forceinline__ KeySpan tile_keys(const AttnArgs &a, int row0, int rows) {
+    if (SPARSE) return {a.k * a.ratio, 0, 0, 0, 0};
+    int most = 0, low = 0x7FFFFFFF;
+    for (int r = 0; r < rows; ++r) {
+        const int v = visible(a, row0 + r);
+        most = max(most, v);
+        if (WINDOW && v > 0) low = min(low, v);
+    }
+    most = __builtin_amdgcn_readfirstlane(most);
+    low = __builtin_amdgcn_readfirstlane(low);
+    return key_span<WINDOW, kStreamKeys>(a, most, low);
 }
 
 // 8 (D = 128) or 4 copies fill a buffer; wait until at most one buffer's are
@@ -119,9 +124,11 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int group, int tile
 
 // NARROW (selected tokens of up to 16 heads): the 16x16x32 MFMA on 16 pairs instead of
 // the 32x32x16 one on 32, with half the products and half the weights per key.
-template <int DT, int D, bool SPARSE, bool NARROW>
+// WINDOW: the newest tokens and the first ones only (see KeySpan).
+template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
 struct Stream {
     static_assert(SPARSE || !NARROW, "dense tiles fill 32 pairs where they can");
+    static_assert(!SPARSE || !WINDOW, "a selection is its own window");
     static constexpr int kTileBytes = kStreamKeys * D * 2;  // one buffer of keys or values
     static constexpr int kCopies = kTileBytes / (16 * kWave);
     static constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
@@ -138,10 +145,11 @@ struct Stream {
     // lanes of a pair nor those of a chunk meet in one bank
     static __device__ __forceinline__ int left_at(int p, int c) { return p * D + 4 * (c ^ (p & (D / 4 - 1))); }
 
-    // keys [32 t0, 32 t1) of tile w (of its `keys`); dest: the workspace place of
-    // the state, or null to write the outputs
-    static __device__ __forceinline__ void run(const AttnArgs &a, Shared &sh, const TileWork &w, int keys, int t0,
+    // steps [t0, t1) of tile w's keys; dest: the workspace place of the state, or null to
+    // write the outputs
+    static __device__ __forceinline__ void run(const AttnArgs &a, Shared &sh, const TileWork &w, KeySpan span, int t0,
                                                int t1, float *dest) {
+        const int keys = span.keys;
         int t = threadIdx.x;
         asm volatile("" : "+v"(t));  // addresses are made anew for each range, not kept live across them
         const int lane = t & 63, wave = __builtin_amdgcn_readfirstlane(t >> 6);
@@ -170,7 +178,9 @@ struct Stream {
         const int32_t *table = a.block_table + (int64_t)max(w.req, 0) * a.max_blocks;
         const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
         // the wave's step j, and this lane's place in it (both half waves alike)
-        const auto place = [&](int j) { return (t0 + wave + j * kStreamWaves) * kStreamKeys + (lane & 31); };
+        const auto place = [&](int j) {
+            return token_step<WINDOW>(span, t0 + wave + j * kStreamWaves) * kStreamKeys + (lane & 31);
+        };
         const auto have = [&](int j) { return t0 + wave + j * kStreamWaves < t1; };
 
         struct Token {
@@ -193,14 +203,17 @@ struct Stream {
             } else {
                 // behind the last visible key the copies take that key again
                 k.seen = true;
-                tok = (uint32_t)max(min(pos, keys - 1), 0);
+                tok = (uint32_t)max(copied_token<WINDOW>(span, pos), 0);
             }
             k.entry = block_index(a, tok);
             k.in = tok - k.entry * (uint32_t)a.block_size;
             return k;
         };
         const auto copy_entry = [&](int j, const Token &k) {
-            copy4(table + k.entry, entry_lds + (j & 1) * 4 * kWave);
+            uint32_t lds = entry_lds + (j & 1) * 4 * kWave;
+            // (with the window's arithmetic the compiler keeps this in a vector register)
+            if constexpr (WINDOW) lds = __builtin_amdgcn_readfirstlane(lds);
+            copy4(table + k.entry, lds);
         };
         // byte offsets of the keys that this lane copies parts of, which keys take part, and which lie
         // behind table entries outside the pool
@@ -265,7 +278,7 @@ struct Stream {
             copy_rows(a.vcache, cur, true);
             for (int j = 0; have(j); ++j) {
                 const bool more = have(j + 1);
-                const int s = t0 + wave + j * kStreamWaves;
+                const int s = token_step<WINDOW>(span, t0 + wave + j * kStreamWaves);
                 wait_all_but<kCopies>();
                 V z[kScores];
                 if constexpr (NARROW) score_narrow<DT, D>(mine, q, z, lane);
@@ -290,9 +303,10 @@ struct Stream {
                             for (int i = 0; i < kRegs; ++i)
                                 z[u][i] = (cur.seen >> key_of(u, i)) & 1 ? z[u][i] : kNegInf;
                     }
-                } else if ((s + 1) * kStreamKeys > least) {
+                } else if (partly_seen<WINDOW, kStreamKeys>(a, s * kStreamKeys, least, keys)) {
 #pragma unroll
-                    for (int i = 0; i < kRegs; ++i) z[0][i] = s * kStreamKeys + key_of(0, i) < ctx ? z[0][i] : kNegInf;
+                    for (int i = 0; i < kRegs; ++i)
+                        z[0][i] = sees<WINDOW>(a, ctx, s * kStreamKeys + key_of(0, i)) ? z[0][i] : kNegInf;
                 }
                 softmax_step<DT>(z, a.scale_log2, m, l, o);
                 if (more) wait_all_but<kCopies>();
@@ -385,19 +399,21 @@ struct Stream {
         }
         if (mend) {
             __threadfence_block();  // what this wave wrote is read back
-            mend_pairs(launch_args(), w, wave, keys, t0 * kStreamKeys, t1 * kStreamKeys, total, dest);
+            mend_pairs(launch_args(), w, wave, span, t0, t1, total, dest);
         }
     }
 
-    // The wave's pairs of the join over places [k0, k1) (see mend_pair); sums: that of
+    // The wave's pairs of the join over steps [t0, t1) (see mend_pair); sums: that of
     // its i-th pair in lanes 16 i on.
-    static __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, TileWork w, int wave, int keys, int k0,
-                                                                int k1, float sums, float *dest) {
+    static __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, TileWork w, int wave, KeySpan span,
+                                                                int t0, int t1, float sums, float *dest) {
+        const int k0 = t0 * kStreamKeys, k1 = min(t1 * kStreamKeys, span.keys);
         constexpr int kMine = kAttnTile / kStreamWaves;
         const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
         const int limit = !SPARSE || !a.ctx_lens ? a.cap : visible(a, w.row0), req = max(w.req, 0);
-        k1 = min(k1, keys);
-        const FirstPlaces<D> f = first_places<DT, D, SPARSE>(a, req, w.hk, idx, limit, k0, k1);
+        FirstPlaces<D> f;
+        if constexpr (!WINDOW) f = first_places<DT, D, SPARSE>(a, req, w.hk, idx, limit, k0, k1);
+        int f_row = -1;  // WINDOW: the row whose tokens f is of
         for (int i = 0; i < kMine; ++i) {
             const int p = wave * kMine + i;
             const Pair x = pair_of(a, w, p);
@@ -412,25 +428,31 @@ struct Stream {
                 at.top = dest + kAttnTile * D + p;
                 at.total = dest + kAttnTile * (D + 1) + p;
             }
-            mend_pair<DT, D, SPARSE>(a, req, w.hk, k0, SPARSE ? k1 : min(k1, visible(a, x.row)), f, false, at);
+            OwnPlaces own = {k0, SPARSE ? k1 : min(k1, visible(a, x.row)), 0, 0};
+            if constexpr (WINDOW) {
+                own = window_places<kStreamKeys>(a, span, visible(a, x.row), t0, t1);
+                if (f_row != x.row) f = own_first_places<DT, D>(a, req, w.hk, own);
+                f_row = x.row;
+            }
+            mend_pair<DT, D, SPARSE>(a, req, w.hk, own, f, false, at);
         }
     }
 };
 
 // one workgroup per tile
-template <int DT, int D, bool SPARSE, bool NARROW>
+template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_stream_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE, NARROW> S;
+    typedef Stream<DT, D, SPARSE, NARROW, WINDOW> S;
     __shared__ typename S::Shared sh;
     TileWork w;
     if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
-    const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w.row0, w.rows));
-    S::run(a, sh, w, keys, 0, (keys + kStreamKeys - 1) / kStreamKeys, nullptr);
+    const KeySpan span = tile_keys<SPARSE, WINDOW>(a, w.row0, w.rows);
+    S::run(a, sh, w, span, 0, span_steps<kStreamKeys>(span), nullptr);
 }
 
-// Work in units of kUnitKeys keys: a tile with rows has one at least, so that
-// rows that see nothing are written too.
-__device__ __forceinline__ int units_of(int keys) { return max((keys + kUnitKeys - 1) / kUnitKeys, 1); }
+// Work in units of a step of every wave: a tile with rows has one at
+// least, so that rows that see nothing are written too.
+__device__ __forceinline__ int units_of(int steps) { return max((steps + kStreamWaves - 1) / kStreamWaves, 1); }
 
 // the workgroups that the line of `total` units is cut for: each has one at least
 __device__ __forceinline__ int groups_of(int64_t total) { return (int)min(total, (int64_t)kStreamGroups); }
@@ -476,9 +498,9 @@ struct LiveSlots {
 
 // Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
 // units of a slot are the same for every hs.
-template <int DT, int D, bool SPARSE, bool NARROW>
+template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE, NARROW> S;
+    typedef Stream<DT, D, SPARSE, NARROW, WINDOW> S;
     __shared__ typename S::Shared sh;
     __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
     __shared__ int32_t wave_sums[kStreamWaves];
@@ -486,18 +508,21 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
     const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
     __shared__ Requests requests;  // dense only, as is `live`
     __shared__ LiveSlots live;
+    __shared__ int32_t lows[WINDOW ? kMaxSlots + 1 : 1];  // each slot's smallest visible count
     if constexpr (SPARSE) {
-        const int u = units_of(a.k * a.ratio);
+        const int u = units_of((a.k * a.ratio + kStreamKeys - 1) / kStreamKeys);
         for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
         __syncthreads();
     } else {
-        slot_counts<kStreamThreads>(a, requests, before);
+        slot_counts<kStreamThreads, WINDOW>(a, requests, before, lows);
         constexpr int kPer = LiveSlots::kPer;
         int u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
-            u[i] = keys < 0 ? 0 : units_of(keys);
+            u[i] = 0;
+            if (keys >= 0)
+                u[i] = units_of(span_steps<kStreamKeys>(key_span<WINDOW, kStreamKeys>(a, keys, WINDOW ? lows[slot] : 0)));
             const uint64_t with_rows = ballot(keys >= 0);
             if ((t & 63) == 0) live.words[kPer * (t >> 6) + i] = with_rows;
         }
@@ -550,8 +575,8 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
             w.row0 = __builtin_amdgcn_readfirstlane(r.row0);
             w.rows = __builtin_amdgcn_readfirstlane(r.rows);
         }
-        const int keys = __builtin_amdgcn_readfirstlane(tile_keys<SPARSE>(a, w.row0, w.rows));
-        const int steps = (keys + kStreamKeys - 1) / kStreamKeys;
+        const KeySpan span = tile_keys<SPARSE, WINDOW>(a, w.row0, w.rows);
+        const int steps = span_steps<kStreamKeys>(span);
         const int t0 = __builtin_amdgcn_readfirstlane((int)(u - tile0) * kStreamWaves);
         const int t1 = __builtin_amdgcn_readfirstlane(min((int)(stop - tile0) * kStreamWaves, steps));
         float *dest = nullptr;
@@ -560,7 +585,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
             const int tile = hs * tiles + (SPARSE ? slot : live.before(slot));
             if (tile < a.tiles) dest = part_of<D>(a, g, tile);
         }
-        S::run(a, sh, w, keys, t0, t1, dest);
+        S::run(a, sh, w, span, t0, t1, dest);
         u = stop;
         __syncthreads();  // the joined states have been read before the next copies land
     }
@@ -587,15 +612,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
         a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }
 
-template <int DT, int D, bool SPARSE, bool NARROW>
+template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
 hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     const unsigned heads = (unsigned)(a.num_kv_heads * a.num_subs);
     if (!a.part) {
-        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE, NARROW>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
+        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE, NARROW, WINDOW>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
                            0, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE, NARROW>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
+    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE, NARROW, WINDOW>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>),
@@ -603,22 +628,30 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+enum class Keys { kAll, kSelected, kWindow };
+
 template <int DT, int D>
-hipError_t run_kind(const AttnArgs &a, bool sparse, hipStream_t s) {
-    if (!sparse) return run_stream<DT, D, false, false>(a, s);
-    return a.sub_heads <= 16 ? run_stream<DT, D, true, true>(a, s) : run_stream<DT, D, true, false>(a, s);
+hipError_t run_kind(const AttnArgs &a, Keys keys, hipStream_t s) {
+    if (keys == Keys::kAll) return run_stream<DT, D, false, false, false>(a, s);
+    if (keys == Keys::kWindow) return run_stream<DT, D, false, false, true>(a, s);
+    return a.sub_heads <= 16 ? run_stream<DT, D, true, true, false>(a, s) : run_stream<DT, D, true, false, false>(a, s);
 }
 
 template <int DT>
-hipError_t run_dim(const AttnArgs &a, bool sparse, hipStream_t s) {
-    return a.head_dim == 128 ? run_kind<DT, 128>(a, sparse, s) : run_kind<DT, 64>(a, sparse, s);
+hipError_t run_dim(const AttnArgs &a, Keys keys, hipStream_t s) {
+    return a.head_dim == 128 ? run_kind<DT, 128>(a, keys, s) : run_kind<DT, 64>(a, keys, s);
+}
+
+hipError_t run_type(const AttnArgs &a, Keys keys, hipStream_t s) {
+    return a.dtype == kBF16 ? run_dim<kBF16>(a, keys, s) : run_dim<kFP16>(a, keys, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s) {
-    return a.dtype == kBF16 ? run_dim<kBF16>(a, sparse, s) : run_dim<kFP16>(a, sparse, s);
+    return run_type(a, sparse ? Keys::kSelected : Keys::kAll, s);
 }
+hipError_t launch_window_stream(const AttnArgs &a, hipStream_t s) { return run_type(a, Keys::kWindow, s); }
 
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles) {
     return (kStreamGroups + tiles) * (kAttnTile * (head_dim + 2) * 4) + (int64_t)sizeof(TileSpan) * tiles;

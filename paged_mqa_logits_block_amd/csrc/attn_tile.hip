@@ -39,13 +39,16 @@ static_assert(kTilePairs == kAttnTile * kTileWaves, "32 pairs to a wave");
 template <int D>
 constexpr int kTilePart = kTilePairs * (D + 2);
 
-// The wave's pairs over keys [k0, k1), mended or done anew (see mend_pair); sums: that
-// of pair p in lane p.
-template <int DT, int D>
+// The wave's pairs over steps [s0, s1), mended or done anew (see mend_pair); sums: that
+// of pair p in lane p; most: their largest visible count.
+template <int DT, int D, bool WINDOW>
 __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, int req, int row0, int rows, int wave, int hk,
-                                                     int k0, int k1, int most, bool anew, float sums, float *dest) {
+                                                     KeySpan span, int s0, int s1, int most, bool anew, float sums,
+                                                     float *dest) {
+    const int k0 = s0 * kTileKeys, k1 = s1 * kTileKeys;
     FirstPlaces<D> f;
-    if (!anew) f = first_places<DT, D, false>(a, req, hk, nullptr, 0, k0, min(k1, most));
+    if (!anew && !WINDOW) f = first_places<DT, D, false>(a, req, hk, nullptr, 0, k0, min(k1, most));
+    int f_row = -1;  // WINDOW: the row whose tokens f is of
     for (int p = 0; p < kAttnTile; ++p) {
         const int m = wave * kAttnTile + p, r = m / a.group;
         if (r >= rows) break;
@@ -61,7 +64,13 @@ __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, int req,
             at.top = dest + kTilePairs * D + m;
             at.total = dest + kTilePairs * (D + 1) + m;
         }
-        mend_pair<DT, D, false>(a, req, hk, k0, min(k1, visible(a, row)), f, anew, at);
+        OwnPlaces own = {k0, min(k1, visible(a, row)), 0, 0};
+        if constexpr (WINDOW) {
+            own = window_places<kTileKeys>(a, span, visible(a, row), s0, s1);
+            if (!anew && f_row != row) f = own_first_places<DT, D>(a, req, hk, own);
+            f_row = row;
+        }
+        mend_pair<DT, D, false>(a, req, hk, own, f, anew, at);
     }
 }
 
@@ -146,12 +155,13 @@ inline unsigned place_grid(int num_kv_heads, int64_t per_head) {
 template <int D>
 struct TileShared {
     __align__(16) uint8_t kring[3][kTileKeys * D * 2], vring[3][kTileKeys * D * 2];
-    int most_of[kTileWaves], any_bad;
+    int most_of[kTileWaves], low_of[kTileWaves], any_bad;
 };
 
 // steps [s0, min(s1, the tile's steps)) of tile w and kv head hk; dest: the place of
-// the state, or null to write the outputs
-template <int DT, int D, bool WHOLE>
+// the state, or null to write the outputs.  WINDOW: the newest tokens and the first ones
+// only (see KeySpan).
+template <int DT, int D, bool WHOLE, bool WINDOW>
 __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, const RowTile &w, int hk, int s0, int s1,
                                           float *dest) {
     constexpr int kStepBytes = kTileKeys * D * 2;  // keys (or values) of one step
@@ -171,6 +181,10 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     const int wave_most = __builtin_amdgcn_readfirstlane(wave_max_i(ctx));
     const int wave_least = -__builtin_amdgcn_readfirstlane(wave_max_i(live ? -ctx : -0x7FFFFFFF));
     if (lane == 0) sh.most_of[wave] = wave_most;
+    if constexpr (WINDOW) {
+        const int low = -wave_max_i(ctx > 0 ? -ctx : -0x7FFFFFFF);
+        if (lane == 0) sh.low_of[wave] = low;
+    }
     if (t == 0) sh.any_bad = 0;
 
     i32x4 q[D / 16];
@@ -181,12 +195,18 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
         if (live) q[c] = *reinterpret_cast<const i32x4 *>(qrow + 16 * c + 8 * (lane >> 5));
     }
     __syncthreads();
-    int keys = 0;
+    int keys = 0, low = 0x7FFFFFFF;
 #pragma unroll
-    for (int i = 0; i < kTileWaves; ++i) keys = max(keys, sh.most_of[i]);
+    for (int i = 0; i < kTileWaves; ++i) {
+        keys = max(keys, sh.most_of[i]);
+        if (WINDOW) low = min(low, sh.low_of[i]);
+    }
     keys = __builtin_amdgcn_readfirstlane(keys);
-    const int steps = min(s1, (keys + kTileKeys - 1) / kTileKeys);
-    const bool active = wave_most > s0 * kTileKeys;
+    const KeySpan span = key_span<WINDOW, kTileKeys>(a, keys, __builtin_amdgcn_readfirstlane(low));
+    const int steps = min(s1, span_steps<kTileKeys>(span));
+    const bool active = wave_most > (WINDOW ? 0 : s0 * kTileKeys);
+    // the first token of this lane's score registers in step s
+    const auto first_token = [&](int s) { return token_step<WINDOW>(span, s) * kTileKeys; };
 
     const uint32_t kring_lds = lds_offset(kring), vring_lds = lds_offset(vring);
     const int32_t *table = a.block_table + (int64_t)w.req * a.max_blocks;
@@ -204,14 +224,21 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     const uint32_t slot_bytes = a.kv_slot * 16;  // WHOLE: 8 slots are below 2^32 bytes
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) lane_at[i] = (uint32_t)(key_row(i) - 8 * wave) * slot_bytes;
+    // WHOLE: the token whose block the wave's 8 keys of step s are copied from: their
+    // first, unless no row sees any of them
+    const auto group_token = [&](int s) {
+        const int f = first_token(s) + 8 * wave;
+        if (f >= keys) return keys - 1;
+        return WINDOW && f >= span.first && f + 7 < span.old ? span.old : f;
+    };
     const auto load_entries = [&](int s) {
         if constexpr (WHOLE) {
-            const uint32_t e = block_index(a, (uint32_t)min(s * kTileKeys + 8 * wave, keys - 1));
+            const uint32_t e = block_index(a, (uint32_t)group_token(s));
             whole_entry = ((const __attribute__((address_space(4))) int32_t *)(uintptr_t)table)[e];
         } else {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i)
-                entry[i] = table[block_index(a, (uint32_t)min(s * kTileKeys + key_row(i), keys - 1))];
+                entry[i] = table[block_index(a, (uint32_t)copied_token<WINDOW>(span, first_token(s) + key_row(i)))];
         }
     };
     // All entries count as waited for here, where the copies are waited for too:
@@ -224,14 +251,25 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     };
     const auto locate = [&](int s) {
         if constexpr (WHOLE) {
-            const int first = min(s * kTileKeys + 8 * wave, keys - 1);
+            const int first = group_token(s);
             const uint32_t e = block_index(a, (uint32_t)first);
             const bool bad = whole_entry < 0 || whole_entry >= a.num_blocks;
             met_bad |= bad;
             const int64_t off = kv_offset(a, bad ? 0 : whole_entry, (uint32_t)first - e * (uint32_t)a.block_size, hk);
             kbase = a.kcache + off;
             vbase = a.vcache + off;
-            if (s * kTileKeys + 8 * wave + 8 > keys) {  // the last keys
+            if constexpr (WINDOW) {
+                // Tokens that no row sees give way to one that is: the group's last of the
+                // first tokens, or the oldest of the window, or the last of all.
+                const int f = first_token(s) + 8 * wave;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const int tok = first_token(s) + key_row(i);
+                    int use = min(tok, keys - 1);
+                    if (tok >= span.first && tok < span.old) use = f < span.first ? span.first - 1 : span.old;
+                    lane_at[i] = (uint32_t)(first == f ? use - first : 0) * slot_bytes;
+                }
+            } else if (s * kTileKeys + 8 * wave + 8 > keys) {  // the last keys
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i)
                     lane_at[i] = (uint32_t)min(key_row(i) - 8 * wave, keys - 1 - first) * slot_bytes;
@@ -239,7 +277,8 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
         } else {
 #pragma unroll
             for (int i = 0; i < kCopies; ++i) {
-                const uint32_t tok = (uint32_t)min(s * kTileKeys + key_row(i), keys - 1), e = block_index(a, tok);
+                const uint32_t tok = (uint32_t)copied_token<WINDOW>(span, first_token(s) + key_row(i));
+                const uint32_t e = block_index(a, tok);
                 const bool bad = entry[i] < 0 || entry[i] >= a.num_blocks;
                 met_bad |= bad;
                 at[i] = kv_offset(a, bad ? 0 : entry[i], tok - e * (uint32_t)a.block_size, hk);
@@ -300,12 +339,13 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
                 }
             }
             if (active) {
-                if ((s + 1) * kTileKeys > wave_least) {
+                const int tok = first_token(s);
+                if (partly_seen<WINDOW, kTileKeys>(a, tok, wave_least, wave_most)) {
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
-                            z[u][i] = s * kTileKeys + 32 * u + score_key(i, lane) < ctx ? z[u][i] : kNegInf;
+                            z[u][i] = sees<WINDOW>(a, ctx, tok + 32 * u + score_key(i, lane)) ? z[u][i] : kNegInf;
                 }
                 softmax_step<DT>(z, a.scale_log2, ref, total, o);
 #pragma unroll
@@ -374,20 +414,20 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     }
     if (anew || mend) {
         __threadfence_block();  // what this wave wrote is read back
-        mend_pairs<DT, D>(launch_args(), w.req, w.row0, w.rows, wave, hk, s0 * kTileKeys, steps * kTileKeys, wave_most,
-                          anew, total, dest);
+        mend_pairs<DT, D, WINDOW>(launch_args(), w.req, w.row0, w.rows, wave, hk, span, s0, steps, wave_most, anew,
+                                  total, dest);
     }
 }
 
 // one workgroup per tile
-template <int DT, int D, bool WHOLE>
+template <int DT, int D, bool WHOLE, bool WINDOW>
 __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_kernel(AttnArgs a) {
     __shared__ TileShared<D> sh;
     int hk, slot;
     RowTile w;
     if (!place_of(a, a.slots, blockIdx.x, hk, slot) || !find_tile(a, slot, w)) return;
     w.req = __builtin_amdgcn_readfirstlane(w.req);
-    run_steps<DT, D, WHOLE>(a, sh, w, hk, 0, 0x7FFFFFFF, nullptr);
+    run_steps<DT, D, WHOLE, WINDOW>(a, sh, w, hk, 0, 0x7FFFFFFF, nullptr);
 }
 
 // Cut launch: every tile's steps are cut into pieces of about `piece` steps, one per
@@ -404,7 +444,7 @@ struct TileSpan {
     int row0, rows;
 };
 
-template <int DT, int D, bool WHOLE>
+template <int DT, int D, bool WHOLE, bool WINDOW>
 __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs a) {
     __shared__ TileShared<D> sh;
     // pieces of the slots before (at most 1,280), and, shifted by 16, those of cut tiles
@@ -412,16 +452,19 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
     __shared__ int32_t before[kMaxSlots + 1];
     __shared__ int32_t steps_of[kMaxSlots + 1];  // steps of the slot; first its largest visible count
     __shared__ int32_t wave_sums[kTileWaves], sums[2];
+    __shared__ int32_t lows[WINDOW ? kMaxSlots + 1 : 1];  // each slot's smallest visible count
     __shared__ Requests requests;
     const int t = threadIdx.x, slots = a.slots;
     constexpr int kPer = kMaxSlots / kTileThreads;
     if (t < 2) sums[t] = 0;
-    slot_counts<kTileThreads>(a, requests, steps_of);
+    slot_counts<kTileThreads, WINDOW>(a, requests, steps_of, lows);
     int u[kPer], steps = 0, tiles = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         const int slot = t * kPer + i, keys = slot < slots ? steps_of[slot] : -1;
-        u[i] = keys < 0 ? 0 : max((keys + kTileKeys - 1) / kTileKeys, 1);  // rows that see nothing are written too
+        u[i] = 0;
+        if (keys >= 0)  // rows that see nothing are written too
+            u[i] = max(span_steps<kTileKeys>(key_span<WINDOW, kTileKeys>(a, keys, WINDOW ? lows[slot] : 0)), 1);
         steps += u[i];
         tiles += keys >= 0;
     }
@@ -477,8 +520,8 @@ __global__ __launch_bounds__(kTileThreads, 2) void attn_tile_cut_kernel(AttnArgs
     w.row0 = __builtin_amdgcn_readfirstlane(w.row0);
     w.rows = __builtin_amdgcn_readfirstlane(w.rows);
     float *dest = n > 1 ? a.part + (int64_t)(hk * cut_per_head + cut_before(slot) + j) * kTilePart<D> : nullptr;
-    run_steps<DT, D, WHOLE>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)((int64_t)all * j / n)),
-                            __builtin_amdgcn_readfirstlane((int)((int64_t)all * (j + 1) / n)), dest);
+    run_steps<DT, D, WHOLE, WINDOW>(a, sh, w, hk, __builtin_amdgcn_readfirstlane((int)((int64_t)all * j / n)),
+                                    __builtin_amdgcn_readfirstlane((int)((int64_t)all * (j + 1) / n)), dest);
 }
 
 template <int DT, int D>
@@ -495,16 +538,16 @@ __global__ __launch_bounds__(kJoinThreads) void attn_tile_join_kernel(AttnArgs a
         a.lse ? a.lse + (int64_t)row * (a.num_kv_heads * a.group) + head : nullptr);
 }
 
-template <int DT, int D, bool WHOLE>
+template <int DT, int D, bool WHOLE, bool WINDOW>
 hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
     if (!a.part) {
-        hipLaunchKernelGGL((attn_tile_kernel<DT, D, WHOLE>), dim3(place_grid(a.num_kv_heads, a.slots)),
+        hipLaunchKernelGGL((attn_tile_kernel<DT, D, WHOLE, WINDOW>), dim3(place_grid(a.num_kv_heads, a.slots)),
                            dim3(kTileThreads), 0, s, a);
         return hipGetLastError();
     }
     // at most kStreamGroups pieces and one more per tile
     const int64_t per_head = a.slots + kStreamGroups / a.num_kv_heads + 1;
-    hipLaunchKernelGGL((attn_tile_cut_kernel<DT, D, WHOLE>), dim3(place_grid(a.num_kv_heads, per_head)),
+    hipLaunchKernelGGL((attn_tile_cut_kernel<DT, D, WHOLE, WINDOW>), dim3(place_grid(a.num_kv_heads, per_head)),
                        dim3(kTileThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -514,17 +557,20 @@ hipError_t run_tile(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <int DT>
+template <int DT, bool WINDOW>
 hipError_t run_dim(const AttnArgs &a, hipStream_t s) {
     const bool whole = a.block_size % 8 == 0 && a.kv_slot < (1u << 25);
-    if (a.head_dim == 128) return whole ? run_tile<DT, 128, true>(a, s) : run_tile<DT, 128, false>(a, s);
-    return whole ? run_tile<DT, 64, true>(a, s) : run_tile<DT, 64, false>(a, s);
+    if (a.head_dim == 128) return whole ? run_tile<DT, 128, true, WINDOW>(a, s) : run_tile<DT, 128, false, WINDOW>(a, s);
+    return whole ? run_tile<DT, 64, true, WINDOW>(a, s) : run_tile<DT, 64, false, WINDOW>(a, s);
 }
 
 }  // namespace
 
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s) {
-    return a.dtype == kBF16 ? run_dim<kBF16>(a, s) : run_dim<kFP16>(a, s);
+    return a.dtype == kBF16 ? run_dim<kBF16, false>(a, s) : run_dim<kFP16, false>(a, s);
+}
+hipError_t launch_window_tile(const AttnArgs &a, hipStream_t s) {
+    return a.dtype == kBF16 ? run_dim<kBF16, true>(a, s) : run_dim<kFP16, true>(a, s);
 }
 
 int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles) {

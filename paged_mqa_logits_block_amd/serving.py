@@ -79,6 +79,9 @@ def _declare():
             ("qsa_paged_attention", [vp] * 8 + [p(AttnShape), vp, i64, vp], ctypes.c_int),
             ("qsa_paged_attention_check", [vp] * 7 + [p(AttnShape), vp, i64], ctypes.c_int),
             ("qsa_paged_attention_workspace_bytes", [p(AttnShape)], i64),
+            ("qsa_window_attention", [vp] * 6 + [i32, i32, vp, vp, p(AttnShape), vp, i64, vp], ctypes.c_int),
+            ("qsa_window_attention_check", [vp] * 6 + [i32, i32, vp, p(AttnShape), vp, i64], ctypes.c_int),
+            ("qsa_window_attention_workspace_bytes", [p(AttnShape), i32, i32], i64),
             ("qsa_sparse_attention", [vp] * 6 + [i32, i32, vp, vp, vp, p(AttnShape), vp, i64, vp], ctypes.c_int),
             ("qsa_sparse_attention_check", [vp] * 6 + [i32, i32, vp, p(AttnShape), vp, i64], ctypes.c_int),
             ("qsa_sparse_attention_workspace_bytes", [p(AttnShape), i32, i32], i64)):
@@ -538,6 +541,38 @@ class PreparedPagedAttention(_Prepared):
         return self.out
 
 
+class PreparedWindowAttention(_Prepared):
+    """A validated ``qsa_window_attention`` call on fixed tensors (see
+    PreparedPagedAttention)."""
+
+    def __init__(self, q, kcache, vcache, block_table, ctx_lens, q_starts, out, *, window: int, sinks: int = 0, lse=None,
+                 scale: Optional[float] = None, workspace="auto", stream=None):
+        import torch
+        dev = _one_device(q=q, kcache=kcache, vcache=vcache, block_table=block_table, ctx_lens=ctx_lens,
+                          q_starts=q_starts, out=out, lse=lse)
+        _attn_checks(q, kcache, vcache, block_table, out, lse)
+        _check_rows_i32("ctx_lens", ctx_lens, int(q.shape[0]))
+        _rows("q_starts", q_starts, int(block_table.shape[0]) + 1, torch.int32)
+        window, sinks = int(window), int(sinks)
+        _require(1 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31, "window must be >= 1 and sinks >= 0, both below 2^31")
+        self.shape = make_attn_shape(q, kcache, block_table, out=out, scale=scale)
+        shape = ctypes.byref(self.shape)
+        args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(ctx_lens), _ptr(q_starts), window, sinks,
+                _ptr(out))
+        _raise_on(lib.qsa_window_attention_check(*args, shape, None, 0))
+        with _on(stream, dev):
+            ws = self.workspace = _scratch(workspace,
+                                           int(lib.qsa_window_attention_workspace_bytes(shape, window, sinks)), dev)
+        _raise_on(lib.qsa_window_attention_check(*args, shape, _ptr(ws), _nbytes(ws)))
+        self.out, self.lse = out, lse
+        self._ready(lib.qsa_window_attention, (*args, _ptr(lse), shape, _ptr(ws), _nbytes(ws)), dev, stream,
+                    (q, kcache, vcache, block_table, ctx_lens, q_starts, out, lse, ws))
+
+    def __call__(self):
+        self._launch()
+        return self.out
+
+
 class PreparedSparseAttention(_Prepared):
     """A validated ``qsa_sparse_attention`` call on fixed tensors (see
     PreparedPagedAttention)."""
@@ -588,6 +623,20 @@ def paged_attention(q, kcache, vcache, block_table, ctx_lens, q_starts, *, scale
                                       workspace=workspace)()
 
 
+def window_attention(q, kcache, vcache, block_table, ctx_lens, q_starts, *, window: int, sinks: int = 0,
+                     scale: Optional[float] = None, out=None, lse=None, workspace="auto", stream=None):
+    """``qsa_window_attention``: ``paged_attention`` in which row r sees the newest ``window`` of
+    its ``ctx_lens[r]`` tokens and the first ``sinks``; blocks that no row of a request sees any
+    more may have been freed.  Returns out."""
+    import torch
+    _one_device(q=q)
+    with _on(stream, q.device):
+        if out is None:  # rows outside all requests are not written
+            out = torch.zeros(tuple(q.shape), dtype=q.dtype, device=q.device)
+        return PreparedWindowAttention(q, kcache, vcache, block_table, ctx_lens, q_starts, out, window=window,
+                                       sinks=sinks, lse=lse, scale=scale, workspace=workspace)()
+
+
 def sparse_attention(q, kcache, vcache, block_table, row_to_req, idx, *, ratio: int = 1, token_lens=None,
                      scale: Optional[float] = None, out=None, lse=None, workspace="auto", stream=None):
     """``qsa_sparse_attention``: the same over the tokens of the selected columns
@@ -605,6 +654,11 @@ def sparse_attention(q, kcache, vcache, block_table, row_to_req, idx, *, ratio: 
 def paged_attention_workspace_bytes(shape: AttnShape) -> int:
     """``qsa_paged_attention_workspace_bytes`` (see ``make_attn_shape``)."""
     return int(lib.qsa_paged_attention_workspace_bytes(ctypes.byref(shape)))
+
+
+def window_attention_workspace_bytes(shape: AttnShape, window: int, sinks: int = 0) -> int:
+    """``qsa_window_attention_workspace_bytes`` (see ``make_attn_shape``)."""
+    return int(lib.qsa_window_attention_workspace_bytes(ctypes.byref(shape), int(window), int(sinks)))
 
 
 def sparse_attention_workspace_bytes(shape: AttnShape, k: int, ratio: int = 1) -> int:

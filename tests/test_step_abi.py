@@ -98,11 +98,55 @@ def test_verify_workspace():
     assert m.lib.qsa_verify_drafts_workspace_bytes(None) == 0
 
 
+def attn_shape(**kw):
+    base = dict(num_rows=36, num_heads=32, num_kv_heads=4, head_dim=128, block_size=16, num_reqs=9, max_blocks=1000,
+                dtype=m.BF16, scale=0.1, num_blocks=9000, q_row_stride=4096, q_head_stride=128, out_row_stride=4096,
+                out_head_stride=128, kv_block_stride=16 * 512, kv_slot_stride=512, kv_head_stride=128)
+    base.update(kw)
+    return m.AttnShape(**base)
+
+
+@pytest.mark.parametrize("window,sinks,kw,status", [
+    (4096, 4, {}, "OK"), (1, 0, {}, "OK"), (2 ** 31 - 1, 2 ** 31 - 1, {}, "OK"), (100, 4, dict(num_rows=0), "OK"),
+    (0, 4, {}, "E_INVALID"), (-5, 4, {}, "E_INVALID"), (100, -1, {}, "E_INVALID"), (100, 4, dict(num_heads=30), "E_INVALID"),
+    (100, 4, dict(scale=0.0), "E_INVALID"), (100, 4, dict(head_dim=96), "E_UNSUPPORTED"),
+    (100, 4, dict(dtype=m.FP8_E4M3FN), "E_DTYPE"), (100, 4, dict(max_blocks=1 << 27), "E_RANGE"),
+    (100, 4, dict(q_head_stride=132), "E_ALIGN"),
+])
+def test_window_check(window, sinks, kw, status):
+    s = attn_shape(**kw)
+    assert m.lib.qsa_window_attention_check(A, A, A, A, A, A, window, sinks, A, s, None, 0) == getattr(m, status)
+
+
+def test_window_pointers_and_workspace():
+    s = attn_shape()
+    check = m.lib.qsa_window_attention_check
+    for i in range(7):
+        ptrs = [A] * 7
+        ptrs[i] = None
+        assert check(*ptrs[:6], 100, 4, ptrs[6], s, None, 0) == m.E_INVALID
+    assert check(A, A, A, A, A, A, 100, 4, A, None, None, 0) == m.E_INVALID
+    need = m.window_attention_workspace_bytes(s, 4096, 4)
+    assert need > 0
+    assert check(A, A, A, A, A, A, 4096, 4, A, s, A, need) == m.OK
+    assert check(A, A, A, A, A, A, 4096, 4, A, s, A, need - 1) == m.E_INVALID
+    assert check(A, A, A, A, A, A, 4096, 4, A, s, A + 4, need) == m.E_ALIGN
+    assert m.window_attention_workspace_bytes(s, 100, 4) == 0       # a short window is not cut
+    assert m.window_attention_workspace_bytes(s, 0, 4) == m.window_attention_workspace_bytes(s, 100, -1) == 0
+    assert m.window_attention_workspace_bytes(attn_shape(num_rows=0), 4096, 4) == 0
+    # tables whose steps do not add up in 32 bits are not cut, however short the window
+    big = dict(num_rows=500, num_reqs=500, block_size=1024, num_heads=8, num_kv_heads=1)
+    assert m.window_attention_workspace_bytes(attn_shape(max_blocks=1 << 17, **big), 4096, 4) > 0
+    assert m.window_attention_workspace_bytes(attn_shape(max_blocks=1 << 19, **big), 4096, 4) == 0
+
+
 def test_host_tensors_are_refused():
     q = torch.zeros(4, 8, 64, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
     p = torch.zeros(4, 10)
-    for call in (lambda: m.norm_rope(q, q, i, torch.zeros(8, dtype=torch.float64)),
+    kc = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    for call in (lambda: m.window_attention(q, kc, kc, i.view(1, 4), i, i[:2], window=4),
+                 lambda: m.norm_rope(q, q, i, torch.zeros(8, dtype=torch.float64)),
                  lambda: m.verify_drafts(p, i, i[:3], p[:, 0].contiguous(), p[0, :2], max_tokens=2)):
         with pytest.raises(m.QsaError) as e:
             call()
