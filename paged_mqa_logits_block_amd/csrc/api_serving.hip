@@ -218,6 +218,20 @@ qsa_status check_verify(const float *probs, const float *draft_probs, const int3
     return ok();
 }
 
+int32_t verify_spans(const qsa_verify_shape *s) { return (s->vocab + qsa::kVerifySpan - 1) / qsa::kVerifySpan; }
+
+// One workgroup per request takes one launch, but a row's entries pass through one CU; many
+// requests of few entries leave most of its waves idle.  us whole / split, drafter without
+// and with probabilities: 9 requests of 16,000 entries 6.0 / 8.0, 6.2 / 8.3; of 32,000
+// 7.9 / 8.1, 8.1 / 8.3; of 40,000 9.1 / 8.2, 9.6 / 8.4; of 131,072 19.2 / 8.1, 19.8 / 8.3;
+// 257 requests of 16,000 7.1 / 9.9, 8.8 / 11.6; of 100,003 29.3 / 24.6, 38.7 / 36.8; 512 of
+// 16,000 9.9 / 11.8, 14.5 / 17.2; 1,024 of 2,000 10.3 / 9.2, 13.6 / 10.8; 4,096 of 2,000
+// 38 / 18, 45 / 26.  (Two workgroups to every CU are the exception: 512 of 131,072 57 / 73, 89 /
+// 107.)  The grid of a split launch has a row per request.
+bool verify_split(const qsa_verify_shape *s) {
+    return s->num_reqs <= 65535 && (s->vocab > 32768 || s->num_reqs > 768);
+}
+
 // Calls with up to this many stacked pairs per kv head and request on average are
 // streamed, small ones at least (the lengths are on the device).  One request, 4 kv
 // heads of 8 query heads at D = 128, us streamed / by the tile kernel: 16 rows of
@@ -535,7 +549,7 @@ qsa_status qsa_norm_rope(const void *q, const void *k, const void *v, const floa
 
 int64_t qsa_verify_drafts_workspace_bytes(const qsa_verify_shape *s) {
     if (check_verify_sizes(s) != QSA_OK || s->num_reqs == 0) return 0;
-    return 0;
+    return verify_split(s) ? qsa::verify_workspace_bytes(s->num_reqs, verify_spans(s)) : 0;
 }
 
 qsa_status qsa_verify_drafts_check(const float *probs, const float *draft_probs, const int32_t *tokens,
@@ -558,8 +572,7 @@ qsa_status qsa_verify_drafts(const float *probs, const float *draft_probs, const
     const int64_t need = qsa_verify_drafts_workspace_bytes(s);
     qsa::VerifyArgs a = {probs, draft_probs, tokens, q_starts, uniforms, sample_uniforms, out_tokens, num_tokens,
                          need > 0 ? static_cast<double *>(workspace) : nullptr, s->num_rows, s->num_reqs, s->vocab,
-                         s->max_tokens, (s->vocab + qsa::kVerifySpan - 1) / qsa::kVerifySpan, s->prob_stride,
-                         s->draft_stride};
+                         s->max_tokens, verify_spans(s), s->prob_stride, s->draft_stride};
     return launched(qsa::launch_verify(a, static_cast<hipStream_t>(stream)));
 }
 

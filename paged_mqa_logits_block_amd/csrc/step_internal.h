@@ -41,5 +41,7 @@ struct VerifyArgs {
 };
 
 hipError_t launch_verify(const VerifyArgs &a, hipStream_t s);
+// bytes of a split launch's workspace
+int64_t verify_workspace_bytes(int64_t num_reqs, int64_t spans);
 
 }  // namespace qsa

@@ -15,23 +15,24 @@
 namespace qsa {
 namespace {
 
-constexpr int kVerifyThreads = 256;
-constexpr int kVerifyWaves = kVerifyThreads / kWave;
 constexpr int kMaxSpans = kVerifyMaxVocab / kVerifySpan;
-typedef float f32x4_a4 __attribute__((ext_vector_type(4), aligned(4)));  // rows start at any element
 
 struct Verdict {
     int row0, rows, kept;  // rows: at most max_tokens are looked at
     bool every;            // all drafts were kept
 };
 
-// by a whole wave
-__device__ __forceinline__ Verdict judge(const VerifyArgs &a, int req) {
-    Verdict v;
+__device__ __forceinline__ Verdict rows_of(const VerifyArgs &a, int req) {
+    Verdict v = {};
     v.row0 = min(max(a.q_starts[req], 0), a.num_rows);
     v.rows = min(min(max(a.q_starts[req + 1], 0), a.num_rows) - v.row0, a.max_tokens);
+    return v;
+}
+
+// by a whole wave
+__device__ __forceinline__ Verdict judge(const VerifyArgs &a, int req) {
+    Verdict v = rows_of(a, req);
     const int drafts = v.rows - 1;
-    v.kept = 0;
     while (v.kept < drafts) {
         const int j = v.kept + lane_id();
         bool good = false;
@@ -54,10 +55,10 @@ __device__ __forceinline__ Verdict judge(const VerifyArgs &a, int req) {
     return v;
 }
 
-// The weights of a request's next token.
+// The weights of a request's next token: p, less q where that is not null.
 struct Weights {
-    const float *p, *q;  // q null: none, or the draft's alone
-    int without;         // an entry of weight 0, or -1
+    const float *p, *q;
+    int without;  // an entry of weight 0, or -1
 };
 __device__ __forceinline__ Weights weights_of(const VerifyArgs &a, const Verdict &v) {
     const int64_t row = v.row0 + v.kept;
@@ -69,222 +70,279 @@ __device__ __forceinline__ Weights weights_of(const VerifyArgs &a, const Verdict
     return w;
 }
 
-// what is not a positive number has no weight
-__device__ __forceinline__ float weight(float x) { return x > 0.0f && x < __builtin_inff() ? x : 0.0f; }
+// What is not a positive number has no weight: as unsigned numbers, the bits of infinity,
+// of NaN and of everything with a sign are not below those of infinity.
+__device__ __forceinline__ float weight(float x) { return __float_as_uint(x) < 0x7F800000u ? x : 0.0f; }
 
-// four entries from `at` on (behind the vocabulary: weight 0): what p has over q, and p
-__device__ __forceinline__ void load4(const Weights &w, int vocab, int at, float (&rest)[4], float (&target)[4]) {
-    float p[4] = {0.0f, 0.0f, 0.0f, 0.0f}, q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (at + 4 <= vocab) {
-        const f32x4 x = *reinterpret_cast<const f32x4_a4 *>(w.p + at);
-        f32x4 y = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (w.q) y = *reinterpret_cast<const f32x4_a4 *>(w.q + at);
+template <int N>
+struct Entries;
+template <>
+struct Entries<4> {
+    typedef float V __attribute__((ext_vector_type(4), aligned(4)));  // rows start at any element
+};
+template <>
+struct Entries<2> {
+    typedef float V __attribute__((ext_vector_type(2), aligned(4)));
+};
+
+// the weights of N entries from `at` on, 0 behind the vocabulary
+template <int N>
+__device__ __forceinline__ void load_weights(const Weights &w, int vocab, int at, float (&x)[N]) {
+    typedef typename Entries<N>::V V;
+    if (at + N <= vocab) {
+        const V p = *reinterpret_cast<const V *>(w.p + at);
+        if (w.q) {
+            const V q = *reinterpret_cast<const V *>(w.q + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[i] = x[i];
-            q[i] = y[i];
+            for (int i = 0; i < N; ++i) x[i] = p[i] - q[i];
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = p[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (at + i >= vocab) continue;
-            p[i] = w.p[at + i];
-            if (w.q) q[i] = w.q[at + i];
+        for (int i = 0; i < N; ++i) {
+            x[i] = 0.0f;
+            if (at + i < vocab) x[i] = w.p[at + i] - (w.q ? w.q[at + i] : 0.0f);
         }
     }
+    if (w.without >= 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        target[i] = weight(p[i]);
-        rest[i] = at + i == w.without ? 0.0f : weight(p[i] - q[i]);
+        for (int i = 0; i < N; ++i) x[i] = at + i == w.without ? 0.0f : x[i];
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = weight(x[i]);
 }
 
-__device__ __forceinline__ double xor_lane_d(double v, int m) {
+// v plus v of the lane that the DPP pattern takes from (0 where there is none)
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_add(double v) {
     const int64_t b = __builtin_bit_cast(int64_t, v);
-    const uint32_t lo = (uint32_t)xor_lane_i((int)b, m), hi = (uint32_t)xor_lane_i((int)(b >> 32), m);
-    return __builtin_bit_cast(double, (int64_t)((uint64_t)hi << 32 | lo));
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, CTRL, ROWS, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
+    return v + __builtin_bit_cast(double, (int64_t)((uint64_t)hi << 32 | lo));
 }
-__device__ __forceinline__ double shfl_d(double v, int src) {
+// Inclusive sums over the wave, in the order of the six steps (LDS permutations in
+// their place took 2 us more per call).  All lanes active.
+__device__ __forceinline__ double wave_incl_sum_d(double v) {
+    v = dpp_add<kDppRowShr1, 0xF>(v);
+    v = dpp_add<kDppRowShr2, 0xF>(v);
+    v = dpp_add<kDppRowShr4, 0xF>(v);
+    v = dpp_add<kDppRowShr8, 0xF>(v);
+    v = dpp_add<kDppRowBcast15, 0xA>(v);
+    return dpp_add<kDppRowBcast31, 0xC>(v);
+}
+// the value of the lane before, 0 in lane 0
+__device__ __forceinline__ double lane_before_d(double v) {
+    constexpr int kDppWaveShr1 = 0x138;
     const int64_t b = __builtin_bit_cast(int64_t, v);
-    const uint32_t lo = (uint32_t)shfl_i((int)b, src), hi = (uint32_t)shfl_i((int)(b >> 32), src);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, kDppWaveShr1, 0xF, 0xF, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), kDppWaveShr1, 0xF, 0xF, false);
     return __builtin_bit_cast(double, (int64_t)((uint64_t)hi << 32 | lo));
 }
 
-// a span's sums of both kinds of weights, by one wave
-struct Sums {
-    double rest, target;
-};
-__device__ __forceinline__ Sums span_sums(const Weights &w, int vocab, int span) {
+// a span's sum, by one wave; in the last lane
+__device__ __forceinline__ double span_sum(const Weights &w, int vocab, int span) {
     constexpr int kSteps = kVerifySpan / (4 * kWave);
-    Sums s = {0.0, 0.0};
+    double sum[2] = {0.0, 0.0};
+    float x[kSteps][4];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        float rest[4], target[4];
-        load4(w, vocab, span * kVerifySpan + 4 * (kWave * i + lane_id()), rest, target);
+    for (int i = 0; i < kSteps; ++i) load_weights<4>(w, vocab, span * kVerifySpan + 4 * (kWave * i + lane_id()), x[i]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            s.rest += (double)rest[j];
-            s.target += (double)target[j];
-        }
-    }
+    for (int i = 0; i < kSteps; ++i)
 #pragma unroll
-    for (int m = 1; m < kWave; m <<= 1) {
-        s.rest += xor_lane_d(s.rest, m);
-        s.target += xor_lane_d(s.target, m);
-    }
-    return s;
+        for (int j = 0; j < 4; ++j) sum[j & 1] += (double)x[i][j];
+    return wave_incl_sum_d(sum[0] + sum[1]);
 }
 
 // What the workgroup's threads share while they look for the token.
+template <int THREADS>
 struct Search {
-    double wave_sum[kVerifyWaves];
-    int32_t first[kVerifyWaves], last[kVerifyWaves];
+    double wave_sum[2][THREADS / kWave], base;
+    uint32_t key[2][THREADS / kWave];
+    double spans[kMaxSpans];
 };
 
-// The sum of the threads before this one, and the total, in a fixed order.
-__device__ __forceinline__ double block_before(Search &sh, double v, double &total) {
-    const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
-    double inc = v;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-        const double u = shfl_d(inc, lane >= d ? lane - d : lane);
-        if (lane >= d) inc += u;
-    }
+// Of the threads' `first` (an index, or INT_MAX) the least, or where none has one the
+// largest `last` (-1: none).
+template <int THREADS>
+__device__ __forceinline__ int block_pick(uint32_t (&key)[THREADS / kWave], int first, int last) {
+    uint32_t k = wave_total_umax(first != 0x7FFFFFFF ? 0xFFFFFFFFu - (uint32_t)first : (uint32_t)(last + 1));
+    if (lane_id() == 0) key[threadIdx.x >> 6] = k;
     __syncthreads();
-    if (lane == kWave - 1) sh.wave_sum[wave] = inc;
+#pragma unroll
+    for (int i = 0; i < THREADS / kWave; ++i) k = max(k, key[i]);
+    return k & 0x80000000u ? (int)(0xFFFFFFFFu - k) : (int)k - 1;
+}
+
+// the sum of the threads before this one; total: of all
+template <int THREADS>
+__device__ __forceinline__ double block_before(double (&wave_sum)[THREADS / kWave], double v, double &total) {
+    const int wave = threadIdx.x >> 6;
+    const double inc = wave_incl_sum_d(v);
+    if (lane_id() == kWave - 1) wave_sum[wave] = inc;
     __syncthreads();
     double before = 0.0;
     total = 0.0;
-    for (int i = 0; i < kVerifyWaves; ++i) {
-        if (i < wave) before += sh.wave_sum[i];
-        total += sh.wave_sum[i];
+#pragma unroll
+    for (int i = 0; i < THREADS / kWave; ++i) {
+        const double x = wave_sum[i];
+        before += i < wave ? x : 0.0;
+        total += x;
     }
-    const double in = shfl_d(inc, lane > 0 ? lane - 1 : 0);  // exclusive
-    return lane > 0 ? before + in : before;
+    return before + lane_before_d(inc);
 }
 
-// The least of the threads' `first`, or where all are INT_MAX the largest `last`.
-__device__ __forceinline__ int block_pick(Search &sh, int first, int last) {
+// The entry of the weights in which u falls, from their spans' sums, by the workgroup: the
+// first one whose cumulative weight passes u * total, or the last one with weight; -1
+// where none has any.
+template <int THREADS>
+__device__ __forceinline__ int find(const VerifyArgs &a, Search<THREADS> &sh, const double *spans, const Weights &w,
+                                    float u) {
+    constexpr int kPer = (kMaxSpans + THREADS - 1) / THREADS, kEach = kVerifySpan / THREADS;
     const int t = threadIdx.x;
-    first = -wave_max_i(-first);
-    last = wave_max_i(last);
-    __syncthreads();
-    if ((t & 63) == 0) {
-        sh.first[t >> 6] = first;
-        sh.last[t >> 6] = last;
-    }
-    __syncthreads();
-    for (int i = 0; i < kVerifyWaves; ++i) {
-        first = min(first, sh.first[i]);
-        last = max(last, sh.last[i]);
-    }
-    return first != 0x7FFFFFFF ? first : last;
-}
-
-// The request's next token from its spans' sums, by the workgroup: the first entry whose
-// cumulative weight passes u * total, or the last one with weight, or -1.
-__device__ __forceinline__ int choose(const VerifyArgs &a, Search &sh, const Sums *spans, const Weights &w, float u) {
-    constexpr int kPer = kMaxSpans / kVerifyThreads, kEach = kVerifySpan / kVerifyThreads;
-    const int t = threadIdx.x;
-    double rest[kPer], target[kPer], sums[2] = {0.0, 0.0};
+    double s[kPer], sum = 0.0, total;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const int s = kPer * t + i;
-        rest[i] = s < a.spans ? spans[s].rest : 0.0;
-        target[i] = s < a.spans ? spans[s].target : 0.0;
-        sums[0] += rest[i];
-        sums[1] += target[i];
+        s[i] = kPer * t + i < a.spans ? spans[kPer * t + i] : 0.0;
+        sum += s[i];
     }
-    double total, all;
-    double before = block_before(sh, sums[0], total);
-    const double other = block_before(sh, sums[1], all);
-    const bool use_target = !(total > 0.0);  // p is nowhere above q
-    if (use_target) {
-        before = other;
-        total = all;
-    }
+    const double begin = block_before<THREADS>(sh.wave_sum[0], sum, total);
     if (!(total > 0.0)) return -1;
     const double goal = (double)u * total;
     int first = 0x7FFFFFFF, last = -1;
-    double at = before, base = 0.0;
+    double at = begin;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-        const double s = use_target ? target[i] : rest[i];
-        if (s > 0.0) {
+        at += s[i];
+        if (s[i] > 0.0) {
             last = kPer * t + i;
-            if (at + s > goal) first = min(first, kPer * t + i);
-        }
-        at += s;
-    }
-    const int span = block_pick(sh, first, last);
-    // the cumulative sum before the span, from the thread that has it
-    if (span / kPer == t) {
-        base = before;
-        for (int i = 0; i < span % kPer; ++i) base += use_target ? target[i] : rest[i];
-        sh.wave_sum[0] = base;
-    }
-    __syncthreads();
-    base = sh.wave_sum[0];
-    __syncthreads();
-    float x[kEach];
-    double sum = 0.0, unused;
-#pragma unroll
-    for (int i = 0; i < kEach; i += 4) {
-        float r[4], p[4];
-        load4(w, a.vocab, span * kVerifySpan + kEach * t + i, r, p);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            x[i + j] = use_target ? p[j] : r[j];
-            sum += (double)x[i + j];
+            if (at > goal) first = min(first, last);
         }
     }
-    at = base + block_before(sh, sum, unused);
+    const int span = block_pick<THREADS>(sh.key[0], first, last);
+    if (span / kPer == t) {  // this thread has the cumulative weight before the span
+        at = begin;
+#pragma unroll
+        for (int i = 0; i < kPer - 1; ++i)
+            if (i < span % kPer) at += s[i];
+        sh.base = at;
+    }
+    constexpr int kLoad = kEach < 4 ? kEach : 4;
+    float x[kEach / kLoad][kLoad];
+    double in = 0.0;
+#pragma unroll
+    for (int i = 0; i < kEach / kLoad; ++i) {
+        load_weights<kLoad>(w, a.vocab, span * kVerifySpan + kEach * t + kLoad * i, x[i]);
+#pragma unroll
+        for (int j = 0; j < kLoad; ++j) in += (double)x[i][j];
+    }
+    at = block_before<THREADS>(sh.wave_sum[1], in, total);
+    at += sh.base;
     first = 0x7FFFFFFF;
     last = -1;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        at += (double)x[i];
-        if (x[i] > 0.0f) {
+        const float v = x[i / kLoad][i % kLoad];
+        at += (double)v;
+        if (v > 0.0f) {
             last = span * kVerifySpan + kEach * t + i;
             if (at > goal) first = min(first, last);
         }
     }
-    return block_pick(sh, first, last);
+    return block_pick<THREADS>(sh.key[1], first, last);
 }
 
+// all spans' sums, by the workgroup
+template <int THREADS>
+__device__ __forceinline__ void all_spans(const VerifyArgs &a, Search<THREADS> &sh, const Weights &w) {
+    for (int s = threadIdx.x >> 6; s < a.spans; s += THREADS / kWave) {
+        const double x = span_sum(w, a.vocab, s);
+        if (lane_id() == kWave - 1) sh.spans[s] = x;
+    }
+    __syncthreads();
+}
+
+// A request's next token; spans: their sums, or null.
+template <int THREADS>
+__device__ __forceinline__ int next_token(const VerifyArgs &a, Search<THREADS> &sh, const Verdict &v, int req,
+                                          const double *spans) {
+    Weights w = weights_of(a, v);
+    const float u = a.sample_uniforms[req];
+    int token;
+    if (!spans) all_spans<THREADS>(a, sh, w);
+    token = find<THREADS>(a, sh, spans ? spans : sh.spans, w, u);
+    if (token >= 0 || v.every) return token;
+    // p is nowhere above q (or has no weight but the rejected draft's): a token of p
+    w.q = nullptr;
+    w.without = -1;
+    __syncthreads();  // find has returned before its second use of what it shares
+    all_spans<THREADS>(a, sh, w);
+    return find<THREADS>(a, sh, sh.spans, w, u);
+}
+
+template <int THREADS>
 __device__ __forceinline__ void write_tokens(const VerifyArgs &a, int req, const Verdict &v, int token) {
     int32_t *out = a.out_tokens + (int64_t)req * a.max_tokens;
-    for (int j = threadIdx.x; j < a.max_tokens; j += kVerifyThreads)
+    for (int j = threadIdx.x; j < a.max_tokens; j += THREADS)
         out[j] = v.rows <= 0 || j > v.kept ? -1 : j < v.kept ? a.tokens[v.row0 + j + 1] : token;
     if (threadIdx.x == 0) a.num_tokens[req] = v.rows <= 0 ? 0 : v.kept + 1;
 }
 
 // one workgroup per request
-__global__ __launch_bounds__(kVerifyThreads) void verify_kernel(VerifyArgs a) {
-    __shared__ Search sh;
-    __shared__ Sums spans[kMaxSpans];
-    const int req = blockIdx.x, wave = threadIdx.x >> 6;
+constexpr int kWholeThreads = 512;
+__global__ __launch_bounds__(kWholeThreads) void verify_kernel(VerifyArgs a) {
+    __shared__ Search<kWholeThreads> sh;
+    const int req = blockIdx.x;
     const Verdict v = judge(a, req);
-    int token = -1;
-    if (v.rows > 0) {
-        const Weights w = weights_of(a, v);
-        for (int s = wave; s < a.spans; s += kVerifyWaves) {
-            const Sums x = span_sums(w, a.vocab, s);
-            if (lane_id() == 0) spans[s] = x;
-        }
-        __syncthreads();
-        token = choose(a, sh, spans, w, a.sample_uniforms[req]);
-    }
-    write_tokens(a, req, v, token);
+    const int token = v.rows > 0 ? next_token<kWholeThreads>(a, sh, v, req, nullptr) : -1;
+    write_tokens<kWholeThreads>(a, req, v, token);
 }
 
-hipError_t run_verify(const VerifyArgs &a, hipStream_t s) {
-    hipLaunchKernelGGL(verify_kernel, dim3((unsigned)a.num_reqs), dim3(kVerifyThreads), 0, s, a);
-    return hipGetLastError();
+// Split launch: a wave per span of every request, then a workgroup per request that looks
+// for the token.  The workspace holds the spans' sums, then the drafts that each
+// request keeps.
+constexpr int kSplitThreads = 256;
+__device__ __forceinline__ int32_t *kept_of(const VerifyArgs &a) {
+    return reinterpret_cast<int32_t *>(a.part + (int64_t)a.num_reqs * a.spans);
+}
+
+__global__ __launch_bounds__(kSplitThreads) void verify_sums_kernel(VerifyArgs a) {
+    const int req = blockIdx.y, span = (int)blockIdx.x * (kSplitThreads / kWave) + (threadIdx.x >> 6);
+    if (span >= a.spans) return;
+    const Verdict v = judge(a, req);
+    if (span == 0 && lane_id() == 0) kept_of(a)[req] = v.kept;
+    if (v.rows <= 0) return;
+    const double x = span_sum(weights_of(a, v), a.vocab, span);
+    if (lane_id() == kWave - 1) a.part[(int64_t)req * a.spans + span] = x;
+}
+
+__global__ __launch_bounds__(kSplitThreads) void verify_find_kernel(VerifyArgs a) {
+    __shared__ Search<kSplitThreads> sh;
+    const int req = blockIdx.x;
+    Verdict v = rows_of(a, req);
+    v.kept = kept_of(a)[req];
+    v.every = v.kept >= v.rows - 1;
+    const int token = v.rows > 0 ? next_token<kSplitThreads>(a, sh, v, req, a.part + (int64_t)req * a.spans) : -1;
+    write_tokens<kSplitThreads>(a, req, v, token);
 }
 
 }  // namespace
 
-hipError_t launch_verify(const VerifyArgs &a, hipStream_t s) { return run_verify(a, s); }
+hipError_t launch_verify(const VerifyArgs &a, hipStream_t s) {
+    if (!a.part) {
+        hipLaunchKernelGGL(verify_kernel, dim3((unsigned)a.num_reqs), dim3(kWholeThreads), 0, s, a);
+        return hipGetLastError();
+    }
+    constexpr int kSpansPer = kSplitThreads / kWave;
+    hipLaunchKernelGGL(verify_sums_kernel, dim3((unsigned)((a.spans + kSpansPer - 1) / kSpansPer), (unsigned)a.num_reqs),
+                       dim3(kSplitThreads), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(verify_find_kernel, dim3((unsigned)a.num_reqs), dim3(kSplitThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+int64_t verify_workspace_bytes(int64_t num_reqs, int64_t spans) { return num_reqs * (spans * (int64_t)sizeof(double) + 4); }
 
 }  // namespace qsa
