@@ -46,6 +46,11 @@ ROPE = [
     ("bf16", 128, 128, 0, False, "qk", 2500, 8, 2, 64, "head", "cache"),
     ("fp16", 64, 48, 16, False, "qk", 2049, 4, 1, 16, "slot", "both"),
     ("bf16", 128, 96, 16, True, "k", 8193, 1, 1, 16, "slot", "both"),
+    # more than 1,024 lanes of a row's heads; more bytes than the L2s hold
+    ("bf16", 128, 128, 0, False, "qk", 3, 130, 10, 16, "slot", "both"),
+    ("fp16", 64, 32, 8, True, "qk", 2, 256, 3, 16, "slot", "cache"),
+    ("bf16", 128, 64, 0, False, "qk", 9000, 6, 2, 64, "head", "both"),
+    ("fp16", 64, 64, 0, True, "q", 20000, 5, 1, 16, "slot", "cache"),
 ]
 
 
