@@ -261,9 +261,9 @@ struct AttnPlan {
     int64_t slots;             // row tiles
     int64_t tiles;             // a cut launch of the streaming kernel: the most tiles with rows
     int64_t bytes;             // workspace of a cut launch, 0: not cut
+    int parts;                 // with a window: parts of a tile
 };
 
-// keys: the most that a tile works through, or with a window about that many
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     AttnPlan p = {};
     const int group = s->num_heads / s->num_kv_heads;
@@ -301,8 +301,7 @@ AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
     const int64_t least = n < R ? n : R, full = (R + T - 1) / T, tiles = (full > least ? full : least) * tile_heads;
     if (p.slots > qsa::kMaxSlots || n > qsa::kMaxSlots || R > kCutRows || tiles > kCutTiles) return p;
     // the workgroups add up the slots' steps of 64 keys in 32 bits
-    const int64_t cap = (int64_t)s->max_blocks * s->block_size;
-    if (p.slots * (cap / 64 + 1) > 0x7FFFFFFF) return p;
+    if (p.slots * (keys / 64 + 1) > 0x7FFFFFFF) return p;
     p.tiles = (R / T + least) * heads;
     if (p.stream && long_keys) p.bytes = qsa::attn_workspace_bytes(s->head_dim, p.tiles);
     if (!p.stream && (n > 1 || fills_badly(tiles)))
@@ -378,10 +377,33 @@ qsa_status check_window(int32_t window, int32_t sinks) {
     return ok();
 }
 
-// what the keys of a windowed call come to
-int64_t window_keys(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
-    const int64_t cap = (int64_t)s->max_blocks * s->block_size, seen = (int64_t)window + sinks;
-    return seen < cap ? seen : cap;
+// A windowed streaming tile works through as many keys as the window, the first tokens and
+// its rows come to, so that all tiles are cut into the same number of parts: with one to
+// a CU at most (a second one on some CUs holds up the others), and no more than make up
+// for the join, which takes about 0.12 us a part where 128 keys take 0.9.  us by parts, 4
+// kv heads of 8 heads at D = 128, windows of 4,096: 1 row 38.2 in 1, 17.1 in 4, 13.3 in 8, 13.1
+// in 14; 9 requests of 4 rows 41.4 in 1, 22.5 in 3, 20.8 in 4, 21.2 in 6, 25.2 in 8; 20 of 4
+// rows 42.7 in 1, 32.8 in 2, 34.0 in 3, 38.1 in 4; 33 of 1 row 49.3 in 1, 63.9 in 2, 50.0 in 3.
+// Windows of 16,384: 9 of 4 rows 179 in 1, 62 in 4, 57 in 6, 74 in 8.  (The tile kernel's
+// tiles are cut as without a window.)
+AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
+    const int64_t cap = (int64_t)s->max_blocks * s->block_size;
+    AttnPlan p = plan_attn(s, false, cap);
+    if (!p.stream) return p;
+    p.bytes = 0;
+    const int64_t seen = (int64_t)window + sinks + p.tile_rows, keys = seen < cap ? seen : cap;
+    constexpr int kUnit = qsa::kStreamKeys * qsa::kWindowWaves;
+    const int64_t units = (keys + kUnit - 1) / kUnit, heads = (int64_t)s->num_kv_heads * p.num_subs;
+    const int64_t reqs = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
+    const int64_t full = (s->num_rows + p.tile_rows - 1) / p.tile_rows, tiles = (full > reqs ? full : reqs) * heads;
+    const int64_t places = (p.slots + 7) / 8 * 8 * heads;  // of tiles, also without rows
+    int n = 1;
+    while (n < qsa::kMaxParts && n < units && (n + 1) * tiles <= qsa::kStreamGroups &&
+           (int64_t)(n + 1) * (n + 1) <= 8 * units && (n + 1) * places <= qsa::kMaxTileParts)
+        ++n;
+    p.parts = n;
+    if (n > 1) p.bytes = qsa::window_workspace_bytes(s->head_dim, places, n);
+    return p;
 }
 
 qsa_status check_workspace(const void *workspace, int64_t bytes, int64_t need) {
@@ -433,6 +455,7 @@ void launch_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.slots = (int32_t)p.slots;
     a.tiles = (int32_t)p.tiles;
     a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
+    a.parts = a.part ? p.parts : 1;
 }
 
 }  // namespace
@@ -608,7 +631,7 @@ qsa_status qsa_paged_attention(const void *q, const void *kcache, const void *vc
 
 int64_t qsa_window_attention_workspace_bytes(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     if (check_attn_sizes(s, false, 0, 0) != QSA_OK || check_window(window, sinks) != QSA_OK || s->num_rows == 0) return 0;
-    return plan_attn(s, false, window_keys(s, window, sinks)).bytes;
+    return plan_window(s, window, sinks).bytes;
 }
 
 qsa_status qsa_window_attention_check(const void *q, const void *kcache, const void *vcache,
@@ -629,7 +652,7 @@ qsa_status qsa_window_attention(const void *q, const void *kcache, const void *v
                                                workspace, workspace_bytes);
     if (st != QSA_OK) return st;
     if (s->num_rows == 0) return ok();
-    const AttnPlan p = plan_attn(s, false, window_keys(s, window, sinks));
+    const AttnPlan p = plan_window(s, window, sinks);
     qsa::AttnArgs a = attn_args(q, kcache, vcache, block_table, out, lse, s);
     a.ctx_lens = ctx_lens;
     a.q_starts = q_starts;

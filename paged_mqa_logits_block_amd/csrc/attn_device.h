@@ -357,12 +357,13 @@ struct KeySpan {
     int keys;        // behind the last token that a row sees
     int first, old;  // tokens of [first, old) are not seen by any row
     int head, gap;
+    int least;       // windows, streaming: the rows' smallest visible count
 };
 
 // hi: the rows' largest visible count, lo: the smallest one above 0
 template <bool WINDOW, int KEYS>
 __device__ __forceinline__ KeySpan key_span(const AttnArgs &a, int hi, int lo) {
-    KeySpan s = {hi, 0, 0, 0, 0};
+    KeySpan s = {hi, 0, 0, 0, 0, 0};
     if constexpr (WINDOW) {
         if (hi <= 0) return s;
         s.first = min(a.sinks, hi);

@@ -12,9 +12,15 @@ constexpr int kAttnTile = 32;
 // Keys per step of a streaming wave, and waves per streaming workgroup.
 constexpr int kStreamKeys = 32;
 constexpr int kStreamWaves = 8;
+// of a windowed call: two workgroups fit a CU, of which one reads while the other starts
+// or ends (257 rows with windows of 1,024 108 us, 114 with 8 waves; 1 row of 4,096 13.1 and 12.3)
+constexpr int kWindowWaves = 4;
 // Workgroups that a cut launch aims at (one per CU), and the most row tiles of one.
 constexpr int kStreamGroups = 256;
 constexpr int kMaxSlots = 1024;
+// The most parts of a windowed streaming tile, and of all tiles (also of slots without
+// rows): their states lie in the workspace.
+constexpr int kMaxParts = 64, kMaxTileParts = 4096;
 
 // Stacked pairs of a workgroup of the tile kernel.
 constexpr int kTilePairs = 256;
@@ -59,6 +65,7 @@ struct AttnArgs {
     int32_t tile_rows;          // query rows per tile
     // window: a row sees its newest `window` tokens and the first `sinks`
     int32_t window, sinks;
+    int32_t parts;              // streaming: of a tile's keys, one to a workgroup
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);
@@ -67,6 +74,8 @@ hipError_t launch_window_tile(const AttnArgs &a, hipStream_t s);
 // bytes of a cut launch's workspace, of the streaming and of the tile kernel
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles);
 int64_t attn_tile_workspace_bytes(int head_dim, int64_t tiles);
+// bytes of the parts of a windowed call's tiles
+int64_t window_workspace_bytes(int head_dim, int64_t tiles, int parts);
 hipError_t launch_attn_tile(const AttnArgs &a, hipStream_t s);
 
 struct PlanArgs {

@@ -40,7 +40,7 @@
 namespace qsa {
 namespace {
 
-constexpr int kStreamThreads = 64 * kStreamWaves;
+constexpr int kStreamThreads = kWave * kStreamWaves;
 
 struct TileWork {
     int req, row0, rows;  // dense: a request's tile; sparse: one row
@@ -90,18 +90,20 @@ __device__ __forceinline__ bool tile_work(const AttnArgs &a, int slot, int hs, T
 
 // keys the tile works through: up to the largest visible count of its rows, or the
 // selected tokens
-template <bool SPARSE, bool WINDOW>
+template <bool SPARSE>
 __device__ __forceinline__ KeySpan tile_keys(const AttnArgs &a, int row0, int rows) {
-    if (SPARSE) return {a.k * a.ratio, 0, 0, 0, 0};
-    int most = 0, low = 0x7FFFFFFF;
-    for (int r = 0; r < rows; ++r) {
-        const int v = visible(a, row0 + r);
-        most = max(most, v);
-        if (WINDOW && v > 0) low = min(low, v);
-    }
-    most = __builtin_amdgcn_readfirstlane(most);
-    low = __builtin_amdgcn_readfirstlane(low);
-    return key_span<WINDOW, kStreamKeys>(a, most, low);
+    if (SPARSE) return {a.k * a.ratio, 0, 0, 0, 0, 0};
+    int most = 0;
+    for (int r = 0; r < rows; ++r) most = max(most, visible(a, row0 + r));
+    return key_span<false, kStreamKeys>(a, __builtin_amdgcn_readfirstlane(most), 0);
+}
+// by a wave, the rows' counts read at once (one after the other they took 1 to 2 us)
+__device__ __forceinline__ KeySpan window_keys(const AttnArgs &a, int row0, int rows) {
+    const int r = lane_id(), v = r < rows ? visible(a, row0 + r) : 0;
+    const int most = (int)wave_total_umax((uint32_t)v), low = 0x7FFFFFFF - (int)wave_total_umax(v > 0 ? 0x7FFFFFFFu - v : 0u);
+    KeySpan s = key_span<true, kStreamKeys>(a, most, low);
+    s.least = 0x7FFFFFFF - (int)wave_total_umax(r < rows ? 0x7FFFFFFFu - v : 0u);
+    return s;
 }
 
 // 8 (D = 128) or 4 copies fill a buffer; wait until at most one buffer's are
@@ -125,8 +127,10 @@ __device__ __forceinline__ float *part_of(const AttnArgs &a, int group, int tile
 // NARROW (selected tokens of up to 16 heads): the 16x16x32 MFMA on 16 pairs instead of
 // the 32x32x16 one on 32, with half the products and half the weights per key.
 // WINDOW: the newest tokens and the first ones only (see KeySpan).
-template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
+// WAVES: of the workgroup.
+template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW, int WAVES = kStreamWaves>
 struct Stream {
+    static constexpr int kThreads = kWave * WAVES;
     static_assert(SPARSE || !NARROW, "dense tiles fill 32 pairs where they can");
     static_assert(!SPARSE || !WINDOW, "a selection is its own window");
     static constexpr int kTileBytes = kStreamKeys * D * 2;  // one buffer of keys or values
@@ -134,10 +138,10 @@ struct Stream {
     static constexpr int kLanesPerKey = D / 8, kKeysPerCopy = kWave / kLanesPerKey;
 
     struct Shared {
-        __align__(16) uint8_t ring[kStreamWaves][2 * kTileBytes];
-        int32_t entry[kStreamWaves][2][kWave];
-        int32_t column[kStreamWaves][2][kWave];
-        float top_of[kStreamWaves][kAttnTile], sum_of[kStreamWaves][kAttnTile];
+        __align__(16) uint8_t ring[WAVES][2 * kTileBytes];
+        int32_t entry[WAVES][2][kWave];
+        int32_t column[WAVES][2][kWave];
+        float top_of[WAVES][kAttnTile], sum_of[WAVES][kAttnTile];
     };
 
     // where f32 output chunk c (4 elements) of pair p lies in a wave's buffers,
@@ -159,8 +163,8 @@ struct Stream {
         if (SPARSE) {
             limit = a.ctx_lens ? visible(a, w.row0) : a.cap;
         } else {
-            least = keys;  // the smallest visible count: steps below it need no mask
-            for (int r = 0; r < w.rows; ++r) least = min(least, visible(a, w.row0 + r));
+            least = WINDOW ? span.least : keys;  // the smallest visible count: steps below it need no mask
+            for (int r = 0; r < w.rows && !WINDOW; ++r) least = min(least, visible(a, w.row0 + r));
         }
         constexpr int kQ = NARROW ? D / 32 : D / 16;
         i32x4 q[kQ];
@@ -179,9 +183,9 @@ struct Stream {
         const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
         // the wave's step j, and this lane's place in it (both half waves alike)
         const auto place = [&](int j) {
-            return token_step<WINDOW>(span, t0 + wave + j * kStreamWaves) * kStreamKeys + (lane & 31);
+            return token_step<WINDOW>(span, t0 + wave + j * WAVES) * kStreamKeys + (lane & 31);
         };
-        const auto have = [&](int j) { return t0 + wave + j * kStreamWaves < t1; };
+        const auto have = [&](int j) { return t0 + wave + j * WAVES < t1; };
 
         struct Token {
             uint32_t entry, in;  // table column, place in the block
@@ -278,7 +282,7 @@ struct Stream {
             copy_rows(a.vcache, cur, true);
             for (int j = 0; have(j); ++j) {
                 const bool more = have(j + 1);
-                const int s = token_step<WINDOW>(span, t0 + wave + j * kStreamWaves);
+                const int s = token_step<WINDOW>(span, t0 + wave + j * WAVES);
                 wait_all_but<kCopies>();
                 V z[kScores];
                 if constexpr (NARROW) score_narrow<DT, D>(mine, q, z, lane);
@@ -346,16 +350,16 @@ struct Stream {
             sh.sum_of[wave][lane] = l;
         }
         __syncthreads();
-        constexpr int kThreadsPer = kStreamThreads / kAttnTile, kPer = D / kThreadsPer;  // outputs per thread
+        constexpr int kThreadsPer = kThreads / kAttnTile, kPer = D / kThreadsPer;  // outputs per thread
         const int pm = t / kThreadsPer, d0 = (t % kThreadsPer) * kPer;
         float top = kNegInf, total = 0.0f, r[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) r[i] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < kStreamWaves; ++i) top = fmaxf(top, sh.top_of[i][pm]);
+        for (int i = 0; i < WAVES; ++i) top = fmaxf(top, sh.top_of[i][pm]);
         const float ref = top == kNegInf ? 0.0f : top;
 #pragma unroll
-        for (int i = 0; i < kStreamWaves; ++i) {
+        for (int i = 0; i < WAVES; ++i) {
             const float f = __builtin_amdgcn_exp2f(sh.top_of[i][pm] - ref);
             total += sh.sum_of[i][pm] * f;
             const float *src = reinterpret_cast<const float *>(sh.ring[i]);
@@ -408,7 +412,7 @@ struct Stream {
     static __device__ __attribute__((noinline)) void mend_pairs(const AttnArgs &a, TileWork w, int wave, KeySpan span,
                                                                 int t0, int t1, float sums, float *dest) {
         const int k0 = t0 * kStreamKeys, k1 = min(t1 * kStreamKeys, span.keys);
-        constexpr int kMine = kAttnTile / kStreamWaves;
+        constexpr int kMine = kAttnTile / WAVES;
         const int32_t *idx = SPARSE ? a.idx + (int64_t)w.row0 * a.k : nullptr;
         const int limit = !SPARSE || !a.ctx_lens ? a.cap : visible(a, w.row0), req = max(w.req, 0);
         FirstPlaces<D> f;
@@ -440,13 +444,13 @@ struct Stream {
 };
 
 // one workgroup per tile
-template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
+template <int DT, int D, bool SPARSE, bool NARROW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_stream_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE, NARROW, WINDOW> S;
+    typedef Stream<DT, D, SPARSE, NARROW, false> S;
     __shared__ typename S::Shared sh;
     TileWork w;
     if (!tile_work<SPARSE>(a, blockIdx.x, blockIdx.y, w)) return;
-    const KeySpan span = tile_keys<SPARSE, WINDOW>(a, w.row0, w.rows);
+    const KeySpan span = tile_keys<SPARSE>(a, w.row0, w.rows);
     S::run(a, sh, w, span, 0, span_steps<kStreamKeys>(span), nullptr);
 }
 
@@ -498,9 +502,9 @@ struct LiveSlots {
 
 // Equal parts of all tiles' keys, one per workgroup.  Tile hs * slots + slot; the
 // units of a slot are the same for every hs.
-template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
+template <int DT, int D, bool SPARSE, bool NARROW>
 __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a) {
-    typedef Stream<DT, D, SPARSE, NARROW, WINDOW> S;
+    typedef Stream<DT, D, SPARSE, NARROW, false> S;
     __shared__ typename S::Shared sh;
     __shared__ int32_t before[kMaxSlots + 1];  // units of the slots before
     __shared__ int32_t wave_sums[kStreamWaves];
@@ -508,21 +512,18 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
     const int hss = a.num_kv_heads * a.num_subs, slots = a.slots;
     __shared__ Requests requests;  // dense only, as is `live`
     __shared__ LiveSlots live;
-    __shared__ int32_t lows[WINDOW ? kMaxSlots + 1 : 1];  // each slot's smallest visible count
     if constexpr (SPARSE) {
         const int u = units_of((a.k * a.ratio + kStreamKeys - 1) / kStreamKeys);
         for (int i = t; i <= slots; i += kStreamThreads) before[i] = i * u;
         __syncthreads();
     } else {
-        slot_counts<kStreamThreads, WINDOW>(a, requests, before, lows);
+        slot_counts<kStreamThreads, false>(a, requests, before, nullptr);
         constexpr int kPer = LiveSlots::kPer;
         int u[kPer];
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             const int slot = t * kPer + i, keys = slot < slots ? before[slot] : -1;
-            u[i] = 0;
-            if (keys >= 0)
-                u[i] = units_of(span_steps<kStreamKeys>(key_span<WINDOW, kStreamKeys>(a, keys, WINDOW ? lows[slot] : 0)));
+            u[i] = keys < 0 ? 0 : units_of((keys + kStreamKeys - 1) / kStreamKeys);
             const uint64_t with_rows = ballot(keys >= 0);
             if ((t & 63) == 0) live.words[kPer * (t >> 6) + i] = with_rows;
         }
@@ -575,7 +576,7 @@ __global__ __launch_bounds__(kStreamThreads, 2) void attn_cut_kernel(AttnArgs a)
             w.row0 = __builtin_amdgcn_readfirstlane(r.row0);
             w.rows = __builtin_amdgcn_readfirstlane(r.rows);
         }
-        const KeySpan span = tile_keys<SPARSE, WINDOW>(a, w.row0, w.rows);
+        const KeySpan span = tile_keys<SPARSE>(a, w.row0, w.rows);
         const int steps = span_steps<kStreamKeys>(span);
         const int t0 = __builtin_amdgcn_readfirstlane((int)(u - tile0) * kStreamWaves);
         const int t1 = __builtin_amdgcn_readfirstlane(min((int)(stop - tile0) * kStreamWaves, steps));
@@ -612,15 +613,15 @@ __global__ __launch_bounds__(kJoinThreads) void attn_join_kernel(AttnArgs a) {
         a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }
 
-template <int DT, int D, bool SPARSE, bool NARROW, bool WINDOW>
+template <int DT, int D, bool SPARSE, bool NARROW>
 hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     const unsigned heads = (unsigned)(a.num_kv_heads * a.num_subs);
     if (!a.part) {
-        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE, NARROW, WINDOW>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
+        hipLaunchKernelGGL((attn_stream_kernel<DT, D, SPARSE, NARROW>), dim3((unsigned)a.slots, heads), dim3(kStreamThreads),
                            0, s, a);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE, NARROW, WINDOW>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
+    hipLaunchKernelGGL((attn_cut_kernel<DT, D, SPARSE, NARROW>), dim3(kStreamGroups), dim3(kStreamThreads), 0, s, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL((attn_join_kernel<DT, D>),
@@ -628,13 +629,103 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// Windows: a tile's keys are bounded by the window, the first tokens and its rows, so the
+// host knows into how many parts it is worth cutting all tiles, and a workgroup finds its
+// part without looking at the other tiles' rows.  Part j of head part hs of tile `tile` is
+// number (tile * heads + hs) * parts + j.
+//
+// The tile with number `tile`, by a wave: false where there is none.  With less than a wave
+// of requests the tiles with rows are numbered without gaps (one load has all starts); with
+// more, as slots.  (Every other slot of a verify step is empty: its workgroups had
+// held CUs before others could start.)
+__device__ __forceinline__ bool window_tile(const AttnArgs &a, int tile, RowTile &t) {
+    const int n = a.num_reqs, lane = lane_id(), T = a.tile_rows;
+    if (n >= kWave) {
+        // slots without rows come at a fixed pace, and workgroups go to the 8 XCDs in turn:
+        // they are rotated among the 8 of a round, by another amount each round
+        const int round = tile / 8, slot = 8 * round + (tile + round + round / 8) % 8;
+        return slot < a.slots && find_tile(a, slot, t);
+    }
+    const int s = request_start(a, min(lane, n)), next = shfl_i(s, min(lane + 1, kWave - 1));
+    const int tiles = lane < n ? (max(next - s, 0) + T - 1) / T : 0, inc = wave_incl_sum(tiles);
+    const uint64_t b = ballot(inc > tile);
+    if (b == 0) return false;
+    const int req = __builtin_ctzll(b), row0 = readlane(s, req) + (tile - readlane(inc - tiles, req)) * T;
+    t = {req, row0, min(T, readlane(next, req) - row0)};
+    return true;
+}
+
+// the rows of a tile whose parts are joined (0: none)
+struct TileRows {
+    int row0, rows;
+};
+template <int D>
+__device__ __forceinline__ float *window_state(const AttnArgs &a, int64_t number) {
+    return a.part + number * (kAttnTile * (D + 2));
+}
+template <int D>
+__device__ __forceinline__ TileRows *window_rows(const AttnArgs &a) {
+    const int64_t tiles = ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
+    return reinterpret_cast<TileRows *>(window_state<D>(a, tiles * a.parts));
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kWave * kWindowWaves, 2) void window_stream_kernel(AttnArgs a) {
+    typedef Stream<DT, D, false, false, true, kWindowWaves> S;
+    __shared__ typename S::Shared sh;
+    const int heads = a.num_kv_heads * a.num_subs, id = blockIdx.x, at = id / a.parts, j = id - at * a.parts;
+    const int tile = at / heads, hs = at - tile * heads;
+    RowTile r;
+    const bool have = window_tile(a, tile, r);
+    if (a.parts > 1 && j == 0 && threadIdx.x == 0) window_rows<D>(a)[at] = {r.row0, have ? r.rows : 0};
+    if (!have) return;
+    TileWork w = {__builtin_amdgcn_readfirstlane(r.req), __builtin_amdgcn_readfirstlane(r.row0),
+                  __builtin_amdgcn_readfirstlane(r.rows), 0, 0, 0};
+    part_heads(a, hs, w);
+    const KeySpan span = window_keys(a, w.row0, w.rows);
+    const int steps = span_steps<kStreamKeys>(span);
+    const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * j / a.parts));
+    const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * (j + 1) / a.parts));
+    S::run(a, sh, w, span, t0, t1, a.parts > 1 ? window_state<D>(a, id) : nullptr);
+}
+
+template <int DT, int D>
+__global__ __launch_bounds__(kJoinThreads) void window_join_kernel(AttnArgs a) {
+    const int tile = blockIdx.x, heads = a.num_kv_heads * a.num_subs;
+    const TileRows r = window_rows<D>(a)[tile];
+    constexpr int kPairs = kJoinThreads / (D / 4);
+    const int m = blockIdx.y * kPairs + threadIdx.x / (D / 4);
+    TileWork w;
+    part_heads(a, tile % heads, w);
+    w.row0 = r.row0;
+    w.rows = r.rows;
+    const Pair pp = pair_of(a, w, m);
+    if (!pp.live) return;
+    join_parts<DT, D, kAttnTile>(
+        window_state<D>(a, (int64_t)tile * a.parts), kAttnTile * (D + 2), a.parts, m, 4 * (threadIdx.x % (D / 4)),
+        static_cast<typename Half<DT>::T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head,
+        a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
+}
+
+template <int DT, int D>
+hipError_t run_window(const AttnArgs &a, hipStream_t s) {
+    // whole rounds of 8 slots (see window_tile)
+    const int64_t tiles = ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
+    hipLaunchKernelGGL((window_stream_kernel<DT, D>), dim3((unsigned)(tiles * a.parts)), dim3(kWave * kWindowWaves), 0, s, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.parts == 1) return e;
+    hipLaunchKernelGGL((window_join_kernel<DT, D>), dim3((unsigned)tiles, kAttnTile * (D / 4) / kJoinThreads),
+                       dim3(kJoinThreads), 0, s, a);
+    return hipGetLastError();
+}
+
 enum class Keys { kAll, kSelected, kWindow };
 
 template <int DT, int D>
 hipError_t run_kind(const AttnArgs &a, Keys keys, hipStream_t s) {
-    if (keys == Keys::kAll) return run_stream<DT, D, false, false, false>(a, s);
-    if (keys == Keys::kWindow) return run_stream<DT, D, false, false, true>(a, s);
-    return a.sub_heads <= 16 ? run_stream<DT, D, true, true, false>(a, s) : run_stream<DT, D, true, false, false>(a, s);
+    if (keys == Keys::kAll) return run_stream<DT, D, false, false>(a, s);
+    if (keys == Keys::kWindow) return run_window<DT, D>(a, s);
+    return a.sub_heads <= 16 ? run_stream<DT, D, true, true>(a, s) : run_stream<DT, D, true, false>(a, s);
 }
 
 template <int DT>
@@ -655,6 +746,10 @@ hipError_t launch_window_stream(const AttnArgs &a, hipStream_t s) { return run_t
 
 int64_t attn_workspace_bytes(int head_dim, int64_t tiles) {
     return (kStreamGroups + tiles) * (kAttnTile * (head_dim + 2) * 4) + (int64_t)sizeof(TileSpan) * tiles;
+}
+
+int64_t window_workspace_bytes(int head_dim, int64_t tiles, int parts) {
+    return tiles * parts * ((int64_t)kAttnTile * (head_dim + 2) * 4) + (int64_t)sizeof(TileRows) * tiles;
 }
 
 }  // namespace qsa

@@ -134,10 +134,12 @@ def test_window_pointers_and_workspace():
     assert m.window_attention_workspace_bytes(s, 100, 4) == 0       # a short window is not cut
     assert m.window_attention_workspace_bytes(s, 0, 4) == m.window_attention_workspace_bytes(s, 100, -1) == 0
     assert m.window_attention_workspace_bytes(attn_shape(num_rows=0), 4096, 4) == 0
-    # tables whose steps do not add up in 32 bits are not cut, however short the window
-    big = dict(num_rows=500, num_reqs=500, block_size=1024, num_heads=8, num_kv_heads=1)
-    assert m.window_attention_workspace_bytes(attn_shape(max_blocks=1 << 17, **big), 4096, 4) > 0
-    assert m.window_attention_workspace_bytes(attn_shape(max_blocks=1 << 19, **big), 4096, 4) == 0
+    # what the parts of the tiles take is bounded, whatever the batch
+    for rows, reqs, kv in ((1, 1, 1), (40, 40, 8), (500, 500, 1), (3000, 2, 4), (300, 200, 8), (20, 1000, 32)):
+        for window in (1, 300, 4096, 100000, 2 ** 31 - 1):
+            big = attn_shape(num_rows=rows, num_reqs=reqs, num_heads=8 * kv, num_kv_heads=kv, max_blocks=1 << 16)
+            assert 0 <= m.window_attention_workspace_bytes(big, window, 4) <= 70 << 20
+            assert check(A, A, A, A, A, A, window, 4, A, big, None, 0) == m.OK
 
 
 def test_host_tensors_are_refused():
