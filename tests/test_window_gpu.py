@@ -97,6 +97,12 @@ CASES = [
     ([0, 5, 900, 100] * 20, [0, 1, 0, 2] * 20, 60, 2, dict(group=8, hk=8)),
     ([300] * 40, [1, 20] * 20, 90, 10, dict(group=8, hk=4, dim=64)),
     ([500] * 20, [0] * 19 + [70], 77, 3, dict(group=8, hk=2)),
+    # as many requests as a wave has lanes, some more, and more than are counted
+    ([200, 90] * 32, [1, 3] * 32, 60, 2, dict(group=8, hk=1, dim=64)),
+    ([200] * 65, [4] * 65, 33, 0, dict(group=8, hk=1)),
+    ([130, 5, 70] * 50, [1, 0, 6] * 50, 40, 4, dict(group=16, hk=2, dim=64, pad=2)),
+    ([60] * 1024, [1, 0, 2, 0] * 256, 33, 1, dict(group=4, hk=1, dim=64)),
+    ([60] * 1030, [1] * 1030, 33, 1, dict(group=4, hk=1, dim=64, block=48)),
 ]
 
 
