@@ -158,6 +158,11 @@ struct TileShared {
     int most_of[kTileWaves], low_of[kTileWaves], any_bad;
 };
 
+// where 16-byte chunk c of a wave's pair p lies in its part of the buffers: chunks permuted
+// so that neither the pairs of a chunk nor the chunks of a pair meet in one bank
+template <int D>
+__device__ __forceinline__ int left_at(int p, int c) { return p * 2 * D + 16 * (c ^ (p & (D / 8 - 1))); }
+
 // steps [s0, min(s1, the tile's steps)) of tile w and kv head hk; dest: the place of
 // the state, or null to write the outputs.  WINDOW: the newest tokens and the first ones
 // only (see KeySpan).
@@ -214,7 +219,7 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
     // kLanesPerKey.  Behind the last visible key the copies take that key again.
     const auto key_row = [&](int i) { return kKeysPerCopy * (kCopies * wave + i) + lane / kLanesPerKey; };
     const int chunk = lane % kLanesPerKey;
-    bool met_bad = false;
+    bool met_bad = false, was_edge = false;  // was_edge: lane_at are a step's at an edge of the span
     // loaded a step ahead of the copies: this lane's table entries, or the wave's
     int32_t entry[kCopies], whole_entry = 0;
     // where the copies of a step come from
@@ -262,13 +267,20 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
                 // Tokens that no row sees give way to one that is: the group's last of the
                 // first tokens, or the oldest of the window, or the last of all.
                 const int f = first_token(s) + 8 * wave;
+                const bool edge = first != f || f + 8 > keys || (f < span.old && f + 8 > span.first);
+                if (edge) {
 #pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const int tok = first_token(s) + key_row(i);
-                    int use = min(tok, keys - 1);
-                    if (tok >= span.first && tok < span.old) use = f < span.first ? span.first - 1 : span.old;
-                    lane_at[i] = (uint32_t)(first == f ? use - first : 0) * slot_bytes;
+                    for (int i = 0; i < kCopies; ++i) {
+                        const int tok = f - 8 * wave + key_row(i);
+                        int use = min(tok, keys - 1);
+                        if (tok >= span.first && tok < span.old) use = f < span.first ? span.first - 1 : span.old;
+                        lane_at[i] = (uint32_t)(first == f ? use - first : 0) * slot_bytes;
+                    }
+                } else if (was_edge) {
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) lane_at[i] = (uint32_t)(key_row(i) - 8 * wave) * slot_bytes;
                 }
+                was_edge = edge;
             } else if (s * kTileKeys + 8 * wave + 8 > keys) {  // the last keys
 #pragma unroll
                 for (int i = 0; i < kCopies; ++i)
@@ -383,11 +395,14 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
 #pragma unroll
         for (int i = 0; i < 16; ++i) nan |= o[c][i] != o[c][i];
     const bool mend = ballot(nan && live && total == total) != 0;
+    // The outputs pass through LDS (every wave has left the buffers): written from the lanes
+    // that have them, 8 bytes in each of 64 rows at once, they took 13 us of a tile.
+    uint8_t *left = reinterpret_cast<uint8_t *>(&sh) + wave * kAttnTile * D * 2;
+    static_assert(kTileWaves * kAttnTile * D * 2 <= sizeof(sh.kring) + sizeof(sh.vring), "a wave's outputs");
     if (live && !anew) {
         const float inv = total == 0.0f ? 0.0f : 1.0f / total;
         typedef typename Half<DT>::T T;
         typedef T V4 __attribute__((ext_vector_type(4)));
-        T *out = static_cast<T *>(a.out) + row * a.o_row + head * a.o_head;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c)
 #pragma unroll
@@ -401,7 +416,7 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
                 V4 x;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = (T)(v[j] * inv);
-                *reinterpret_cast<V4 *>(out + at) = x;
+                *reinterpret_cast<V4 *>(left + left_at<D>(lane & 31, at / 8) + 2 * (at & 4)) = x;
             }
         if (lane < kAttnTile) {
             if (dest) {
@@ -410,6 +425,21 @@ __device__ __forceinline__ void run_steps(const AttnArgs &a, TileShared<D> &sh, 
             } else if (a.lse) {
                 a.lse[(int64_t)row * (a.num_kv_heads * a.group) + head] = (ref + __builtin_amdgcn_logf(total)) * kLn2;
             }
+        }
+    }
+    if (!dest && !anew) {
+        // whole rows of the outputs, by the wave that left them (its LDS accesses complete in order)
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+        constexpr int kLanes = D / 8, kPairs = kWave / kLanes;  // per pair; at once
+#pragma unroll
+        for (int i = 0; i < kAttnTile / kPairs; ++i) {
+            const int p = kPairs * i + lane / kLanes, pm = wave * kAttnTile + p, pr = pm / a.group;
+            if (pr >= w.rows) continue;
+            *reinterpret_cast<i32x4 *>(static_cast<uint16_t *>(a.out) + (w.row0 + pr) * a.o_row +
+                                       (hk * a.group + (pm - pr * a.group)) * a.o_head + 8 * (lane % kLanes)) =
+                *reinterpret_cast<const i32x4 *>(left + left_at<D>(p, lane % kLanes));
         }
     }
     if (anew || mend) {
