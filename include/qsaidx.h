@@ -489,7 +489,7 @@ typedef struct qsa_rope_shape {
  *
  * Device precondition: the slots written are distinct.  Outputs must not overlap inputs
  * but for q_out = q and k_out = k with their strides.  Compiled set: D in {64, 128};
- * Hq <= 8192, Hk <= 1024.  Range: R <= 2^27.  Alignment: q, k, v, their outputs and the
+ * Hq <= 8192, Hk <= 1024.  Range: R <= 2^21.  Alignment: q, k, v, their outputs and the
  * caches 16 bytes, strides multiples of 8 elements.
  */
 QSA_API qsa_status qsa_norm_rope(const void *q, const void *k, const void *v, const float *q_weight,
@@ -668,7 +668,7 @@ typedef struct qsa_verify_shape {
  *                   tokens do not change).  No initialisation; calls that share it must be
  *                   ordered.
  *
- * Compiled set: V <= 2^20.  Range: R and n <= 2^24, n * max_tokens <= 2^30.
+ * Compiled set: V <= 2^20.  Range: R <= 2^24, n <= 2^22, n * max_tokens <= 2^30.
  */
 QSA_API qsa_status qsa_verify_drafts(const float *probs, const float *draft_probs, const int32_t *tokens,
                                      const int32_t *q_starts, const float *uniforms, const float *sample_uniforms,

@@ -140,7 +140,8 @@ qsa_status check_rope(const void *q, const void *k, const void *v, const int32_t
     if (s->num_heads > 8192 || s->num_kv_heads > 1024)
         return fail(QSA_E_UNSUPPORTED, "num_heads = %d, num_kv_heads = %d (built: up to 8192 and 1024)", s->num_heads,
                     s->num_kv_heads);
-    if (s->num_rows > (1 << 27)) return fail(QSA_E_RANGE, "num_rows = %d > 2^27", s->num_rows);
+    // a workgroup of up to 1,024 lanes to a row, in a grid of less than 2^32 lanes
+    if (s->num_rows > (1 << 21)) return fail(QSA_E_RANGE, "num_rows = %d > 2^21", s->num_rows);
     if (negative({s->q_row_stride, s->q_head_stride, s->k_row_stride, s->k_head_stride, s->v_row_stride,
                   s->v_head_stride, s->q_out_row_stride, s->q_out_head_stride, s->k_out_row_stride,
                   s->k_out_head_stride, s->kv_block_stride, s->kv_slot_stride, s->kv_head_stride}))
@@ -194,7 +195,8 @@ qsa_status check_verify_sizes(const qsa_verify_shape *s) {
     if (s->vocab < 1 || s->max_tokens < 1) return fail(QSA_E_INVALID, "vocab and max_tokens must be >= 1");
     if (s->vocab > qsa::kVerifyMaxVocab)
         return fail(QSA_E_UNSUPPORTED, "vocab = %d (built: up to %d)", s->vocab, qsa::kVerifyMaxVocab);
-    if (s->num_rows > (1 << 24) || s->num_reqs > (1 << 24) || (int64_t)s->num_reqs * s->max_tokens > (1 << 30))
+    // a workgroup of 512 lanes to a request, in a grid of less than 2^32 lanes
+    if (s->num_rows > (1 << 24) || s->num_reqs > (1 << 22) || (int64_t)s->num_reqs * s->max_tokens > (1 << 30))
         return fail(QSA_E_RANGE, "num_rows, num_reqs or num_reqs * max_tokens too large");
     return ok();
 }

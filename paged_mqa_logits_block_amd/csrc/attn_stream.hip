@@ -694,7 +694,8 @@ template <int DT, int D>
 __global__ __launch_bounds__(kWave * kWindowWaves, 2) void window_stream_kernel(AttnArgs a) {
     typedef Stream<DT, D, false, false, true, kWindowWaves> S;
     __shared__ typename S::Shared sh;
-    const int heads = a.num_kv_heads * a.num_subs, id = blockIdx.x, at = id / a.parts, j = id - at * a.parts;
+    const int heads = a.num_kv_heads * a.num_subs, id = (int)(blockIdx.y * gridDim.x + blockIdx.x);
+    const int at = id / a.parts, j = id - at * a.parts;
     const int tile = at / heads, hs = at - tile * heads;
     RowTile r;
     const bool have = window_tile(a, tile, r);
@@ -732,7 +733,11 @@ template <int DT, int D>
 hipError_t run_window(const AttnArgs &a, hipStream_t s) {
     // whole rounds of 8 slots (see window_tile)
     const int64_t tiles = ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
-    hipLaunchKernelGGL((window_stream_kernel<DT, D>), dim3((unsigned)(tiles * a.parts)), dim3(kWave * kWindowWaves), 0, s, a);
+    // in rows of 2^16 workgroups: a dimension of a grid has less than 2^32 lanes (the places
+    // behind the last tile have none)
+    const int64_t groups = tiles * a.parts, row = 1 << 16;
+    const dim3 grid((unsigned)(groups < row ? groups : row), (unsigned)((groups + row - 1) / row));
+    hipLaunchKernelGGL((window_stream_kernel<DT, D>), grid, dim3(kWave * kWindowWaves), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
     hipLaunchKernelGGL((window_join_kernel<DT, D>), dim3((unsigned)tiles, kAttnTile * (D / 4) / kJoinThreads),

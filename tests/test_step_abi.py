@@ -41,7 +41,7 @@ NO_K = dict(k=None, v=None, s=None, kc=None, vc=None, num_kv_heads=0)
     (dict(rot_offset=2 ** 31 - 8), "E_INVALID"), (dict(rot_dim=2 ** 31 - 16), "E_INVALID"),
     (dict(rot_dim=40), "E_UNSUPPORTED"), (dict(rot_offset=4), "E_UNSUPPORTED"), (dict(head_dim=96), "E_UNSUPPORTED"),
     (dict(num_heads=8193), "E_UNSUPPORTED"), (dict(num_kv_heads=1025), "E_UNSUPPORTED"), (dict(block_size=1025), "E_UNSUPPORTED"),
-    (dict(dtype=m.FP8_E4M3FN), "E_DTYPE"), (dict(num_rows=(1 << 27) + 1), "E_RANGE"),
+    (dict(dtype=m.FP8_E4M3FN), "E_DTYPE"), (dict(num_rows=1 << 21), "OK"), (dict(num_rows=(1 << 21) + 1), "E_RANGE"),
     (dict(q_row_stride=(1 << 30) + 8), "E_RANGE"), (dict(num_blocks=1 << 49), "E_RANGE"),
     (dict(q=None), "E_INVALID"), (dict(qo=None), "E_INVALID"), (dict(k=None), "E_INVALID"), (dict(pos=None), "E_INVALID"),
     (dict(f=None), "E_INVALID"), (dict(s=None), "E_INVALID"), (dict(v=None), "E_INVALID"), (dict(vc=None), "E_INVALID"),
@@ -80,8 +80,8 @@ def verify_check(p=A, d=A, t=A, s=A, u=A, us=A, o=A, c=A, ws=None, nbytes=0, **k
     (dict(p=None), "E_INVALID"), (dict(t=None), "E_INVALID"), (dict(s=None), "E_INVALID"), (dict(u=None), "E_INVALID"),
     (dict(us=None), "E_INVALID"), (dict(o=None), "E_INVALID"), (dict(c=None), "E_INVALID"), (dict(p=A + 2), "E_ALIGN"),
     (dict(vocab=(1 << 20) + 1, prob_stride=1 << 21, draft_stride=1 << 21), "E_UNSUPPORTED"),
-    (dict(num_rows=(1 << 24) + 1), "E_RANGE"), (dict(num_reqs=(1 << 24) + 1), "E_RANGE"),
-    (dict(num_reqs=1 << 24, max_tokens=65), "E_RANGE"), (dict(prob_stride=(1 << 36) + 1), "E_RANGE"),
+    (dict(num_rows=(1 << 24) + 1), "E_RANGE"), (dict(num_reqs=1 << 22), "OK"), (dict(num_reqs=(1 << 22) + 1), "E_RANGE"),
+    (dict(num_reqs=1 << 22, max_tokens=257), "E_RANGE"), (dict(prob_stride=(1 << 36) + 1), "E_RANGE"),
 ])
 def test_verify_check(kw, status):
     assert verify_check(**kw) == getattr(m, status), m.last_error()

@@ -299,6 +299,29 @@ def test_verify_odd_inputs():
     assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(count.cpu().numpy(), want[1])
 
 
+def test_verify_largest_vocabulary():
+    """As many entries as are built, and tokens among the last ones; rows that start at
+    any element."""
+    V, R = 1 << 20, 3
+    rng = np.random.default_rng(9)
+    p, q = (rng.random((R, V)).astype(np.float32) for _ in range(2))
+    wide = rng.random((R, V + 1)).astype(np.float32)
+    wide[:, 1:] = p
+    tokens, u = np.array([0, V - 1, V - 2]), np.array([0.0, 0.0, 0.0], np.float32)
+    for kept in (2, 0):
+        if kept == 0:
+            u[:] = 1.0
+            q[0, V - 1] = p[0, V - 1] + 0.5
+        for us in (0.0, 0.37, np.float32(1 - 2.0 ** -24)):
+            want = ref.verify(p, q, tokens, [0, R], u, [us], 3)
+            assert want[1][0] == kept + 1
+            for ws in ("auto", None):
+                out, count = m.verify_drafts(dev(wide)[:, 1:], dev(tokens.astype(np.int32)), dev(np.array([0, R], np.int32)),
+                                             dev(u), dev(np.array([us], np.float32)), max_tokens=3, draft_probs=dev(q),
+                                             workspace=ws)
+                assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(count.cpu().numpy(), want[1])
+
+
 def test_verify_distribution():
     """A kept draft or the token in its place is distributed as the target: 49,152 requests
     of one draft, each token's share within 5 standard deviations."""
