@@ -387,6 +387,8 @@ class PreparedNormRope(_Prepared):
         _require((q is None) == (q_out is None), "q and q_out belong together")
         _require((v is None) == (vcache is None), "v and vcache belong together")
         _require(k is not None or (k_out is None and kcache is None and v is None), "outputs of keys without k")
+        for name, x in (("rot_offset", rot_offset), ("layout", layout), ("position_offset", position_offset)):
+            _require(-2 ** 31 <= int(x) < 2 ** 31, f"{name} = {x} does not fit 32 bits")
         strides = {}
         for name, t, like in (("q", q, q), ("k", k, k), ("v", v, k), ("q_out", q_out, q), ("k_out", k_out, k)):
             strides[name] = (0, 0)

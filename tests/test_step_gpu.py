@@ -188,6 +188,10 @@ def test_norm_rope_refusals():
                  (q, q.to(torch.float16), i, f), (q, q[:3], i, f)):
         with pytest.raises(m.QsaError):
             m.norm_rope(*args)
+    for kw in (dict(rot_offset=2 ** 32), dict(layout=2 ** 32), dict(position_offset=2 ** 32), dict(position_offset=2 ** 31)):
+        with pytest.raises(m.QsaError) as e:  # not taken for 0 or a negative number
+            m.norm_rope(q, q, i, f, **kw)
+        assert e.value.status == m.E_INVALID, kw
     out, _ = m.norm_rope(q[:0], q[:0], i[:0], f)  # no rows
     assert out.shape == (0, 8, 64)
 
