@@ -485,7 +485,8 @@ typedef struct qsa_rope_shape {
  *
  * Norms, angles' reduction and products are 32-bit or more with one rounding at the end;
  * the angle itself is a 64-bit product.  A head's sum of squares has to stay below 2^127 (heads
- * of larger values come out 0 or NaN).  An infinity or a NaN spoils its own head only.
+ * of larger values come out 0 or NaN), and a head of zeros is NaN with eps = 0.  An infinity
+ * or a NaN spoils its own head only.
  *
  * Device precondition: the slots written are distinct.  Outputs must not overlap inputs
  * but for q_out = q and k_out = k with their strides.  Compiled set: D in {64, 128};
@@ -656,7 +657,8 @@ typedef struct qsa_verify_shape {
  * A draft outside [0, V) is not kept.
  *
  *   probs, draft_probs [R][V] f32 (draft_probs or NULL; a request's last row of it is not
- *                   read).  Rows that do not decide anything are not read.
+ *                   read).  Of rows that decide nothing at most the entries of their drafts
+ *                   are read.
  *   tokens          [R] int32.
  *   uniforms        [R] f32 in [0, 1), one per draft (a request's last is not used).
  *   sample_uniforms [n] f32 in [0, 1).
@@ -665,9 +667,11 @@ typedef struct qsa_verify_shape {
  *                   a request without rows.
  *   workspace       qsa_verify_drafts_workspace_bytes(shape) bytes (0: none is used), 16-byte
  *                   aligned, or NULL: then few requests are not spread over the chip (the
- *                   tokens do not change).  No initialisation; calls that share it must be
- *                   ordered.
+ *                   tokens do not change, unless a cumulative weight and the number it has
+ *                   to pass are alike to 2^-40 without being equal sums of exact terms).  No
+ *                   initialisation; calls that share it must be ordered.
  *
+ * Device precondition: the outputs overlap neither the inputs nor each other.
  * Compiled set: V <= 2^20.  Range: R <= 2^24, n <= 2^22, n * max_tokens <= 2^30.
  */
 QSA_API qsa_status qsa_verify_drafts(const float *probs, const float *draft_probs, const int32_t *tokens,

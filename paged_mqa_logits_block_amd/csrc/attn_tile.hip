@@ -23,6 +23,11 @@
 // turns and scalar table entries, 552 with heads dealt to the XCDs.  The clock drops
 // from 2.3 to 1.9 GHz while the matrix cores work, so the card's power is part of the
 // bound.
+//
+// With a window of 4,096 and 64 first tokens the same rows take 131 to 142 us by card, 983 to
+// 1,065 TFLOP/s: 66 steps of 1.9 us a tile behind 5 for its rows, counts and first keys.  17
+// requests of 1 to 333 rows with windows of 777 (D = 64, blocks of 100 tokens) 27 us and 5 for
+// the join, latency: 5 until a workgroup has found its piece, then 5 steps of 1.4 us.
 
 #include "attn_device.h"
 

@@ -3,12 +3,15 @@
 // was rejected, else from the last p, by the inverse of its cumulative sums.
 //
 // A row of weights is added up in spans of kVerifySpan entries, one wave to a span, in
-// 64 bits (a sum of 100,000 probabilities in 32 would move the chosen token), always in
-// the same order; the token lies in the first span whose cumulative sum passes
+// 64 bits (of softmax rows of 50,021 normal numbers, sums in 32 bits from the first entry on
+// moved 3 tokens in a hundred, of 131,072 19), always in the same order; the token lies in the first span whose cumulative sum passes
 // u * total, which is read once more for its place inside.
 //
 // What bounds it is the bytes of one row of p, and of q where a draft was rejected, per
-// request: rows of drafts that were kept or not reached are not read.
+// request: rows of drafts that were kept or not reached are not read.  Measured, spans over
+// the chip and then the search: 257 requests of 100,003 entries (161 MB) 29 us at 5.6 TB/s,
+// and 4.8; 9 of 131,072 4.7 and 4.1, 1 of 50,021 4.4 and 3.6, where latency bounds both: the
+// starts, the drafts' entries, the row and its sum follow one another.
 #include "qsa_device.h"
 #include "step_internal.h"
 
@@ -122,8 +125,8 @@ __device__ __forceinline__ double dpp_add(double v) {
     const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(b >> 32), CTRL, ROWS, 0xF, false);
     return v + __builtin_bit_cast(double, (int64_t)((uint64_t)hi << 32 | lo));
 }
-// Inclusive sums over the wave, in the order of the six steps (LDS permutations in
-// their place took 2 us more per call).  All lanes active.
+// Inclusive sums over the wave, in the order of the six steps (LDS permutations and two
+// sums per entry in their place took 1 us more per call).  All lanes active.
 __device__ __forceinline__ double wave_incl_sum_d(double v) {
     v = dpp_add<kDppRowShr1, 0xF>(v);
     v = dpp_add<kDppRowShr2, 0xF>(v);
