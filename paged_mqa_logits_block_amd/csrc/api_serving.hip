@@ -264,6 +264,7 @@ struct AttnPlan {
     int64_t tiles;             // a cut launch of the streaming kernel: the most tiles with rows
     int64_t bytes;             // workspace of a cut launch, 0: not cut
     int parts;                 // with a window: parts of a tile
+    int64_t whole;             // with a window: the first places of tiles, which are not cut
 };
 
 AttnPlan plan_attn(const qsa_attn_shape *s, bool sparse, int64_t keys) {
@@ -382,12 +383,20 @@ qsa_status check_window(int32_t window, int32_t sinks) {
 // A windowed streaming tile works through as many keys as the window, the first tokens and
 // its rows come to, so that all tiles are cut into the same number of parts: with one to
 // a CU at most (a second one on some CUs holds up the others), and no more than make up
-// for the join, which takes about 0.12 us a part where 128 keys take 0.9.  us by parts, 4
+// for the join, which takes about 0.12 us a part where 128 keys take 0.9.  Of more tiles
+// than CUs those are cut that are left over from one or two whole rounds, where that saves
+// twice the 5 us of the second kernel (tiles numbered by slots have rows anywhere; after
+// more rounds, or where lengths differ, CUs end one by one).  us by parts, 4
 // kv heads of 8 heads at D = 128, windows of 4,096: 1 row 38.2 in 1, 17.1 in 4, 13.3 in 8, 13.1
 // in 14; 9 requests of 4 rows 41.4 in 1, 22.5 in 3, 20.8 in 4, 21.2 in 6, 25.2 in 8; 20 of 4
 // rows 42.7 in 1, 32.8 in 2, 34.0 in 3, 38.1 in 4; 33 of 1 row 49.3 in 1, 63.9 in 2, 50.0 in 3.
-// Windows of 16,384: 9 of 4 rows 179 in 1, 62 in 4, 57 in 6, 74 in 8.  (The tile kernel's
-// tiles are cut as without a window.)
+// Windows of 16,384: 9 of 4 rows 179 in 1, 62 in 4, 57 in 6, 74 in 8.  Rows of 20,000
+// tokens, all whole and with those left over cut: windows of 4,096, 65 rows 140 and 108, 96 157
+// and 147, 129 227 and 198, 160 248 and 240; of 2,048 65 rows 60 and 51; of 8,192 271 and 201.
+// Of 100 to 16,000 tokens, windows of 4,096: 65 129 and 101, 96 148 and 135, 129 177 and 184, 160
+// 238 and 218.  Not cut: 257 rows of 20,000 409 and 385, of 100 to 16,000 351 and 358; windows of
+// 1,024, 65 rows 31.1 and 29.4, 96 35.0 and 37.2, 257 of 100 to 16,000 81.4 and 85.6 (fp16).
+// (The tile kernel's tiles are cut as without a window.)
 AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     const int64_t cap = (int64_t)s->max_blocks * s->block_size;
     AttnPlan p = plan_attn(s, false, cap);
@@ -398,13 +407,18 @@ AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     const int64_t units = (keys + kUnit - 1) / kUnit, heads = (int64_t)s->num_kv_heads * p.num_subs;
     const int64_t reqs = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
     const int64_t full = (s->num_rows + p.tile_rows - 1) / p.tile_rows, tiles = (full > reqs ? full : reqs) * heads;
-    const int64_t places = (p.slots + 7) / 8 * 8 * heads;  // of tiles, also without rows
+    const int64_t whole = s->num_reqs <= qsa::kCountedReqs ? tiles / qsa::kStreamGroups * qsa::kStreamGroups : 0;
+    const int64_t places = (p.slots + 7) / 8 * 8 * heads - whole;  // of tiles, also without rows
     int n = 1;
-    while (n < qsa::kMaxParts && n < units && (n + 1) * tiles <= qsa::kStreamGroups &&
+    while (tiles > whole && n < qsa::kMaxParts && n < units && (n + 1) * (tiles - whole) <= qsa::kStreamGroups &&
            (int64_t)(n + 1) * (n + 1) <= 8 * units && (n + 1) * places <= qsa::kMaxTileParts)
         ++n;
+    if (whole > 0 && (whole > 2 * qsa::kStreamGroups || units * (n - 1) <= 12 * n)) n = 1;
     p.parts = n;
-    if (n > 1) p.bytes = qsa::window_workspace_bytes(s->head_dim, places, n);
+    if (n > 1) {
+        p.whole = whole;
+        p.bytes = qsa::window_workspace_bytes(s->head_dim, places, n);
+    }
     return p;
 }
 
@@ -458,6 +472,7 @@ void launch_shape(qsa::AttnArgs &a, const AttnPlan &p, void *workspace) {
     a.tiles = (int32_t)p.tiles;
     a.part = p.bytes > 0 ? static_cast<float *>(workspace) : nullptr;
     a.parts = a.part ? p.parts : 1;
+    a.whole = a.part ? (int32_t)p.whole : 0;
 }
 
 }  // namespace

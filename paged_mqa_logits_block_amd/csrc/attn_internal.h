@@ -21,6 +21,8 @@ constexpr int kMaxSlots = 1024;
 // The most parts of a windowed streaming tile, and of all tiles (also of slots without
 // rows): their states lie in the workspace.
 constexpr int kMaxParts = 64, kMaxTileParts = 4096;
+// The most requests whose windowed tiles are numbered without gaps.
+constexpr int kCountedReqs = 1024;
 
 // Stacked pairs of a workgroup of the tile kernel.
 constexpr int kTilePairs = 256;
@@ -66,6 +68,7 @@ struct AttnArgs {
     // window: a row sees its newest `window` tokens and the first `sinks`
     int32_t window, sinks;
     int32_t parts;              // streaming: of a tile's keys, one to a workgroup
+    int32_t whole;              // the first tiles, which are not cut
 };
 
 hipError_t launch_attn_stream(const AttnArgs &a, bool sparse, hipStream_t s);

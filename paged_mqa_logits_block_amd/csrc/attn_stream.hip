@@ -630,15 +630,15 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
 }
 
 // Windows: a tile's keys are bounded by the window, the first tokens and its rows, so the
-// host knows into how many parts it is worth cutting all tiles, and a workgroup finds its
-// part without looking at the other tiles' rows.  Part j of head part hs of tile `tile` is
-// number (tile * heads + hs) * parts + j.
+// host knows into how many parts it is worth cutting tiles, and a workgroup finds its part
+// without looking at the other tiles' rows.  Head part hs of tile `tile` has place
+// tile * heads + hs; the first `whole` places have a workgroup each, the others one for
+// each of their parts.
 //
 // The tile with number `tile`, by a wave: false where there is none.  Of up to 1,024
 // requests the tiles with rows are numbered without gaps, of more as slots.  (Slots without
 // rows hold CUs before others can start: 64 requests of a row with windows of 4,096, 80 slots,
 // 129 us, 98 without gaps.)
-constexpr int kCountedReqs = 16 * kWave;
 __device__ __forceinline__ int tiles_of(const AttnArgs &a, int s, int e) { return (max(e - s, 0) + a.tile_rows - 1) / a.tile_rows; }
 __device__ __forceinline__ bool window_tile(const AttnArgs &a, int tile, RowTile &t) {
     const int n = a.num_reqs, lane = lane_id(), T = a.tile_rows;
@@ -684,10 +684,13 @@ template <int D>
 __device__ __forceinline__ float *window_state(const AttnArgs &a, int64_t number) {
     return a.part + number * (kAttnTile * (D + 2));
 }
+// places of tiles, also without rows: whole rounds of 8 slots (see window_tile)
+__host__ __device__ __forceinline__ int64_t tile_places(const AttnArgs &a) {
+    return ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
+}
 template <int D>
 __device__ __forceinline__ TileRows *window_rows(const AttnArgs &a) {
-    const int64_t tiles = ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
-    return reinterpret_cast<TileRows *>(window_state<D>(a, tiles * a.parts));
+    return reinterpret_cast<TileRows *>(window_state<D>(a, (tile_places(a) - a.whole) * a.parts));
 }
 
 template <int DT, int D>
@@ -695,52 +698,54 @@ __global__ __launch_bounds__(kWave * kWindowWaves, 2) void window_stream_kernel(
     typedef Stream<DT, D, false, false, true, kWindowWaves> S;
     __shared__ typename S::Shared sh;
     const int heads = a.num_kv_heads * a.num_subs, id = (int)(blockIdx.y * gridDim.x + blockIdx.x);
-    const int at = id / a.parts, j = id - at * a.parts;
+    const bool cut = id >= a.whole && a.parts > 1;
+    const int parts = cut ? a.parts : 1, cut_at = cut ? (id - a.whole) / parts : 0;  // among those that are cut
+    const int j = cut ? id - a.whole - cut_at * parts : 0, at = cut ? a.whole + cut_at : id;
+    if (at >= tile_places(a)) return;  // behind the last one in the grid's last row
     const int tile = at / heads, hs = at - tile * heads;
     RowTile r;
     const bool have = window_tile(a, tile, r);
-    if (a.parts > 1 && j == 0 && threadIdx.x == 0) window_rows<D>(a)[at] = {r.row0, have ? r.rows : 0};
+    if (cut && j == 0 && threadIdx.x == 0) window_rows<D>(a)[cut_at] = {r.row0, have ? r.rows : 0};
     if (!have) return;
     TileWork w = {__builtin_amdgcn_readfirstlane(r.req), __builtin_amdgcn_readfirstlane(r.row0),
                   __builtin_amdgcn_readfirstlane(r.rows), 0, 0, 0};
     part_heads(a, hs, w);
     const KeySpan span = window_keys(a, w.row0, w.rows);
     const int steps = span_steps<kStreamKeys>(span);
-    const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * j / a.parts));
-    const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * (j + 1) / a.parts));
-    S::run(a, sh, w, span, t0, t1, a.parts > 1 ? window_state<D>(a, id) : nullptr);
+    const int t0 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * j / parts));
+    const int t1 = __builtin_amdgcn_readfirstlane((int)((int64_t)steps * (j + 1) / parts));
+    S::run(a, sh, w, span, t0, t1, cut ? window_state<D>(a, id - a.whole) : nullptr);
 }
 
 template <int DT, int D>
 __global__ __launch_bounds__(kJoinThreads) void window_join_kernel(AttnArgs a) {
-    const int tile = blockIdx.x, heads = a.num_kv_heads * a.num_subs;
-    const TileRows r = window_rows<D>(a)[tile];
+    const int cut_at = blockIdx.x, heads = a.num_kv_heads * a.num_subs;
+    const TileRows r = window_rows<D>(a)[cut_at];
     constexpr int kPairs = kJoinThreads / (D / 4);
     const int m = blockIdx.y * kPairs + threadIdx.x / (D / 4);
     TileWork w;
-    part_heads(a, tile % heads, w);
+    part_heads(a, (a.whole + cut_at) % heads, w);
     w.row0 = r.row0;
     w.rows = r.rows;
     const Pair pp = pair_of(a, w, m);
     if (!pp.live) return;
     join_parts<DT, D, kAttnTile>(
-        window_state<D>(a, (int64_t)tile * a.parts), kAttnTile * (D + 2), a.parts, m, 4 * (threadIdx.x % (D / 4)),
+        window_state<D>(a, (int64_t)cut_at * a.parts), kAttnTile * (D + 2), a.parts, m, 4 * (threadIdx.x % (D / 4)),
         static_cast<typename Half<DT>::T *>(a.out) + pp.row * a.o_row + pp.head * a.o_head,
         a.lse ? a.lse + (int64_t)pp.row * (a.num_kv_heads * a.group) + pp.head : nullptr);
 }
 
 template <int DT, int D>
 hipError_t run_window(const AttnArgs &a, hipStream_t s) {
-    // whole rounds of 8 slots (see window_tile)
-    const int64_t tiles = ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
+    const int64_t cut = tile_places(a) - a.whole;
     // in rows of 2^16 workgroups: a dimension of a grid has less than 2^32 lanes (the places
     // behind the last tile have none)
-    const int64_t groups = tiles * a.parts, row = 1 << 16;
+    const int64_t groups = a.whole + cut * a.parts, row = 1 << 16;
     const dim3 grid((unsigned)(groups < row ? groups : row), (unsigned)((groups + row - 1) / row));
     hipLaunchKernelGGL((window_stream_kernel<DT, D>), grid, dim3(kWave * kWindowWaves), 0, s, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.parts == 1) return e;
-    hipLaunchKernelGGL((window_join_kernel<DT, D>), dim3((unsigned)tiles, kAttnTile * (D / 4) / kJoinThreads),
+    hipLaunchKernelGGL((window_join_kernel<DT, D>), dim3((unsigned)cut, kAttnTile * (D / 4) / kJoinThreads),
                        dim3(kJoinThreads), 0, s, a);
     return hipGetLastError();
 }

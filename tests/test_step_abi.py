@@ -134,6 +134,11 @@ def test_window_pointers_and_workspace():
     assert m.window_attention_workspace_bytes(s, 100, 4) == 0       # a short window is not cut
     assert m.window_attention_workspace_bytes(s, 0, 4) == m.window_attention_workspace_bytes(s, 100, -1) == 0
     assert m.window_attention_workspace_bytes(attn_shape(num_rows=0), 4096, 4) == 0
+    # of more tiles than CUs those left over from whole rounds, where that pays
+    for rows, window, cut in ((64, 4096, False), (65, 4096, True), (65, 1024, False), (96, 4096, True), (97, 4096, False),
+                              (129, 4096, True), (193, 4096, False)):
+        rest = attn_shape(num_rows=rows, num_reqs=rows)
+        assert (m.window_attention_workspace_bytes(rest, window, 4) > 0) == cut
     # what the parts of the tiles take is bounded, whatever the batch
     for rows, reqs, kv in ((1, 1, 1), (40, 40, 8), (500, 500, 1), (3000, 2, 4), (300, 200, 8), (20, 1000, 32)):
         for window in (1, 300, 4096, 100000, 2 ** 31 - 1):

@@ -145,6 +145,57 @@ def test_window_any_counts(new, block):
             b.check(out, lse, lambda r: seen(int(lim[r]), window, sinks))
 
 
+LEFT_OVER = [
+    # past, new, window, sinks, kwargs: more tiles of long windows than CUs, of which the ones left
+    # over from whole rounds are cut: a few, many more than rows and requests tell (two tiles
+    # of a request), fewer (requests and rows of padding), half a round
+    ([2090] * 65, [1] * 65, 2000, 4, {}),
+    ([1000] * 40 + [2300] * 30, [1] * 40 + [5] * 30, 2000, 40, dict(dtype="fp16")),
+    ([1900] * 70, [1] * 60 + [0] * 10, 1800, 4, dict(pad=11, block=100)),
+    ([200] * 48 + [3250] * 48, [1] * 96, 3150, 33, dict(order="head")),
+]
+
+
+@pytest.mark.parametrize("i", range(len(LEFT_OVER)))
+def test_window_left_over_tiles(i):
+    past, new, window, sinks, kw = LEFT_OVER[i]
+    b = Batch(50 + i, past, new, hk=4, group=8, dim=64, **kw)
+    free_unseen(b, window, sinks)
+    shape = m.make_attn_shape(b.q.cuda(), b.kc, b.table)
+    assert 0 < m.window_attention_workspace_bytes(shape, window, sinks) <= 70 << 20  # they are cut
+    check_window(b, window, sinks, rows=sorted({*range(0, b.rows, 7), *range(max(b.rows - 20, 0), b.rows)}))
+    # values that are not finite, in tiles that are cut and in others
+    bad = {int(b.req[r]): int(b.ctx[r]) - 150 for r in (2, b.rows - 1)}
+    for req, tok in bad.items():
+        b.vc[int(b.table[req, tok // b.block]), tok % b.block] = float("nan")
+    out, _ = run_window(b, window, sinks)
+    for r in range(b.rows):
+        hit = bad.get(int(b.req[r])) in seen(int(b.ctx[r]), window, sinks)
+        assert bool(torch.isnan(out[r]).all()) == hit and bool(torch.isnan(out[r]).any()) == hit, r
+
+
+def test_window_more_tiles_than_a_row_of_the_grid():
+    """1,016 requests of one row with 70 heads over the same tokens: rows with equal queries are
+    equal, the first and the last ones right."""
+    n, hk, d, window, sinks, total = 1016, 70, 64, 300, 4, 500
+    g = torch.Generator().manual_seed(9)
+    k, v = torch.randn(total, hk, d, generator=g), torch.randn(total, hk, d, generator=g)
+    kc, vc, table = device_cache(k, v, "bf16")
+    q = torch.randn(8, hk, d, generator=g).to(torch.bfloat16).repeat(n // 8, 1, 1)
+    lse = torch.empty(n, hk, device="cuda")
+    args = (q.cuda(), kc, vc, table.repeat(n, 1), torch.full((n,), total, dtype=torch.int32, device="cuda"),
+            torch.arange(n + 1, dtype=torch.int32, device="cuda"))
+    out = m.window_attention(*args, window=window, sinks=sinks, lse=lse)
+    for x in (out, lse):
+        x = x.view(n // 8, 8, -1)
+        assert torch.equal(x, x[:1].expand_as(x))
+    toks = seen(total, window, sinks)
+    for r in (0, 3, n - 1):
+        for h in range(hk):
+            check_values(out[r:r + 1, h:h + 1].double().cpu().numpy(), lse[r:r + 1, h:h + 1].double().cpu().numpy(),
+                         q[r:r + 1, h:h + 1], k[toks, h:h + 1], v[toks, h:h + 1], [len(toks)], "bf16")
+
+
 def test_window_counts_past_the_table():
     """Counts past the table's end are cut to it, and the window is taken from there."""
     for new in ([1], [70]):
