@@ -326,6 +326,37 @@ def test_verify_largest_vocabulary():
                 assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(count.cpu().numpy(), want[1])
 
 
+@pytest.mark.parametrize("n", [768, 769, 65535, 65536])
+def test_verify_many_requests(n):
+    """Batches on either side of the numbers of requests where the launch changes, of 0 to 3
+    rows each."""
+    rng = np.random.default_rng(n)
+    starts = np.concatenate([[0], np.cumsum(rng.integers(0, 4, n))])
+    R, V = int(starts[-1]), 9
+    p, q = distributions(rng, R, V)
+    tokens, u, us = rng.integers(0, V, R), rng.random(R).astype(np.float32), rng.random(n).astype(np.float32)
+    want = ref.verify(p, q, tokens, starts, u, us, 3)
+    got = run_verify(p, q, tokens, starts, u, us, 3)
+    assert np.array_equal(got[0], want[0]) and np.array_equal(got[1], want[1])
+
+
+def test_verify_rows_far_apart():
+    """Rows more than 2^31 elements behind the first one."""
+    rng = np.random.default_rng(3)
+    R, V, stride = 5, 5000, 600_000_001
+    p, q = distributions(rng, R, V)
+    far = torch.empty(2, (R - 1) * stride + V, device="cuda")
+    pt, qt = (x.as_strided((R, V), (stride, 1)) for x in far)
+    pt.copy_(dev(p))
+    qt.copy_(dev(q))
+    tokens, u, us = rng.integers(0, V, R), rng.random(R).astype(np.float32), rng.random(1).astype(np.float32)
+    for u in (u, np.zeros(R, np.float32), np.array([0, 0, 0, 1e9, 0], np.float32)):
+        want = ref.verify(p, q, tokens, [0, R], u, us, R)
+        out, count = m.verify_drafts(pt, dev(tokens.astype(np.int32)), dev(np.array([0, R], np.int32)), dev(u), dev(us),
+                                     max_tokens=R, draft_probs=qt)
+        assert np.array_equal(out.cpu().numpy(), want[0]) and np.array_equal(count.cpu().numpy(), want[1])
+
+
 def test_verify_distribution():
     """A kept draft or the token in its place is distributed as the target: 49,152 requests
     of one draft, each token's share within 5 standard deviations."""
