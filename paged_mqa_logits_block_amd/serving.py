@@ -510,6 +510,14 @@ def _scratch(workspace, nbytes: int, device):
     return workspace
 
 
+def _window_sizes(window, sinks):
+    """Both as integers that the call takes unchanged (ctypes drops higher bits)."""
+    window, sinks = int(window), int(sinks)
+    for name, x in (("window", window), ("sinks", sinks)):
+        _require(-2 ** 31 <= x < 2 ** 31, f"{name} = {x} does not fit 32 bits")
+    return window, sinks
+
+
 def _nbytes(t) -> int:
     return 0 if t is None else int(t.numel() * t.element_size())
 
@@ -555,8 +563,7 @@ class PreparedWindowAttention(_Prepared):
         _attn_checks(q, kcache, vcache, block_table, out, lse)
         _check_rows_i32("ctx_lens", ctx_lens, int(q.shape[0]))
         _rows("q_starts", q_starts, int(block_table.shape[0]) + 1, torch.int32)
-        window, sinks = int(window), int(sinks)
-        _require(1 <= window < 2 ** 31 and 0 <= sinks < 2 ** 31, "window must be >= 1 and sinks >= 0, both below 2^31")
+        window, sinks = _window_sizes(window, sinks)
         self.shape = make_attn_shape(q, kcache, block_table, out=out, scale=scale)
         shape = ctypes.byref(self.shape)
         args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(ctx_lens), _ptr(q_starts), window, sinks,
@@ -660,7 +667,7 @@ def paged_attention_workspace_bytes(shape: AttnShape) -> int:
 
 def window_attention_workspace_bytes(shape: AttnShape, window: int, sinks: int = 0) -> int:
     """``qsa_window_attention_workspace_bytes`` (see ``make_attn_shape``)."""
-    return int(lib.qsa_window_attention_workspace_bytes(ctypes.byref(shape), int(window), int(sinks)))
+    return int(lib.qsa_window_attention_workspace_bytes(ctypes.byref(shape), *_window_sizes(window, sinks)))
 
 
 def sparse_attention_workspace_bytes(shape: AttnShape, k: int, ratio: int = 1) -> int:
