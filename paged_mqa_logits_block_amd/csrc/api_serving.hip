@@ -261,7 +261,8 @@ struct AttnPlan {
     int sub_heads, num_subs;   // streaming: heads per workgroup, workgroups per kv head
     int tile_rows;             // query rows per tile
     int64_t slots;             // row tiles
-    int64_t tiles;             // a cut launch of the streaming kernel: the most tiles with rows
+    int64_t tiles;             // a cut launch of the streaming kernel: the most tiles with rows;
+                               // streaming with a window: the places of tiles
     int64_t bytes;             // workspace of a cut launch, 0: not cut
     int parts;                 // with a window: parts of a tile
     int64_t whole;             // with a window: the first places of tiles, which are not cut
@@ -407,8 +408,12 @@ AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     const int64_t units = (keys + kUnit - 1) / kUnit, heads = (int64_t)s->num_kv_heads * p.num_subs;
     const int64_t reqs = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
     const int64_t full = (s->num_rows + p.tile_rows - 1) / p.tile_rows, tiles = (full > reqs ? full : reqs) * heads;
-    const int64_t whole = s->num_reqs <= qsa::kCountedReqs ? tiles / qsa::kStreamGroups * qsa::kStreamGroups : 0;
-    const int64_t places = (p.slots + 7) / 8 * 8 * heads - whole;  // of tiles, also without rows
+    // Tiles that are counted have rows: of k requests' R rows at most (R - k) / T + k, whatever the
+    // table's size.  Of more requests every slot has a place, in whole rounds of 8 (window_tile).
+    const bool counted = s->num_reqs <= qsa::kCountedReqs;
+    p.tiles = (counted ? (s->num_rows - reqs) / p.tile_rows + reqs : (p.slots + 7) / 8 * 8) * heads;
+    const int64_t whole = counted ? tiles / qsa::kStreamGroups * qsa::kStreamGroups : 0;
+    const int64_t places = p.tiles - whole;  // of tiles that may be cut
     int n = 1;
     while (tiles > whole && n < qsa::kMaxParts && n < units && (n + 1) * (tiles - whole) <= qsa::kStreamGroups &&
            (int64_t)(n + 1) * (n + 1) <= 8 * units && (n + 1) * places <= qsa::kMaxTileParts)

@@ -19,8 +19,8 @@ constexpr int kWindowWaves = 4;
 // Workgroups that a cut launch aims at (one per CU), and the most row tiles of one.
 constexpr int kStreamGroups = 256;
 constexpr int kMaxSlots = 1024;
-// The most parts of a windowed streaming tile, and of all tiles (also of slots without
-// rows): their states lie in the workspace.
+// The most parts of a windowed streaming tile, and of all places of tiles: their states
+// lie in the workspace.
 constexpr int kMaxParts = 64, kMaxTileParts = 4096;
 // The most requests whose windowed tiles are numbered without gaps.
 constexpr int kCountedReqs = 1024;
@@ -62,7 +62,8 @@ struct AttnArgs {
     int32_t div_shift;
     // launch shape
     int32_t slots;              // row tiles of the grid
-    int32_t tiles;              // the most tiles with rows, of all head parts (a cut launch)
+    int32_t tiles;              // the most tiles with rows, of all head parts (a cut launch);
+                                // streaming with a window: the places of tiles
     int32_t sub_heads;          // query heads per workgroup of one kv head
     int32_t num_subs;           // workgroups per kv head
     int32_t tile_rows;          // query rows per tile

@@ -633,7 +633,10 @@ hipError_t run_stream(const AttnArgs &a, hipStream_t s) {
 // host knows into how many parts it is worth cutting tiles, and a workgroup finds its part
 // without looking at the other tiles' rows.  Head part hs of tile `tile` has place
 // tile * heads + hs; the first `whole` places have a workgroup each, the others one for
-// each of their parts.
+// each of their parts.  There are a.tiles places: those of tiles without rows hold CUs, take a
+// state in the workspace and count against the most parts.  (With one for each of 128 requests of
+// which 4 have a row, 23.1 us for 8 kv heads and windows of 4,096 where 4 requests take 19.7; of
+// 256, too many to be cut, 41.6.)
 //
 // The tile with number `tile`, by a wave: false where there is none.  Of up to 1,024
 // requests the tiles with rows are numbered without gaps, of more as slots.  (Slots without
@@ -684,13 +687,9 @@ template <int D>
 __device__ __forceinline__ float *window_state(const AttnArgs &a, int64_t number) {
     return a.part + number * (kAttnTile * (D + 2));
 }
-// places of tiles, also without rows: whole rounds of 8 slots (see window_tile)
-__host__ __device__ __forceinline__ int64_t tile_places(const AttnArgs &a) {
-    return ((int64_t)a.slots + 7) / 8 * 8 * a.num_kv_heads * a.num_subs;
-}
 template <int D>
 __device__ __forceinline__ TileRows *window_rows(const AttnArgs &a) {
-    return reinterpret_cast<TileRows *>(window_state<D>(a, (tile_places(a) - a.whole) * a.parts));
+    return reinterpret_cast<TileRows *>(window_state<D>(a, (int64_t)(a.tiles - a.whole) * a.parts));
 }
 
 template <int DT, int D>
@@ -701,7 +700,7 @@ __global__ __launch_bounds__(kWave * kWindowWaves, 2) void window_stream_kernel(
     const bool cut = id >= a.whole && a.parts > 1;
     const int parts = cut ? a.parts : 1, cut_at = cut ? (id - a.whole) / parts : 0;  // among those that are cut
     const int j = cut ? id - a.whole - cut_at * parts : 0, at = cut ? a.whole + cut_at : id;
-    if (at >= tile_places(a)) return;  // behind the last one in the grid's last row
+    if (at >= a.tiles) return;  // behind the last one in the grid's last row
     const int tile = at / heads, hs = at - tile * heads;
     RowTile r;
     const bool have = window_tile(a, tile, r);
@@ -737,7 +736,7 @@ __global__ __launch_bounds__(kJoinThreads) void window_join_kernel(AttnArgs a) {
 
 template <int DT, int D>
 hipError_t run_window(const AttnArgs &a, hipStream_t s) {
-    const int64_t cut = tile_places(a) - a.whole;
+    const int64_t cut = a.tiles - a.whole;
     // in rows of 2^16 workgroups: a dimension of a grid has less than 2^32 lanes (the places
     // behind the last tile have none)
     const int64_t groups = a.whole + cut * a.parts, row = 1 << 16;
