@@ -356,7 +356,8 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, *, scaling: str = "non
 
         low = max(math.floor(pair(beta_fast)), 0)
         high = min(math.ceil(pair(beta_slow)), rot_dim - 1)
-        ramp = ((i / 2 - low) / max(high - low, 0.001)).clamp(0.0, 1.0)
+        # (below 0: not even the first pair turns so often)
+        ramp = ((i / 2 - low) / max(high - low, 0.001)).clamp(0.0, 1.0) if pair(beta_slow) >= 0 else torch.ones_like(i)
         freq = freq / factor * ramp + freq * (1.0 - ramp)
         scale = 0.1 * math.log(factor) + 1.0
     return freq.to(device), scale
