@@ -49,3 +49,18 @@ def test_few_rows_in_a_large_table(i):
     out, lse = run_window(b, window, sinks)
     want, want_lse = run_window(alone, window, sinks)
     assert torch.equal(b.q, alone.q) and torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("live", [range(6), range(1024, 1030), (0, 7, 8, 515, 1023, 1029)], ids=["first", "last", "spread"])
+@pytest.mark.parametrize("new", [1, 6])
+def test_few_rows_among_more_requests_than_are_counted(live, new):
+    """Above 1,024 requests tiles are numbered as slots, most of them without rows, in rounds of 8 that
+    are rotated; they are cut, and parts without rows are not joined."""
+    n, window, sinks = 1030, 3000, 70
+    past, a = [0] * n, [0] * n
+    for j, r in enumerate(live):
+        past[r], a[r] = (3700, 0, 3100, 40, 3700, 2999)[j], new
+    b = Batch(330 + new, past, a, hk=1, group=8, dim=64, pad=3)
+    free_unseen(b, window, sinks)
+    assert m.window_attention_workspace_bytes(m.make_attn_shape(b.q.cuda(), b.kc, b.table), window, sinks) > 0
+    check_window(b, window, sinks)
