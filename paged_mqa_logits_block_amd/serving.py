@@ -109,6 +109,12 @@ def _rows(name, t, n, dtype):
              f"{name} must be contiguous {dtype} [{n}]")
 
 
+def _int32(name, x) -> int:
+    """x as an integer that the call takes unchanged (ctypes drops higher bits)."""
+    _require(-2 ** 31 <= int(x) < 2 ** 31, f"{name} = {x} does not fit 32 bits")
+    return int(x)
+
+
 def _half_code(name, t) -> int:
     import torch
     if t.dtype == torch.bfloat16:
@@ -190,8 +196,8 @@ class PreparedPlanBatch(_Prepared):
             t = getattr(out, name)
             if t is not None or name in ("q_starts", "row_to_req", "ctx_lens", "slots"):
                 _rows(name, t, size, dtype)
-        shape = PlanShape(num_reqs=n, max_blocks=int(block_table.shape[1]), block_size=int(block_size),
-                          ratio=int(ratio), num_rows=rows, num_free=int(free_blocks.numel()),
+        shape = PlanShape(num_reqs=n, max_blocks=int(block_table.shape[1]), block_size=_int32("block_size", block_size),
+                          ratio=_int32("ratio", ratio), num_rows=rows, num_free=int(free_blocks.numel()),
                           num_blocks=int(num_blocks))
         ins = (_ptr(past_lens), _ptr(new_lens), _ptr(free_blocks), _ptr(block_table))
         outs = (_ptr(out.q_starts), _ptr(out.row_to_req), _ptr(out.ctx_lens), _ptr(out.slots))
@@ -299,7 +305,7 @@ class PreparedWriteKeys(_Prepared):
                      "kscale must be contiguous f32 [num_blocks, block_size]")
         _rows("slots", slots, R, torch.int64)
         shape = KeysShape(num_rows=R, head_dim=D, block_size=b, src_dtype=src,
-                          k_dtype=FP8_E4M3FN if fp8 else src, kv_layout=int(layout), num_blocks=nb,
+                          k_dtype=FP8_E4M3FN if fp8 else src, kv_layout=_int32("layout", layout), num_blocks=nb,
                           src_stride=int(keys.stride(0)) if R > 1 else D)
         args = (_ptr(keys), _ptr(slots), _ptr(kcache), _ptr(kscale), ctypes.byref(shape))
         _raise_on(lib.qsa_write_keys_check(*args))
@@ -389,7 +395,7 @@ class PreparedNormRope(_Prepared):
         _require((v is None) == (vcache is None), "v and vcache belong together")
         _require(k is not None or (k_out is None and kcache is None and v is None), "outputs of keys without k")
         for name, x in (("rot_offset", rot_offset), ("layout", layout), ("position_offset", position_offset)):
-            _require(-2 ** 31 <= int(x) < 2 ** 31, f"{name} = {x} does not fit 32 bits")
+            _int32(name, x)
         strides = {}
         for name, t, like in (("q", q, q), ("k", k, k), ("v", v, k), ("q_out", q_out, q), ("k_out", k_out, k)):
             strides[name] = (0, 0)
@@ -511,14 +517,6 @@ def _scratch(workspace, nbytes: int, device):
     return workspace
 
 
-def _window_sizes(window, sinks):
-    """Both as integers that the call takes unchanged (ctypes drops higher bits)."""
-    window, sinks = int(window), int(sinks)
-    for name, x in (("window", window), ("sinks", sinks)):
-        _require(-2 ** 31 <= x < 2 ** 31, f"{name} = {x} does not fit 32 bits")
-    return window, sinks
-
-
 def _nbytes(t) -> int:
     return 0 if t is None else int(t.numel() * t.element_size())
 
@@ -564,7 +562,7 @@ class PreparedWindowAttention(_Prepared):
         _attn_checks(q, kcache, vcache, block_table, out, lse)
         _check_rows_i32("ctx_lens", ctx_lens, int(q.shape[0]))
         _rows("q_starts", q_starts, int(block_table.shape[0]) + 1, torch.int32)
-        window, sinks = _window_sizes(window, sinks)
+        window, sinks = _int32("window", window), _int32("sinks", sinks)
         self.shape = make_attn_shape(q, kcache, block_table, out=out, scale=scale)
         shape = ctypes.byref(self.shape)
         args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(ctx_lens), _ptr(q_starts), window, sinks,
@@ -599,7 +597,7 @@ class PreparedSparseAttention(_Prepared):
             _check_rows_i32("token_lens", token_lens, R)
         _require(idx.dtype == torch.int32 and idx.dim() == 2 and idx.is_contiguous() and int(idx.shape[0]) == R,
                  "idx must be contiguous int32 [R, k]")
-        k, ratio = int(idx.shape[1]), int(ratio)
+        k, ratio = int(idx.shape[1]), _int32("ratio", ratio)
         self.shape = make_attn_shape(q, kcache, block_table, out=out, scale=scale)
         shape = ctypes.byref(self.shape)
         args = (_ptr(q), _ptr(kcache), _ptr(vcache), _ptr(block_table), _ptr(row_to_req), _ptr(idx), k, ratio)
@@ -668,12 +666,13 @@ def paged_attention_workspace_bytes(shape: AttnShape) -> int:
 
 def window_attention_workspace_bytes(shape: AttnShape, window: int, sinks: int = 0) -> int:
     """``qsa_window_attention_workspace_bytes`` (see ``make_attn_shape``)."""
-    return int(lib.qsa_window_attention_workspace_bytes(ctypes.byref(shape), *_window_sizes(window, sinks)))
+    return int(lib.qsa_window_attention_workspace_bytes(ctypes.byref(shape), _int32("window", window),
+                                                        _int32("sinks", sinks)))
 
 
 def sparse_attention_workspace_bytes(shape: AttnShape, k: int, ratio: int = 1) -> int:
     """``qsa_sparse_attention_workspace_bytes`` (see ``make_attn_shape``)."""
-    return int(lib.qsa_sparse_attention_workspace_bytes(ctypes.byref(shape), int(k), int(ratio)))
+    return int(lib.qsa_sparse_attention_workspace_bytes(ctypes.byref(shape), _int32("k", k), _int32("ratio", ratio)))
 
 
 # ---------------------------------------------------------------------------
