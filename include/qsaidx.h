@@ -651,8 +651,8 @@ typedef struct qsa_verify_shape {
  *
  * with q = draft_probs[s + j], or the certainty of x without draft_probs.  The token is
  * the lowest index whose cumulative weight passes sample_uniforms[i] times the weights'
- * sum (the last index with weight where none does): sums and products in 64 bits, a row's
- * own sum need not be 1.  Entries that are not positive numbers have no weight.  Where
+ * sum (the last index with weight where none does): sums and products in 64 bits, a
+ * difference p - q rounded once to 32; a row's own sum need not be 1.  Entries that are not positive numbers have no weight.  Where
  * p is nowhere above q the token is taken from p, and it is -1 where p has no weight either.
  * A draft outside [0, V) is not kept.
  *

@@ -4,8 +4,10 @@
 //
 // A row of weights is added up in spans of kVerifySpan entries, one wave to a span, in
 // 64 bits (of softmax rows of 50,021 normal numbers, sums in 32 bits from the first entry on
-// moved 3 tokens in a hundred, of 131,072 19), always in the same order; the token lies in the first span whose cumulative sum passes
-// u * total, which is read once more for its place inside.
+// moved 3 tokens in a hundred, of 131,072 19), always in the same order; the token lies in
+// the first span whose cumulative sum passes u * total, which is read once more for its
+// place inside.  A weight p - q is rounded once to 32 bits, as p and q are: it is exact where they
+// are within a factor of 2, else off by at most 2^-24 of itself.
 //
 // What bounds it is the bytes of one row of p, and of q where a draft was rejected, per
 // request: rows of drafts that were kept or not reached are not read.  Measured, spans over
@@ -77,44 +79,33 @@ __device__ __forceinline__ Weights weights_of(const VerifyArgs &a, const Verdict
 // of NaN and of everything with a sign are not below those of infinity.
 __device__ __forceinline__ float weight(float x) { return __float_as_uint(x) < 0x7F800000u ? x : 0.0f; }
 
-template <int N>
-struct Entries;
-template <>
-struct Entries<4> {
-    typedef float V __attribute__((ext_vector_type(4), aligned(4)));  // rows start at any element
-};
-template <>
-struct Entries<2> {
-    typedef float V __attribute__((ext_vector_type(2), aligned(4)));
-};
+typedef float Entries __attribute__((ext_vector_type(4), aligned(4)));  // rows start at any element
 
-// the weights of N entries from `at` on, 0 behind the vocabulary
-template <int N>
-__device__ __forceinline__ void load_weights(const Weights &w, int vocab, int at, float (&x)[N]) {
-    typedef typename Entries<N>::V V;
-    if (at + N <= vocab) {
-        const V p = *reinterpret_cast<const V *>(w.p + at);
+// the weights of 4 entries from `at` on, 0 behind the vocabulary
+__device__ __forceinline__ void load_weights(const Weights &w, int vocab, int at, float (&x)[4]) {
+    if (at + 4 <= vocab) {
+        const Entries p = *reinterpret_cast<const Entries *>(w.p + at);
         if (w.q) {
-            const V q = *reinterpret_cast<const V *>(w.q + at);
+            const Entries q = *reinterpret_cast<const Entries *>(w.q + at);
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = p[i] - q[i];
+            for (int i = 0; i < 4; ++i) x[i] = p[i] - q[i];
         } else {
 #pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = p[i];
+            for (int i = 0; i < 4; ++i) x[i] = p[i];
         }
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
+        for (int i = 0; i < 4; ++i) {
             x[i] = 0.0f;
             if (at + i < vocab) x[i] = w.p[at + i] - (w.q ? w.q[at + i] : 0.0f);
         }
     }
     if (w.without >= 0) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = at + i == w.without ? 0.0f : x[i];
+        for (int i = 0; i < 4; ++i) x[i] = at + i == w.without ? 0.0f : x[i];
     }
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = weight(x[i]);
+    for (int i = 0; i < 4; ++i) x[i] = weight(x[i]);
 }
 
 // v plus v of the lane that the DPP pattern takes from (0 where there is none)
@@ -150,7 +141,7 @@ __device__ __forceinline__ double span_sum(const Weights &w, int vocab, int span
     double sum[2] = {0.0, 0.0};
     float x[kSteps][4];
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) load_weights<4>(w, vocab, span * kVerifySpan + 4 * (kWave * i + lane_id()), x[i]);
+    for (int i = 0; i < kSteps; ++i) load_weights(w, vocab, span * kVerifySpan + 4 * (kWave * i + lane_id()), x[i]);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i)
 #pragma unroll
@@ -231,14 +222,14 @@ __device__ __forceinline__ int find(const VerifyArgs &a, Search<THREADS> &sh, co
             if (i < span % kPer) at += s[i];
         sh.base = at;
     }
-    constexpr int kLoad = kEach < 4 ? kEach : 4;
-    float x[kEach / kLoad][kLoad];
+    static_assert(kEach % 4 == 0, "whole loads of 4 entries");
+    float x[kEach / 4][4];
     double in = 0.0;
 #pragma unroll
-    for (int i = 0; i < kEach / kLoad; ++i) {
-        load_weights<kLoad>(w, a.vocab, span * kVerifySpan + kEach * t + kLoad * i, x[i]);
+    for (int i = 0; i < kEach / 4; ++i) {
+        load_weights(w, a.vocab, span * kVerifySpan + kEach * t + 4 * i, x[i]);
 #pragma unroll
-        for (int j = 0; j < kLoad; ++j) in += (double)x[i][j];
+        for (int j = 0; j < 4; ++j) in += (double)x[i][j];
     }
     at = block_before<THREADS>(sh.wave_sum[1], in, total);
     at += sh.base;
@@ -246,7 +237,7 @@ __device__ __forceinline__ int find(const VerifyArgs &a, Search<THREADS> &sh, co
     last = -1;
 #pragma unroll
     for (int i = 0; i < kEach; ++i) {
-        const float v = x[i / kLoad][i % kLoad];
+        const float v = x[i / 4][i % 4];
         at += (double)v;
         if (v > 0.0f) {
             last = span * kVerifySpan + kEach * t + i;
