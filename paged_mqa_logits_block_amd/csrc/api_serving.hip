@@ -228,8 +228,15 @@ int32_t verify_spans(const qsa_verify_shape *s) { return (s->vocab + qsa::kVerif
 // 7.9 / 8.1, 8.1 / 8.3; of 40,000 9.1 / 8.2, 9.6 / 8.4; of 131,072 19.2 / 8.1, 19.8 / 8.3;
 // 257 requests of 16,000 7.1 / 9.9, 8.8 / 11.6; of 100,003 29.3 / 24.6, 38.7 / 36.8; 512 of
 // 16,000 9.9 / 11.8, 14.5 / 17.2; 1,024 of 2,000 10.3 / 9.2, 13.6 / 10.8; 4,096 of 2,000
-// 38 / 18, 45 / 26.  (Two workgroups to every CU are the exception: 512 of 131,072 57 / 73, 89 /
-// 107.)  The grid of a split launch has a row per request.
+// 38 / 18, 45 / 26.  Of 2 to 4 rows, a draft kept 7 times in 10, two sets of inputs in turn: 64
+// requests of 40,000 9.4 / 9.8, 14.2 / 10.8, of 131,072 32 / 13, 33 / 15; 256 16.0 / 14.1, 17.6 /
+// 16.8 and 45 / 28, 53 / 41; 512 21.2 / 20.9, 26.2 / 27.4 and 63 / 55, 78 / 79; 768 27.4 / 27.8,
+// 37 / 39 and 84 / 78, 110 / 112.  The split launch costs most with two or three workgroups to
+// every CU, more so the more alike the requests are: of 65,536 entries 512 requests of 4 to 8 rows
+// 30 / 30, 47 / 54, and with every first draft rejected 25 / 30, 50 / 58; there the whole one costs
+// most where few requests are kept: 26 / 21, 31 / 26 (320 of 2 rows, a third rejected).  The
+// lengths of drafts, which decide it, are on the device.  The grid of a split launch has a row per
+// request.
 bool verify_split(const qsa_verify_shape *s) {
     return s->num_reqs <= 65535 && (s->vocab > 32768 || s->num_reqs > 768);
 }
@@ -382,7 +389,8 @@ qsa_status check_window(int32_t window, int32_t sinks) {
 }
 
 // A windowed streaming tile works through as many keys as the window, the first tokens and
-// its rows come to, so that all tiles are cut into the same number of parts: with one to
+// its rows come to, so that all tiles are cut into the same number of parts (where the requests are
+// shorter than the window those with few keys have short parts; see the end): with one to
 // a CU at most (a second one on some CUs holds up the others), and no more than make up
 // for the join, which takes about 0.12 us a part where 128 keys take 0.9.  Of more tiles
 // than CUs those are cut that are left over from one or two whole rounds, where that saves
@@ -398,6 +406,13 @@ qsa_status check_window(int32_t window, int32_t sinks) {
 // 238 and 218.  Not cut: 257 rows of 20,000 409 and 385, of 100 to 16,000 351 and 358; windows of
 // 1,024, 65 rows 31.1 and 29.4, 96 35.0 and 37.2, 257 of 100 to 16,000 81.4 and 85.6 (fp16).
 // (The tile kernel's tiles are cut as without a window.)
+// Where the window is longer than the requests both calls compute the same.  us windowed / dense, 4
+// kv heads of 8 heads at D = 128, windows as long as the table: tables of 512 tokens, 1 request 11.2 /
+// 13.0, 33 of that length 10.3 / 21.2, 300 of 4 rows 66 / 122; of 4,096 12.8 / 13.6, 9 of 4 rows 21.5 /
+// 29.6, 257 of mixed lengths 238 / 205; of 16,384 17.8 / 20.9, 9 of 4 rows 57 / 61 and of mixed lengths 33 / 38,
+// 64 of mixed lengths 241 / 214; of 65,536 36.3 / 36.5, 20 of 4 rows of mixed lengths 350 / 305.  Of 139
+// batches 72 are faster windowed by a tenth or more and 15 slower; the worst are 33 requests of
+// mixed lengths, just too many tiles to be cut: 197 / 126 and 739 / 407.
 AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     const int64_t cap = (int64_t)s->max_blocks * s->block_size;
     AttnPlan p = plan_attn(s, false, cap);
@@ -407,6 +422,8 @@ AttnPlan plan_window(const qsa_attn_shape *s, int32_t window, int32_t sinks) {
     constexpr int kUnit = qsa::kStreamKeys * qsa::kWindowWaves;
     const int64_t units = (keys + kUnit - 1) / kUnit, heads = (int64_t)s->num_kv_heads * p.num_subs;
     const int64_t reqs = s->num_reqs < s->num_rows ? s->num_reqs : s->num_rows;
+    // what the parts are chosen for: a row to a request where the table has room (9 requests of 4 rows
+    // 21.3 us in a table of 9, 23.4 in one of 18, 42.5, not cut, in one of 36)
     const int64_t full = (s->num_rows + p.tile_rows - 1) / p.tile_rows, tiles = (full > reqs ? full : reqs) * heads;
     // Tiles that are counted have rows: of k requests' R rows at most (R - k) / T + k, whatever the
     // table's size.  Of more requests every slot has a place, in whole rounds of 8 (window_tile).
