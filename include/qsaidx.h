@@ -485,8 +485,9 @@ typedef struct qsa_rope_shape {
  *
  * Norms, angles' reduction and products are 32-bit or more with one rounding at the end;
  * the angle itself is a 64-bit product.  A head's sum of squares has to stay below 2^127 (heads
- * of larger values come out 0 or NaN), and a head of zeros is NaN with eps = 0.  An infinity
- * or a NaN spoils its own head only.
+ * of larger values come out 0 or NaN); with eps below 2^-118 it has to be 2^-118 at least (smaller
+ * bf16 heads are off or NaN, as is a head of zeros with eps = 0).  An infinity or a NaN spoils its
+ * own head only.
  *
  * Device precondition: the slots written are distinct.  Outputs must not overlap inputs
  * but for q_out = q and k_out = k with their strides.  Compiled set: D in {64, 128};

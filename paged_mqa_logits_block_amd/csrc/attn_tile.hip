@@ -27,7 +27,10 @@
 // With a window of 4,096 and 64 first tokens the same rows take 131 to 142 us by card, 983 to
 // 1,065 TFLOP/s: 66 steps of 1.9 us a tile behind 5 for its rows, counts and first keys.  17
 // requests of 1 to 333 rows with windows of 777 (D = 64, blocks of 100 tokens) 27 us and 5 for
-// the join, latency: 5 until a workgroup has found its piece, then 5 steps of 1.4 us.
+// the join, latency: 5 until a workgroup has found its piece, about 5 for a tile's start, 5
+// steps of 1.4, and the state's write; some 9 us are not accounted for.  A NaN that all rows
+// see is searched for once per row of a wave: the rows above 160 -> 2,205 us, of 32 kv heads with
+// one query head each 168 -> 17,500.
 
 #include "attn_device.h"
 
